@@ -1,4 +1,4 @@
-"""ctypes binding of libw4a8.so (include/w4a8.h).
+"""ctypes binding of libw4a8.so (include/w4a8.h, include/w4a8_rows.h).
 
 Argument marshalling only: torch supplies device memory and the current
 stream; every step of the layer runs in the library's HIP kernels.  If the
@@ -36,7 +36,7 @@ PATH_PREFILL_N256 = 5      # w4a8_gemm_debug only: prefill with 256 x 256 tiles 
 
 GROUP = 128
 
-# Every symbol include/w4a8.h declares, with its ctypes signature.
+# Every symbol the headers declare, with its ctypes signature.
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 SIGNATURES = {
     "w4a8_abi_version": (ctypes.c_int, []),
@@ -78,6 +78,15 @@ SIGNATURES = {
     "w8a8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "w8a8_linear": (ctypes.c_int, [_vp, _i32, _vp, _sz, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
     "w4a8_linear_noalloc": (ctypes.c_int, [_vp, _i32, _vp, _sz, _i64, _i64, _i64, _i32, _vp, _vp]),
+    # include/w4a8_rows.h
+    "w4a8_moe_route": (ctypes.c_int, [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                      _i32, ctypes.c_float, _vp, _vp, _vp]),
+    "w4a8_moe_mlp_workspace_bytes": (_sz, [_i64, _i32, _i32, _i64, _i64]),
+    "w4a8_moe_mlp": (ctypes.c_int, [_vp, _i32, _vp, _sz, _vp, _sz, _vp, _vp, _i64, _i32, _i32, _i64,
+                                    _i64, _vp, _vp, _sz, _vp]),
+    "w4a8_lora_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "w4a8_lora_linear": (ctypes.c_int, [_vp, _i32, _vp, _sz, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                        _i32, _i32, _vp, _vp, _sz, _vp]),
     # include/w4a8_peaks.h
     "w4a8_peak_stream_read": (ctypes.c_int, [_vp, _sz, _vp, _i32, _vp]),
     "w4a8_peak_mfma_i8": (ctypes.c_int, [_i32, _vp, _vp, _i32, _vp]),
@@ -530,6 +539,165 @@ def w4a16_linear(x: torch.Tensor, w: PackedWeight, out=None, workspace=None,
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.w4a16_linear_path(_p(x), _p(w.buf), w.buf.numel(), M, w.N, w.K, w.group, path,
                                  _p(out), _p(workspace), wsb, _stream(x.device)))
+    return out
+
+
+# ------------------------------------ weights that depend on the row
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _act_dtype(x: torch.Tensor) -> int:
+    if x.dtype == torch.bfloat16:
+        return BF16
+    if x.dtype == torch.float32:
+        return F32
+    raise TypeError(x.dtype)
+
+
+def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+              n_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalize: bool = True,
+              scale: float = 1.0, ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None):
+    """logits bfloat16 or float32 [M][E] -> (ids int32 [M][k], weights float32
+    [M][k]): the k experts of each token by softmax or sigmoid score, with an
+    optional balance bias float32 [E] that takes part in the choice only and
+    an optional limit to the best topk_groups of n_groups groups (a group's
+    value: the sum of its group_top best).  An expert whose logit is minus
+    infinity is never chosen; where fewer than k remain, ids are -1."""
+    lib = load()
+    _need_cuda(logits, bias, ids, weights)
+    if score not in SCORES:
+        raise ValueError(f"unknown score function {score!r}")
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1]):
+        raise TypeError("bias must be float32 [E]")
+    dt = _act_dtype(logits)
+    M, E = logits.shape
+    ids = torch.empty((M, k), dtype=torch.int32, device=logits.device) if ids is None else ids
+    weights = torch.empty((M, k), dtype=torch.float32, device=logits.device) if weights is None \
+        else weights
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32 or \
+            tuple(ids.shape) != (M, k) or tuple(weights.shape) != (M, k):
+        raise TypeError("ids must be int32 and weights float32, both [M][k]")
+    _check(lib.w4a8_moe_route(_p(logits), dt, _p(bias), M, E, k, SCORES[score], n_groups,
+                              topk_groups, group_top, int(renormalize), scale, _p(ids), _p(weights),
+                              _stream(logits.device)))
+    return ids, weights
+
+
+@dataclass
+class ExpertWeights:
+    """The packed weights of n_experts experts of N channels each, stacked
+    along the channels of one packed weight."""
+    packed: PackedWeight
+    n_experts: int
+    N: int
+
+    @property
+    def K(self) -> int:
+        return self.packed.K
+
+
+def pack_experts(q: torch.Tensor, z: torch.Tensor | None, s: torch.Tensor, n_experts: int,
+                 group: int = GROUP, out: torch.Tensor | None = None) -> ExpertWeights:
+    """pack_weights of the experts' weights stacked along the channels: q
+    uint8 [n_experts * N][K], z and s [n_experts * N][K / group].  An up
+    weight has I gate channels, then I up channels per expert."""
+    if n_experts < 1 or q.shape[0] % n_experts:
+        raise ValueError(f"{q.shape[0]} channels are not those of {n_experts} experts")
+    return ExpertWeights(pack_weights(q, z, s, group=group, out=out), n_experts,
+                         q.shape[0] // n_experts)
+
+
+def moe_mlp_workspace_bytes(M: int, k: int, n_experts: int, intermediate: int, hidden: int) -> int:
+    return int(load().w4a8_moe_mlp_workspace_bytes(M, k, n_experts, intermediate, hidden))
+
+
+def moe_mlp(x: torch.Tensor, up: ExpertWeights, down: ExpertWeights, ids: torch.Tensor,
+            weights: torch.Tensor, out: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated MLP of each token's experts: bf16 y [M][hidden] = sum over
+    the slots of weights * down(silu(gate) * up), from bf16/f32 x [M][hidden],
+    ids int32 [M][k] (outside [0, n_experts): the slot adds nothing) and
+    weights float32 [M][k]."""
+    lib = load()
+    up.packed.check()
+    down.packed.check()
+    _need_cuda(x, ids, weights, out)
+    M, K = x.shape
+    dt = _act_dtype(x)
+    E, inter = up.n_experts, down.K
+    if up.K != K or down.N != K or up.N != 2 * inter or down.n_experts != E:
+        raise ValueError(f"x [{M}][{K}], up {E} x [{up.N}][{up.K}] and down {down.n_experts} x "
+                         f"[{down.N}][{down.K}] do not fit together")
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise TypeError("ids must be int32 and weights float32")
+    k = ids.shape[1]
+    if tuple(ids.shape) != (M, k) or tuple(weights.shape) != (M, k):
+        raise ValueError("ids and weights must be [M][k]")
+    out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if out is None else out
+    _need_out(out, M, K)
+    if workspace is None:
+        workspace = torch.empty(max(moe_mlp_workspace_bytes(M, k, E, inter, K), 16),
+                                dtype=torch.uint8, device=x.device)
+    _check(lib.w4a8_moe_mlp(_p(x), dt, _p(up.packed.buf), up.packed.buf.numel(), _p(down.packed.buf),
+                            down.packed.buf.numel(), _p(ids), _p(weights), M, k, E, inter, K, _p(out),
+                            _p(workspace), workspace.numel() * workspace.element_size(),
+                            _stream(x.device)))
+    return out
+
+
+def _need_out(out: torch.Tensor, M: int, N: int):
+    if out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N):
+        raise TypeError(f"out must be bfloat16 [{M}][{N}]")
+
+
+@dataclass
+class LoraAdapters:
+    """Low-rank adapters of one projection: A bfloat16 [L][R][K], B bfloat16
+    [L][N][R], scale float32 [L]."""
+    A: torch.Tensor
+    B: torch.Tensor
+    scale: torch.Tensor
+
+    def __post_init__(self):
+        _need_cuda(self.A, self.B, self.scale)
+        if self.A.dtype != torch.bfloat16 or self.B.dtype != torch.bfloat16 or \
+                self.scale.dtype != torch.float32:
+            raise TypeError("A and B must be bfloat16 and scale float32")
+        L, R, _ = self.A.shape
+        if self.B.shape[0] != L or self.B.shape[2] != R or tuple(self.scale.shape) != (L,):
+            raise ValueError("A [L][R][K], B [L][N][R] and scale [L] do not fit together")
+
+
+def lora_linear_workspace_bytes(M: int, N: int, K: int, L: int, R: int) -> int:
+    return int(load().w4a8_lora_linear_workspace_bytes(M, N, K, L, R))
+
+
+def lora_linear(x: torch.Tensor, w: PackedWeight, adapters: LoraAdapters, ids: torch.Tensor,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A shared W4A8 linear plus each row's low-rank adapter: bf16 y [M][N] =
+    linear(x) + scale[l] (x A[l]^T) B[l]^T with l = ids[m], rounded once;
+    a row whose id lies outside [0, L) has no adapter."""
+    lib = load()
+    w.check()
+    _need_cuda(x, ids, out)
+    M, K = x.shape
+    dt = _act_dtype(x)
+    L, R, AK = adapters.A.shape
+    if K != w.K or AK != K or adapters.B.shape[1] != w.N:
+        raise ValueError(f"x [{M}][{K}], weight [{w.N}][{w.K}] and adapters [{L}][{R}][{AK}], "
+                         f"[{L}][{adapters.B.shape[1]}][{R}] do not fit together")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,):
+        raise TypeError("ids must be int32 [M]")
+    out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device) if out is None else out
+    _need_out(out, M, w.N)
+    if workspace is None:
+        workspace = torch.empty(max(lora_linear_workspace_bytes(M, w.N, K, L, R), 16),
+                                dtype=torch.uint8, device=x.device)
+    _check(lib.w4a8_lora_linear(_p(x), dt, _p(w.buf), w.buf.numel(), _p(adapters.A), _p(adapters.B),
+                                _p(adapters.scale), _p(ids), M, w.N, K, L, R, _p(out), _p(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(x.device)))
     return out
 
 

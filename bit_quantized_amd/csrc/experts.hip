@@ -1,0 +1,409 @@
+// Grouping of a batch by expert, and what the expert MLP needs beside its two
+// row-tile products (rows.hip): the down projection of single tokens and the
+// sum over a token's experts.
+#include "experts.h"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+
+// ------------------------------------------------ grouping + quantisation
+//
+// Workgroup 0 groups the pairs: a histogram of the experts in LDS, prefix
+// sums, the tiles of at most BM pairs of one expert each, then the pairs in
+// expert order.  The place of a pair inside its expert follows the order of
+// LDS atomics and may differ between calls; no output depends on it (rows.h).
+// The other workgroups quantise one token each (w4a8_quant_act's rule).
+template <int ACT>
+__global__ void __launch_bounds__(kThreads)
+group_kernel(const void* __restrict__ x, const int* __restrict__ ids, int P, int E, int bm, int K,
+             int8_t* __restrict__ qa, float* __restrict__ sa, int* __restrict__ ntiles,
+             RowTile* __restrict__ tiles, int* __restrict__ list, int* __restrict__ rank) {
+  __shared__ float red[kWaves];
+  __shared__ int s_count[kMaxExperts], s_first[kMaxExperts], s_tile[kMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (blockIdx.x > 0) {
+    const int64_t m = blockIdx.x - 1;
+    quantise_row<ACT, kThreads>(static_cast<const uint8_t*>(x) + m * K * RawRow<ACT>::kBytes, K, qa + m * K,
+                      sa + m, red);
+    return;
+  }
+  for (int e = tid; e < E; e += kThreads) s_count[e] = 0;
+  __syncthreads();
+  constexpr int kAtOnce = 8;
+  for (int p0 = tid; p0 < P; p0 += kAtOnce * kThreads) {
+    int e[kAtOnce], r[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) e[i] = p0 + i * kThreads < P ? ids[p0 + i * kThreads] : -1;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) r[i] = e[i] >= 0 && e[i] < E ? atomicAdd(&s_count[e[i]], 1) : 0;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (p0 + i * kThreads < P) rank[p0 + i * kThreads] = r[i];
+  }
+  __syncthreads();
+  if (tid < 64) {  // prefix sums of pairs and tiles, E / 64 experts per lane
+    const int per = (E + 63) / 64, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+    int pairs = 0, nt = 0;
+    for (int e = e0; e < e1; ++e) {
+      pairs += s_count[e];
+      nt += (s_count[e] + bm - 1) / bm;
+    }
+    int ps = pairs, ts = nt;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int a = __shfl_up(ps, d), b = __shfl_up(ts, d);
+      if (lane >= d) {
+        ps += a;
+        ts += b;
+      }
+    }
+    if (lane == 63) ntiles[0] = ts;
+    ps -= pairs;
+    ts -= nt;
+    for (int e = e0; e < e1; ++e) {
+      s_first[e] = ps;
+      s_tile[e] = ts;
+      ps += s_count[e];
+      ts += (s_count[e] + bm - 1) / bm;
+    }
+  }
+  __syncthreads();
+  for (int e = tid >> 6; e < E; e += kWaves) {
+    const int c = s_count[e], n = (c + bm - 1) / bm;
+    for (int i = lane; i < n; i += 64)
+      tiles[s_tile[e] + i] = RowTile{e, s_first[e] + i * bm, min(bm, c - i * bm), i | (n << 16)};
+  }
+  for (int p0 = tid; p0 < P; p0 += kAtOnce * kThreads) {
+    int e[kAtOnce], r[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int p = p0 + i * kThreads;
+      e[i] = p < P ? ids[p] : -1;
+      r[i] = p < P ? rank[p] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (e[i] >= 0 && e[i] < E) list[s_first[e[i]] + r[i]] = p0 + i * kThreads;
+  }
+}
+
+// ------------------------------------------------- down, single tokens
+//
+// y[m] = sum over the token's slots of weight * (h's codes x the expert's
+// down weight): each wavefront takes the slots wave, wave + 8, ... of one
+// 16-channel block, quantises that slot's h row itself and streams the
+// block's units (all groups, D in flight); the slots are summed in slot
+// order through LDS.  One launch, no partial sums in memory.
+__global__ void __launch_bounds__(kThreads)
+down_token_kernel(RowsArgs a, int k) {
+  constexpr int D = 8;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // [wavefronts][K] codes
+  __shared__ float s_part[kWaves][16];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r16 = lane & 15, j = lane >> 4;
+  const int64_t m = blockIdx.y;
+  const int nb = blockIdx.x, G = a.K / kGroup, nch = a.K / 8;
+  uint8_t* q = smem + wave * a.K;
+  float total = 0.0f;
+  for (int s0 = 0; s0 < k; s0 += kWaves) {
+    const int slot = s0 + wave;
+    const int e = slot < k ? uniform(a.ids[m * k + slot]) : -1;
+    float v = 0.0f;
+    if (e >= 0 && e < a.n_experts) {
+      const int64_t p = m * k + slot;
+      const int64_t b0 = ((int64_t)e * a.nbe + nb) * G;
+      const __amdgpu_buffer_rsrc_t rc = rsrc_of(a.codes + b0 * kBlockBytes, (int64_t)G * kBlockBytes);
+      const __amdgpu_buffer_rsrc_t rs = rsrc_of(a.scales + b0 * 16, (int64_t)G * 64);
+      const __amdgpu_buffer_rsrc_t rz = rsrc_of(a.zeros + b0 * kZeroBlockBytes, (int64_t)G * kZeroBlockBytes);
+      v4u_rows d[D];
+      float sc[D];
+      uint32_t z[D];
+      auto load = [&](int i, int t) __attribute__((always_inline)) {
+        d[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, 16 * lane, (unsigned)uniform(t * kBlockBytes),
+                                                     kNontemporal);
+        sc[i] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * r16, (unsigned)uniform(t * 64), 0));
+        z[i] = __builtin_amdgcn_raw_buffer_load_b8(rz, r16 >> 1, (unsigned)uniform(t * kZeroBlockBytes), 0);
+      };
+#pragma unroll
+      for (int i = 0; i < D; ++i) load(i, i);
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t* hr = reinterpret_cast<const uint8_t*>(a.x) + p * a.K * 2;
+      float amax = 0.0f;
+      for (int ch = lane; ch < nch; ch += 64) {
+        v4u_rows raw[1];
+        float t[8];
+        RawRow<kRawBf16>::load(hr, ch, raw);
+        RawRow<kRawBf16>::widen(raw, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(t[i]));
+      }
+      amax = wave_max64(amax);
+      const float scale = amax / 127.0f, inv = 1.0f / scale;
+      for (int ch = lane; ch < nch; ch += 64) {
+        v4u_rows raw[1];
+        float t[8];
+        RawRow<kRawBf16>::load(hr, ch, raw);
+        RawRow<kRawBf16>::widen(raw, t);
+        *reinterpret_cast<uint2*>(q + 8 * ch) =
+            amax != 0.0f ? quant8_codes(t, scale, inv) : make_uint2(0u, 0u);
+      }
+      // the wavefront's own LDS writes, read by its other lanes
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      for (int tb = 0; tb < G; tb += D) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+          if (tb + i < G) {
+            v4i lo, hi;
+            unpack_unit(d[i], ((z[i] >> (4 * (r16 & 1))) & 0xFu) * 0x01010101u, lo, hi);
+            const uint8_t* frag = q + (tb + i) * kGroup + 16 * j;  // every row the same
+            v4i c = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const v4i*>(frag), lo,
+                                                          kBiasSeed, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const v4i*>(frag + 64), hi, c,
+                                                      0, 0, 0);
+            v += sc[i] * unbias(c[0]);
+          }
+          load(i, tb + i + D);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      v *= scale * a.pw[p];
+    }
+    if (lane < 16) s_part[wave][lane] = v;
+    __syncthreads();
+    if (threadIdx.x < 16) {
+      const int n = min(kWaves, k - s0);
+      for (int i = 0; i < n; ++i) total += s_part[i][threadIdx.x];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x < 16) a.y[m * (16 * a.nbe) + 16 * nb + threadIdx.x] = f32_to_bf16_rne(total);
+}
+
+// ------------------------------------------------------- sum over experts
+//
+// y[m][n] = bf16(sum_j parts[m k + j][n]) over the slots held here, in slot
+// order; eight channels per thread.
+__global__ void __launch_bounds__(256)
+combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids, int64_t M, int k, int E,
+               int N, uint16_t* __restrict__ y) {
+  const int per = N / 8;
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= M * per) return;
+  const int64_t m = t / per;
+  const int n = (int)(t - m * per) * 8;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < k; ++s) {
+    const int e = ids[m * k + s];
+    if (e < 0 || e >= E) continue;
+    const float4* p = reinterpret_cast<const float4*>(parts + (m * k + s) * N + n);
+    const float4 a = p[0], b = p[1];
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = (uint32_t)f32_to_bf16_rne(v[2 * i]) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1]) << 16);
+  *reinterpret_cast<uint4*>(y + m * N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+// Rows a tile of the planned kernels holds: the smallest of 16, 32, 64 and
+// 256 that holds an expert's even share of the pairs with room to spare.
+static int tile_rows(int64_t P, int E) {
+  const double share = (double)P / E;
+  return share <= 10 ? 16 : share <= 22 ? 32 : share <= 96 ? 64 : kTileRows;
+}
+
+// Single tokens (a few pairs) skip the grouping: each pair is a tile.
+static bool direct(int64_t P, int64_t I, int64_t K) {
+  return P <= 16 && I <= 4096 && K <= 16384;
+}
+
+MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
+  MoePlan p;
+  // tokens of one pass: 32-bit offsets into the codes, tile counts of 16 bits
+  int64_t mc = M;
+  const int64_t most = (int64_t)1 << 19;
+  if (mc > most / k) mc = most / k;
+  const int64_t rows = kPrefillMaxBytes / (K > I * k ? K : I * k);
+  if (mc > rows) mc = rows;
+  p.tokens = mc;
+  if (mc < 1) return p;
+  const int64_t P = mc * k;
+  p.direct = direct(M * k, I, K);
+  p.bm = tile_rows(P, E);
+  p.max_tiles = P / p.bm + (E < P ? E : P);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up256(bytes);
+    return o;
+  };
+  p.h = take(P * I * 2);
+  if (!p.direct) {
+    p.qa = take(mc * K);
+    p.sa = take(mc * 4);
+    p.count = take(4);
+    p.tiles = take(p.max_tiles * (int64_t)sizeof(RowTile));
+    p.list = take(P * 4);
+    p.rank = take(P * 4);
+    p.hq = take(P * I);
+    p.hs = take(P * 4);
+    p.parts = take(P * K * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+static hipError_t moe_direct(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
+  uint16_t* h = reinterpret_cast<uint16_t*>(m.ws + p.h);
+  RowsArgs a{};
+  a.x = m.x;
+  a.codes = m.up.codes;
+  a.zeros = m.up.zeros;
+  a.scales = m.up.scales;
+  a.ids = m.ids;
+  a.n_experts = m.E;
+  a.kind = kDirect;
+  a.src_rows = m.M;
+  a.K = (int)m.K;
+  a.nbe = (int)(2 * m.I / 16);
+  a.div = m.k;
+  a.cols = (int)(m.I / 16);
+  a.kw = 3;
+  a.ncol = 1;
+  a.strips = a.cols;
+  a.sg = (int)(m.K / kGroup);
+  a.h = h;
+  hipError_t e = launch_rows_stream(a, 1, m.x_dtype == 0 ? kRawBf16 : kRawF32, kSwiglu,
+                                    m.M * m.k * a.strips, 1, st);
+  if (e != hipSuccess) return e;
+  RowsArgs d{};
+  d.x = h;
+  d.codes = m.down.codes;
+  d.zeros = m.down.zeros;
+  d.scales = m.down.scales;
+  d.ids = m.ids;
+  d.n_experts = m.E;
+  d.K = (int)m.I;
+  d.nbe = (int)(m.K / 16);
+  d.pw = m.weights;
+  d.y = m.y;
+  hipLaunchKernelGGL(down_token_kernel, dim3((unsigned)d.nbe, (unsigned)m.M), dim3(kThreads),
+                     (size_t)kWaves * m.I, st, d, m.k);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
+  if (p.direct) return moe_direct(m, p, st);
+  const int64_t P = m.M * m.k;
+  int8_t* qa = reinterpret_cast<int8_t*>(m.ws + p.qa);
+  float* sa = reinterpret_cast<float*>(m.ws + p.sa);
+  int* count = reinterpret_cast<int*>(m.ws + p.count);
+  RowTile* tiles = reinterpret_cast<RowTile*>(m.ws + p.tiles);
+  int* list = reinterpret_cast<int*>(m.ws + p.list);
+  int* rank = reinterpret_cast<int*>(m.ws + p.rank);
+  uint16_t* h = reinterpret_cast<uint16_t*>(m.ws + p.h);
+  int8_t* hq = reinterpret_cast<int8_t*>(m.ws + p.hq);
+  float* hs = reinterpret_cast<float*>(m.ws + p.hs);
+  float* parts = reinterpret_cast<float*>(m.ws + p.parts);
+  const int64_t max_tiles = P / p.bm + (m.E < P ? m.E : P);
+
+  if (m.x_dtype == 0)
+    hipLaunchKernelGGL((group_kernel<kRawBf16>), dim3((unsigned)(1 + m.M)), dim3(kThreads), 0, st, m.x,
+                       m.ids, (int)P, m.E, p.bm, (int)m.K, qa, sa, count, tiles, list, rank);
+  else
+    hipLaunchKernelGGL((group_kernel<kRawF32>), dim3((unsigned)(1 + m.M)), dim3(kThreads), 0, st, m.x,
+                       m.ids, (int)P, m.E, p.bm, (int)m.K, qa, sa, count, tiles, list, rank);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+
+  const bool big = p.bm == kTileRows;
+  const int mt = p.bm / 16;
+  RowsArgs a{};
+  a.qa = qa;
+  a.sa = sa;
+  a.codes = m.up.codes;
+  a.zeros = m.up.zeros;
+  a.scales = m.up.scales;
+  a.ntiles = count;
+  a.tiles = tiles;
+  a.list = list;
+  a.ids = m.ids;
+  a.n_experts = m.E;
+  a.kind = kPlanned;
+  a.src_rows = m.M;
+  a.K = (int)m.K;
+  a.nbe = (int)(2 * m.I / 16);
+  a.div = m.k;
+  a.cols = (int)(m.I / 16);
+  a.h = h;
+  const int G = (int)(m.K / kGroup), GI = (int)(m.I / kGroup);
+  // LDS of 64 KiB: 32 / mt groups at a time, in slices of equal length
+  auto slice = [&](int groups) {
+    const int most = 32 / mt, n = (groups + most - 1) / most;
+    return (groups + n - 1) / n;
+  };
+  if (big) {
+    a.strips = a.cols / 8;
+    e = launch_rows_tile(a, kSwiglu, max_tiles * a.strips, 1, st);
+  } else {
+    a.kw = 0;
+    a.ncol = 1;
+    a.strips = (a.cols + 7) / 8;
+    a.sg = slice(G);
+    e = launch_rows_stream(a, mt, kCodes, kSwiglu, max_tiles * a.strips, 1, st);
+  }
+  if (e != hipSuccess) return e;
+
+  // the down product quantises its rows itself where few rows share a tile
+  const bool raw = p.bm == 16 && GI <= 32;
+  if (!raw) {
+    e = launch_quant(h, 0, P, m.I, hq, hs, st);
+    if (e != hipSuccess) return e;
+  }
+  RowsArgs d = a;
+  d.qa = hq;
+  d.sa = hs;
+  d.x = h;
+  d.codes = m.down.codes;
+  d.zeros = m.down.zeros;
+  d.scales = m.down.scales;
+  d.src_rows = P;
+  d.K = (int)m.I;
+  d.nbe = (int)(m.K / 16);
+  d.div = 1;
+  d.cols = d.nbe;
+  d.pw = m.weights;
+  d.h = nullptr;
+  d.parts = parts;
+  if (big) {
+    d.strips = (d.nbe + 15) / 16;
+    e = launch_rows_tile(d, kParts, max_tiles * d.strips, 1, st);
+  } else {
+    d.sg = raw ? GI : slice(GI);
+    d.kw = 0;
+    // runs of about 24 units per wavefront where one slice holds all groups
+    d.ncol = d.sg == GI ? (24 + GI - 1) / GI : 1;
+    const int per = 8 * d.ncol;
+    d.strips = (d.cols + per - 1) / per;
+    e = launch_rows_stream(d, mt, raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st);
+  }
+  if (e != hipSuccess) return e;
+  const int64_t total = m.M * (m.K / 8);
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, parts,
+                     m.ids, m.M, m.k, m.E, (int)m.K, m.y);
+  return hipGetLastError();
+}
+
+}  // namespace w4a8

@@ -1,0 +1,270 @@
+// A shared W4A8 projection with a low-rank adapter chosen per row:
+//   y[m] = bf16( sa[m] * sum_g s P  +  scale[l] * (x[m] A[l]^T) B[l]^T ),  l = ids[m].
+//
+// The shared product runs on the row-tile kernels (rows.hip); this file has
+// the adapters' first half x A^T, and the reduction that adds the second half
+// where the shared product was split over K.
+#include "lora.h"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+
+// ----------------------------------------- quantisation and x A^T together
+//
+// Workgroups [0, M) quantise one row each.  The others take a fragment of 16
+// rows, every `slots`-th of the distinct adapters among them, and a K slice,
+// which the wavefronts share: for an adapter, v_mfma_f32_16x16x32_bf16 of the
+// 16 rows (A operand) against its rows of A (B operand), float sums, and only
+// the rows that use this adapter are written.  Many rows that use one adapter
+// read it once; a row alone with its adapter wastes matrix-core slots, not
+// memory traffic, which is what bounds this step.  bf16 activations are exact
+// operands; float ones go in as two bf16 parts (16 significant bits, below
+// the bf16 weights' own 8).
+template <int ACT, int RT>
+__global__ void __launch_bounds__(kThreads)
+adapter_down_kernel(LoraArgs a, int8_t* __restrict__ qa, float* __restrict__ sa,
+                    float* __restrict__ hx, int slots, int slices) {
+  constexpr int U = RT >= 4 ? 2 : 4;  // steps of 32 inputs whose loads are in flight
+  constexpr bool F32 = ACT == kRawF32;
+  __shared__ float s_red[kWaves][RT * 4][64];
+  __shared__ float s_max[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const uint8_t* x = static_cast<const uint8_t*>(a.x);
+  const int K = (int)a.K;
+  if ((int64_t)blockIdx.x < a.M) {
+    const int64_t m = blockIdx.x;
+    quantise_row<ACT, kThreads>(x + m * K * RawRow<ACT>::kBytes, K, qa + m * K, sa + m, s_max);
+    return;
+  }
+  const int b = (int)(blockIdx.x - a.M);
+  const int slice = b % slices, slot = b / slices % slots;
+  const int64_t m0 = (int64_t)(b / slices / slots) * 16;
+  const int r16 = lane & 15, j = lane >> 4;
+  const int64_t m = m0 + r16;
+  const int id = m < a.M ? a.ids[m] : -1;
+  const bool has = id >= 0 && id < a.L;
+  const int steps = K / 32;
+  const int s0 = steps * slice / slices, s1 = steps * (slice + 1) / slices;
+  const int t0 = s0 + (s1 - s0) * wave / kWaves, t1 = s0 + (s1 - s0) * (wave + 1) / kWaves;
+  const uint8_t* xrow = x + (m < a.M ? m : a.M - 1) * K * RawRow<ACT>::kBytes;
+  uint64_t todo = __ballot(has) & 0xFFFFull;
+  for (int at = 0; todo; ++at) {
+    const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    const uint64_t mine = __ballot(has && id == l) & 0xFFFFull;
+    todo &= ~mine;
+    if (at % slots != slot) continue;
+    const uint16_t* arow[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      arow[t] = a.A + ((int64_t)l * a.R + min(16 * t + r16, a.R - 1)) * K;
+    v4f_rows acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = v4f_rows{0.f, 0.f, 0.f, 0.f};
+    for (int t = t0; t < t1; t += U) {
+      v4u_rows xr[U][RawRow<ACT>::kLoads];
+      v4i br[U][RT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = 32 * min(t + u, t1 - 1) + 8 * j;
+        RawRow<ACT>::load(xrow, k / 8, xr[u]);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) br[u][q] = *reinterpret_cast<const v4i*>(arow[q] + k);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= t1) break;
+        v4i hi, lo;
+        if constexpr (F32) {
+          float v[8];
+          RawRow<ACT>::widen(xr[u], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t h0 = f32_to_bf16_rne(v[2 * e]), h1 = f32_to_bf16_rne(v[2 * e + 1]);
+            const uint32_t l0 = f32_to_bf16_rne(v[2 * e] - __uint_as_float(h0 << 16));
+            const uint32_t l1 = f32_to_bf16_rne(v[2 * e + 1] - __uint_as_float(h1 << 16));
+            hi[e] = (int)(h0 | (h1 << 16));
+            lo[e] = (int)(l0 | (l1 << 16));
+          }
+        } else {
+          hi = __builtin_bit_cast(v4i, xr[u][0]);
+        }
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          const v8bf_rows bv = __builtin_bit_cast(v8bf_rows, br[u][q]);
+          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, hi), bv,
+                                                           acc[q], 0, 0, 0);
+          if constexpr (F32)
+            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, lo), bv,
+                                                             acc[q], 0, 0, 0);
+        }
+      }
+    }
+    // the wavefronts' sums, in order; one adapter after another reuses the LDS
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_red[wave][q * 4 + r][lane] = acc[q][r];
+    __syncthreads();
+    for (int o = tid; o < RT * 256; o += kThreads) {
+      const int q = o >> 8, r = (o >> 6) & 3, ln = o & 63;
+      const int row = 4 * (ln >> 4) + r, rank = 16 * q + (ln & 15);
+      if (!((mine >> row) & 1) || rank >= a.R) continue;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v += s_red[w][q * 4 + r][ln];
+      hx[((int64_t)slice * a.M + m0 + row) * a.R + rank] = v;
+    }
+  }
+}
+
+// --------------------------------- K slices summed, adapter product added
+__global__ void __launch_bounds__(256)
+adapt_reduce_kernel(const float* __restrict__ parts, int ksplit, const float* __restrict__ sa,
+                    int64_t M, int N, AdaptArgs ad, uint16_t* __restrict__ y) {
+  __shared__ float s_hx[kMaxRank];
+  const int64_t m = blockIdx.y;
+  const int id = ad.ids[m];
+  const bool has = id >= 0 && id < ad.L;
+  if (has)
+    for (int r = threadIdx.x; r < ad.R; r += 256) s_hx[r] = adapter_sum(ad, M, m, r, ad.scale[id]);
+  __syncthreads();
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float v = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < ksplit; ++k) v += parts[((int64_t)k * M + m) * N + n];
+  v *= sa[m];
+  if (has) v += adapter_dot(s_hx, ad.B + ((int64_t)id * N + n) * ad.R, ad.R);
+  y[m * N + n] = f32_to_bf16_rne(v);
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+template <int ACT, int RT>
+void down_launch(const LoraArgs& l, const LoraPlan& p, int8_t* qa, float* sa, float* hx, hipStream_t st) {
+  const int64_t blocks = l.M + (l.M + 15) / 16 * p.slots * p.slices;
+  hipLaunchKernelGGL((adapter_down_kernel<ACT, RT>), dim3((unsigned)blocks), dim3(kThreads), 0, st, l, qa,
+                     sa, hx, p.slots, p.slices);
+}
+
+template <int ACT>
+void down_rank(const LoraArgs& l, const LoraPlan& p, int8_t* qa, float* sa, float* hx, hipStream_t st) {
+  if (l.R <= 16)
+    down_launch<ACT, 1>(l, p, qa, sa, hx, st);
+  else if (l.R <= 32)
+    down_launch<ACT, 2>(l, p, qa, sa, hx, st);
+  else if (l.R <= 64)
+    down_launch<ACT, 4>(l, p, qa, sa, hx, st);
+  else
+    down_launch<ACT, 8>(l, p, qa, sa, hx, st);
+}
+
+}  // namespace
+
+LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
+  LoraPlan p;
+  const int64_t cus = device_cus(), G = K / kGroup, cols = N / kBlockCols;
+  int64_t mc = kPrefillMaxBytes / K;
+  if (mc >= kTileRows) mc = mc / kTileRows * kTileRows;
+  if (mc > M) mc = M;
+  p.rows = mc;
+  if (mc < 1) return p;
+  if (mc <= 64) {
+    p.mt = (int)((mc + 15) / 16);
+    if (mc <= 16) {  // whole K per workgroup, one launch, while the columns fill the machine
+      while (p.kw < 3 && cols / (8 >> p.kw) < cus) ++p.kw;
+      if (cols < cus / 2) p.kw = -1;
+    } else {
+      p.kw = -1;
+    }
+    if (p.kw < 0) {  // K slices: two workgroups per compute unit
+      p.kw = 0;
+      const int64_t strips = (cols + 7) / 8;
+      int64_t ks = 2 * cus / strips;
+      if (ks > G / 4) ks = G / 4;
+      p.ksplit = (int)(ks > 1 ? ks : 1);
+      if (p.ksplit == 1) p.ksplit = 1;
+    }
+  } else {
+    const int64_t tiles = (mc + kTileRows - 1) / kTileRows * ((N + kTileCols - 1) / kTileCols);
+    int64_t ks = cus / tiles;
+    if (ks > G / 4) ks = G / 4;
+    p.ksplit = (int)(ks > 1 ? ks : 1);
+  }
+  const int64_t frags = (mc + 15) / 16;
+  p.slots = (int)(mc > 256 ? 1 : mc < 16 ? mc : 16);
+  if (p.slots > L) p.slots = L;
+  int64_t sl = 4 * cus / (frags * p.slots), most = (K / 32 + kWaves - 1) / kWaves;
+  if (sl > most) sl = most;
+  if (sl > 16) sl = 16;
+  p.slices = (int)(sl > 1 ? sl : 1);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up256(bytes);
+    return o;
+  };
+  p.qa = take(mc * K);
+  p.sa = take(mc * 4);
+  p.hx = take((int64_t)p.slices * mc * R * 4);
+  // (the streaming kernel past 16 rows always goes through the sums)
+  const bool sums = p.ksplit > 1 || p.mt > 1 || (p.mt == 1 && cols < cus / 2);
+  if (sums) p.parts = take((int64_t)p.ksplit * mc * N * 4);
+  else p.parts = -1;
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {
+  int8_t* qa = reinterpret_cast<int8_t*>(l.ws + p.qa);
+  float* sa = reinterpret_cast<float*>(l.ws + p.sa);
+  float* hx = reinterpret_cast<float*>(l.ws + p.hx);
+  float* parts = p.parts >= 0 ? reinterpret_cast<float*>(l.ws + p.parts) : nullptr;
+  if (l.x_dtype == 0)
+    down_rank<kRawBf16>(l, p, qa, sa, hx, st);
+  else
+    down_rank<kRawF32>(l, p, qa, sa, hx, st);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  RowsArgs a{};
+  a.qa = qa;
+  a.sa = sa;
+  a.codes = l.w.codes;
+  a.zeros = l.w.zeros;
+  a.scales = l.w.scales;
+  a.kind = kDense;
+  a.M = l.M;
+  a.src_rows = l.M;
+  a.K = (int)l.K;
+  a.nbe = (int)(l.N / 16);
+  a.n_experts = 1;
+  a.div = 1;
+  a.cols = a.nbe;
+  a.parts = parts;
+  a.y = l.y;
+  a.ad = AdaptArgs{hx, l.B, l.scale, l.ids, p.slices, l.L, l.R};
+  const int G = (int)(l.K / kGroup);
+  if (p.mt) {
+    a.kw = p.kw;
+    a.ncol = 1;
+    const int cw = 8 >> p.kw, per = (G + p.ksplit - 1) / p.ksplit;
+    const int most = 32 / p.mt, n = (per + most - 1) / most;
+    a.strips = (a.cols + cw - 1) / cw;
+    a.sg = (per + n - 1) / n;
+    e = launch_rows_stream(a, p.mt, kCodes, parts ? kSplit : kAdapt, a.strips, p.ksplit, st);
+  } else {
+    const int64_t tiles = (l.M + kTileRows - 1) / kTileRows;
+    a.strips = (a.nbe + 15) / 16;
+    e = launch_rows_tile(a, parts ? kSplit : kAdapt, tiles * a.strips, p.ksplit, st);
+  }
+  if (e != hipSuccess || !parts) return e;
+  hipLaunchKernelGGL(adapt_reduce_kernel, dim3((unsigned)((l.N + 255) / 256), (unsigned)l.M), dim3(256), 0,
+                     st, parts, p.ksplit, sa, l.M, (int)l.N, a.ad, l.y);
+  return hipGetLastError();
+}
+
+}  // namespace w4a8

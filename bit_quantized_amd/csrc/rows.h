@@ -1,0 +1,263 @@
+// The W4A8 product for batches whose rows use different weights, shared by the
+// expert MLP (experts.hip) and the per-row adapters (lora.hip).
+//
+// Both products work on tiles of rows that share one weight:
+//   - a tile of the expert MLP is a run of (token, slot) pairs routed to one
+//     expert, from the list that the grouping step of the call wrote;
+//   - the adapter linear has one weight, and its tiles are consecutive rows.
+// The arithmetic is that of w4a8_gemm: exact int32 products per group of 128
+// input channels, rescaled by s[n][g] in float32, groups in order.  A row's
+// result depends on its own codes and on the weight only, never on which
+// other rows share its tile or where in the tile it sits (every row of a
+// matrix-core product is computed by itself), so the order in which rows are
+// grouped does not show in the output.
+#pragma once
+
+#include "w4a8_internal.h"
+
+namespace w4a8 {
+
+typedef unsigned int v4u_rows __attribute__((ext_vector_type(4)));
+typedef float v4f_rows __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf_rows __attribute__((ext_vector_type(8)));
+
+// Where a workgroup's rows come from.
+enum RowKind {
+  kPlanned = 0,  // tiles listed by the grouping step
+  kDirect = 1,   // tile t is pair t alone, its expert ids[t]
+  kDense = 2,    // one weight; tile t is rows [t * BM, ...)
+};
+// What becomes of a row's sums.
+enum RowOut {
+  kSwiglu = 0,  // gate and up blocks together: silu(gate) * up as bf16
+  kParts = 1,   // float, times the activation scale and the pair's weight
+  kSplit = 2,   // unscaled float sums of one K slice
+  kAdapt = 3,   // bf16 with the row's adapter product added
+};
+enum RowAct { kCodes = 0, kRawBf16 = 1, kRawF32 = 2 };
+
+// A tile of grouped rows: pairs list[first .. first + rows) of `expert`; it is
+// tile `place & 0xFFFF` of the expert's `place >> 16`.
+struct RowTile {
+  int expert, first, rows, place;
+};
+
+// The adapters of a call: y[m] += scale[l] * (x[m] A[l]^T) B[l]^T, l = ids[m];
+// rows whose id lies outside [0, L) have none.  hx: the sums x A^T of the
+// call, [slices][M][R], not yet scaled.
+struct AdaptArgs {
+  const float* hx;
+  const uint16_t* B;
+  const float* scale;
+  const int* ids;
+  int slices, L, R;
+};
+
+struct RowsArgs {
+  const int8_t* qa;  // activation codes [source rows][K] and their scales
+  const float* sa;
+  const void* x;     // raw activations [source rows][K] (RowAct kRaw*)
+  const uint8_t* codes;  // planes of the packed weight of all experts
+  const uint8_t* zeros;
+  const float* scales;
+  const int* ntiles;     // kPlanned
+  const RowTile* tiles;
+  const int* list;
+  const int* ids;        // kDirect: the pairs' experts
+  int n_experts;
+  int kind;
+  int64_t M;             // kDense: rows
+  int64_t src_rows;      // rows of qa / x
+  int K;                 // input channels
+  int nbe;               // 16-channel blocks of one expert's weight
+  int div;               // source row of pair p is p / div
+  int cols;              // column units per expert: blocks, or gate/up block pairs
+  int strips;            // workgroups per tile along the columns
+  int kw;                // log2 of the wavefronts that share a column's groups
+  int ncol;              // consecutive columns per wavefront
+  int sg;                // groups of input channels staged at a time
+  const float* pw;       // weights of the pairs (kParts)
+  uint16_t* h;           // kSwiglu output [pairs][16 * cols]
+  float* parts;          // kParts [pairs][16 nbe]; kSplit [slices][M][16 nbe]
+  uint16_t* y;           // kAdapt output [M][16 nbe]
+  AdaptArgs ad;
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Workgroups are dealt to the 8 XCDs round-robin; workgroup b of T takes item
+// xcd_run(b, T), so that each XCD has a contiguous run of items.
+__device__ __forceinline__ int xcd_run(int b, int T) {
+  const int xcd = b & 7, local = b >> 3;
+  const int per = T >> 3, rem = T & 7;
+  return xcd * per + (xcd < rem ? xcd : rem) + local;
+}
+
+struct Where {
+  int expert, first, rows, strip;
+};
+
+// The tile and the column strip of this workgroup; false: nothing to do.
+// Work is ordered by expert, then strip, then tile: the tiles of one expert
+// that read the same weights run side by side on one XCD.
+template <int BM>
+__device__ __forceinline__ bool locate(const RowsArgs& a, Where& w) {
+  const int b = blockIdx.x;
+  if (a.kind == kPlanned) {
+    const int total = uniform(a.ntiles[0]) * a.strips;
+    if (b >= total) return false;
+    const int at = xcd_run(b, total);
+    const int t0 = at / a.strips;
+    const int place = uniform(a.tiles[t0].place);
+    const int f = t0 - (place & 0xFFFF), n = place >> 16;
+    const int local = at - f * a.strips;
+    w.strip = local / n;
+    const RowTile t = a.tiles[f + local % n];
+    w.expert = uniform(t.expert);
+    w.first = uniform(t.first);
+    w.rows = uniform(t.rows);
+    return true;
+  }
+  if (a.kind == kDirect) {
+    w.first = b / a.strips;
+    w.strip = b % a.strips;
+    w.rows = 1;
+    w.expert = uniform(a.ids[w.first]);
+    return w.expert >= 0 && w.expert < a.n_experts;
+  }
+  const int tiles = (int)((a.M + BM - 1) / BM);
+  const int at = xcd_run(b, tiles * a.strips);
+  w.strip = at / tiles;
+  w.first = (at % tiles) * BM;
+  w.rows = (int)(a.M - w.first < BM ? a.M - w.first : BM);
+  w.expert = 0;
+  return true;
+}
+
+// Pair (or row) i of the tile.
+__device__ __forceinline__ int pair_of(const RowsArgs& a, const Where& w, int i) {
+  return a.kind == kPlanned ? a.list[w.first + i] : w.first + i;
+}
+
+// Eight consecutive raw activations as float.
+template <int ACT>
+struct RawRow {
+  static constexpr int kBytes = ACT == kRawF32 ? 4 : 2;
+  static constexpr int kLoads = ACT == kRawF32 ? 2 : 1;
+  static __device__ __forceinline__ void load(const uint8_t* row, int ch, v4u_rows* r) {
+    const v4u_rows* p = reinterpret_cast<const v4u_rows*>(row + (int64_t)ch * 8 * kBytes);
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) r[l] = p[l];
+  }
+  static __device__ __forceinline__ void widen(const v4u_rows* r, float* v) {
+    if constexpr (ACT == kRawF32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i >> 2][i & 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(r[0][i] << 16);
+        v[2 * i + 1] = __uint_as_float(r[0][i] & 0xFFFF0000u);
+      }
+    }
+  }
+};
+
+// One row quantised by a workgroup of kThreads (the rule of w4a8_quant_act);
+// red: one float per wavefront in LDS.
+constexpr int kHeld = 2;  // chunks of eight a thread keeps in registers
+template <int ACT, int kThreads>
+__device__ __forceinline__ void quantise_row(const uint8_t* xr, int K, int8_t* out, float* sa,
+                                             float* red) {
+  using RR = RawRow<ACT>;
+  const int tid = threadIdx.x, nch = K / 8;
+  const bool held = nch <= kHeld * kThreads;
+  v4u_rows raw[kHeld][RR::kLoads];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * kThreads < nch) RR::load(xr, tid + i * kThreads, raw[i]);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * kThreads < nch) {
+      float v[8];
+      RR::widen(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    }
+  for (int ch = tid + kHeld * kThreads; ch < nch; ch += kThreads) {
+    v4u_rows r[RR::kLoads];
+    float v[8];
+    RR::load(xr, ch, r);
+    RR::widen(r, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  }
+  amax = wave_max64(amax);
+  if ((tid & 63) == 0) red[tid >> 6] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) amax = fmaxf(amax, red[w]);
+  const float scale = amax / 127.0f, inv = 1.0f / scale;
+  if (tid == 0) *sa = scale;
+  auto put = [&](int ch, const v4u_rows* r) __attribute__((always_inline)) {
+    float v[8];
+    RR::widen(r, v);
+    *reinterpret_cast<uint2*>(out + 8 * (int64_t)ch) =
+        amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * kThreads < nch) put(tid + i * kThreads, raw[i]);
+  if (!held)
+    for (int ch = tid + kHeld * kThreads; ch < nch; ch += kThreads) {
+      v4u_rows r[RR::kLoads];
+      RR::load(xr, ch, r);
+      put(ch, r);
+    }
+}
+
+// Codes of one packed unit (16 channels x 128 inputs), its lane's zero point
+// applied: the two int8 matrix-core operands.
+__device__ __forceinline__ void unpack_unit(const v4u_rows& d, uint32_t zz, v4i& lo, v4i& hi) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    lo[t] = (int)sub_zero_bytes(d[t] & 0x0F0F0F0Fu, zz);
+    hi[t] = (int)sub_zero_bytes((d[t] >> 4) & 0x0F0F0F0Fu, zz);
+  }
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// sum_r hx[r] B[n][r] over one adapter, hx already scaled (LDS or global).
+__device__ __forceinline__ float adapter_dot(const float* hx, const uint16_t* brow, int R) {
+  float v = 0.0f;
+  for (int r = 0; r < R; r += 8) {
+    const v4u_rows d = *reinterpret_cast<const v4u_rows*>(brow + r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v += hx[r + 2 * i] * __uint_as_float(d[i] << 16);
+      v += hx[r + 2 * i + 1] * __uint_as_float(d[i] & 0xFFFF0000u);
+    }
+  }
+  return v;
+}
+
+// Row m's scaled adapter sums: scale * sum over the slices of hx[.][m][r].
+__device__ __forceinline__ float adapter_sum(const AdaptArgs& ad, int64_t M, int64_t m, int r, float s) {
+  float v = 0.0f;
+  for (int k = 0; k < ad.slices; ++k) v += ad.hx[((int64_t)k * M + m) * ad.R + r];
+  return s * v;
+}
+
+// Launchers (rows.hip).  `raw`: RowAct of the input; mt: 16-row tiles per
+// workgroup (1..4) of the weight-streaming kernel.
+hipError_t launch_rows_stream(const RowsArgs& a, int mt, int act, int out, int64_t blocks,
+                              int ksplit, hipStream_t st);
+hipError_t launch_rows_tile(const RowsArgs& a, int out, int64_t blocks, int ksplit, hipStream_t st);
+// Rows per workgroup of launch_rows_tile, and its output channels.
+constexpr int kTileRows = 256;
+constexpr int kTileCols = 256;
+constexpr int kMaxRank = 128;  // of an adapter
+
+}  // namespace w4a8

@@ -1,0 +1,615 @@
+// Row-tile kernels of the W4A8 product whose weight depends on the row.
+//
+// rows_stream_kernel: few rows per weight.  The call costs what streaming
+// the weights costs, so the weights go straight from memory to registers
+// (one 1 KiB unit of 16 channels x 128 inputs per wavefront load, D units in
+// flight per wavefront), are unpacked there and multiplied on the int8 matrix
+// cores with up to 64 rows of activations staged in LDS in operand order.
+//
+// rows_tile_kernel: many rows per weight, 256 rows x 256 channels, bound by
+// the matrix cores and the per-group rescale.
+#include "rows.h"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+
+// ------------------------------------------------------------ few rows
+//
+// Per group: acc += s[n][g] * P, P the exact int32 product.  A workgroup of
+// eight wavefronts takes one tile (up to 16 MT rows) and a strip of columns;
+// 2^kw wavefronts share a column's groups (summed in order through LDS), the
+// rest take columns of their own.  A column is a 16-channel block, or for
+// kSwiglu a gate block with its up block.
+//
+// Staged activations: [MT][groups][2 halves][64 lanes][16 B], lane 16 j + r
+// holding row r, input channels 128 g + 64 h + 16 j .. + 15, so a fragment is
+// one conflict-free 16-byte read per lane.  Rows past the tile are never
+// written: an int8 product of any bytes is finite and belongs to no output.
+// ONE: the tile is a single row, kept as [groups][2][4][16 B] and read by all
+// rows of the operand.
+template <int MT, bool ONE, int ACT, int OUT>
+__global__ void __launch_bounds__(kThreads)
+rows_stream_kernel(RowsArgs a) {
+  constexpr int BM = 16 * MT;
+  constexpr int NBK = OUT == kSwiglu ? 2 : 1;  // blocks per column
+  constexpr int D = NBK == 2 ? 4 : 8;          // columns' units in flight
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int s_pair[BM], s_src[BM];
+  __shared__ float s_scale[BM], s_max[kWaves];
+  __shared__ float s_hx[OUT == kAdapt ? BM * kMaxRank : 1];  // scaled x A^T of the rows
+
+  Where w;
+  if (!locate<BM>(a, w)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int r16 = lane & 15, j = lane >> 4;
+  const int G = a.K / kGroup;
+  const int KW = 1 << a.kw, CW = kWaves >> a.kw;
+  const int kwi = wave & (KW - 1), cw = wave >> a.kw;
+  const int c0 = (w.strip * CW + cw) * a.ncol;
+  const int nc = min(a.ncol, a.cols - c0) > 0 ? min(a.ncol, a.cols - c0) : 0;
+  const int gb = G * blockIdx.y / gridDim.y, ge = G * (blockIdx.y + 1) / gridDim.y;
+
+  // the tile's rows
+  if (tid < w.rows) {
+    const int p = pair_of(a, w, tid);
+    const int src = p / a.div;
+    s_pair[tid] = p;
+    s_src[tid] = src;
+    if constexpr (ACT == kCodes) s_scale[tid] = a.sa[src];
+  }
+  if constexpr (OUT == kAdapt) {
+    for (int i = tid; i < w.rows * a.ad.R; i += kThreads) {
+      const int row = i / a.ad.R, id = a.ad.ids[w.first + row];
+      if (id >= 0 && id < a.ad.L)
+        s_hx[i] = adapter_sum(a.ad, a.M, w.first + row, i - row * a.ad.R, a.ad.scale[id]);
+    }
+  }
+
+  float acc[NBK][MT][4];
+#pragma unroll
+  for (int b = 0; b < NBK; ++b)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[b][m][r] = 0.0f;
+
+  // One column's sums to where they go.
+  auto emit = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * m + 4 * j + r;
+        if (row >= w.rows) continue;
+        if constexpr (OUT == kSwiglu) {
+          const float s = s_scale[row];
+          a.h[(int64_t)s_pair[row] * (16 * a.cols) + 16 * c + r16] =
+              f32_to_bf16_rne(silu_mul(s * acc[0][m][r], s * acc[1][m][r]));
+        } else if constexpr (OUT == kParts) {
+          a.parts[(int64_t)s_pair[row] * (16 * a.nbe) + 16 * c + r16] =
+              s_scale[row] * a.pw[s_pair[row]] * acc[0][m][r];
+        } else if constexpr (OUT == kSplit) {
+          a.parts[((int64_t)blockIdx.y * a.M + w.first + row) * (16 * a.nbe) + 16 * c + r16] =
+              acc[0][m][r];
+        } else {
+          const int64_t row_m = w.first + row, n = 16 * c + r16;
+          const int id = a.ad.ids[row_m];
+          float v = s_scale[row] * acc[0][m][r];
+          if (id >= 0 && id < a.ad.L)
+            v += adapter_dot(s_hx + row * a.ad.R, a.ad.B + ((int64_t)id * (16 * a.nbe) + n) * a.ad.R,
+                             a.ad.R);
+          a.y[row_m * (16 * a.nbe) + n] = f32_to_bf16_rne(v);
+        }
+      }
+  };
+
+  const int64_t eb = (int64_t)w.expert * a.nbe;  // the expert's first block
+  for (int s0 = gb; s0 < ge; s0 += a.sg) {
+    const int sgn = min(a.sg, ge - s0);
+    const bool last = s0 + sgn == ge;
+    // this wavefront's groups of the slice, and its run of units: nc columns
+    // of them (several columns only when they cover all groups, so the run
+    // is contiguous in the packed planes)
+    const int k0 = sgn * kwi / KW, kn = sgn * (kwi + 1) / KW - k0;
+    const int T = kn * nc;
+    __amdgpu_buffer_rsrc_t rc[NBK], rs[NBK], rz[NBK];
+#pragma unroll
+    for (int b = 0; b < NBK; ++b) {
+      const int64_t b0 = (eb + b * a.cols + (nc > 0 ? c0 : 0)) * G + s0 + k0;
+      rc[b] = rsrc_of(a.codes + b0 * kBlockBytes, (int64_t)T * kBlockBytes);
+      rs[b] = rsrc_of(a.scales + b0 * 16, (int64_t)T * 64);
+      rz[b] = rsrc_of(a.zeros + b0 * kZeroBlockBytes, (int64_t)T * kZeroBlockBytes);
+    }
+    v4u_rows d[D][NBK];
+    float s[D][NBK];
+    uint32_t z[D][NBK];
+    // past the run: no memory request, zeros
+    auto load = [&](int i, int t) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < NBK; ++b) {
+        d[i][b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], 16 * lane, (unsigned)uniform(t * kBlockBytes),
+                                                        kNontemporal);
+        s[i][b] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rs[b], 4 * r16, (unsigned)uniform(t * 64), 0));
+        z[i][b] = __builtin_amdgcn_raw_buffer_load_b8(rz[b], r16 >> 1, (unsigned)uniform(t * kZeroBlockBytes), 0);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      load(i, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // ---- stage the activations
+    __syncthreads();  // the row tables; and the last slice's reads are done
+    if constexpr (ACT == kCodes) {
+      const int n = MT * sgn * 128;
+#pragma unroll 4
+      for (int c = tid; c < n; c += kThreads) {
+        const int q = c >> 7, m = q / sgn, g = q - m * sgn;
+        const int h = (c >> 6) & 1, row = 16 * m + r16;
+        if (row < w.rows)
+          *reinterpret_cast<v4u_rows*>(smem + c * 16) = *reinterpret_cast<const v4u_rows*>(
+              a.qa + (int64_t)s_src[row] * a.K + (s0 + g) * kGroup + 64 * h + 16 * j);
+      }
+    } else {
+      // quantise the rows here (the rule of w4a8_quant_act): 2^rl wavefronts
+      // per row, so a lone row is not left to one of them
+      using RR = RawRow<ACT>;
+      const int rl = w.rows <= 1 ? 3 : w.rows <= 2 ? 2 : w.rows <= 4 ? 1 : 0;
+      const int wpr = 1 << rl, nch = a.K / 8, sub = (wave & (wpr - 1)) * 64 + lane;
+      for (int row0 = 0; row0 < w.rows; row0 += kWaves >> rl) {
+        const int row = row0 + (wave >> rl);
+        const bool live = row < w.rows;
+        const uint8_t* xr =
+            static_cast<const uint8_t*>(a.x) + (int64_t)(live ? s_src[row] : 0) * a.K * RR::kBytes;
+        float amax = 0.0f;
+        if (live)
+          for (int ch = sub; ch < nch; ch += 64 * wpr) {
+            v4u_rows raw[RR::kLoads];
+            RR::load(xr, ch, raw);
+            float v[8];
+            RR::widen(raw, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+          }
+        amax = wave_max64(amax);
+        if (wpr > 1) {  // one pass of the row loop: at most 8 / wpr rows
+          if (lane == 0) s_max[wave] = amax;
+          __syncthreads();
+          for (int i = 0; i < wpr; ++i) amax = fmaxf(amax, s_max[(wave & ~(wpr - 1)) + i]);
+        }
+        if (live) {
+          const float scale = amax / 127.0f, inv = 1.0f / scale;
+          if (sub == 0) s_scale[row] = scale;
+          for (int ch = sub; ch < nch; ch += 64 * wpr) {
+            v4u_rows raw[RR::kLoads];
+            RR::load(xr, ch, raw);
+            float v[8];
+            RR::widen(raw, v);
+            const uint2 codes = amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+            const int g = ch >> 4, h = (ch >> 3) & 1, jj = (ch >> 1) & 3;
+            const int at = ONE ? ((g * 2 + h) * 4 + jj) * 16
+                               : (((row >> 4) * sgn + g) * 2 + h) * 1024 + (16 * jj + (row & 15)) * 16;
+            *reinterpret_cast<uint2*>(smem + at + 8 * (ch & 1)) = codes;
+          }
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- stream the run
+    int g = 0, c = c0;
+    for (int tb = 0; tb < T; tb += D) {
+#pragma unroll
+      for (int i = 0; i < D; ++i) {
+        if (tb + i < T) {
+          v4i lo[NBK], hi[NBK];
+          float sc[NBK];
+#pragma unroll
+          for (int b = 0; b < NBK; ++b) {
+            const uint32_t zz = ((z[i][b] >> (4 * (r16 & 1))) & 0xFu) * 0x01010101u;
+            unpack_unit(d[i][b], zz, lo[b], hi[b]);
+            sc[b] = s[i][b];
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint8_t* frag = ONE ? smem + (k0 + g) * 128 + 16 * j
+                                      : smem + (m * sgn + k0 + g) * 2048 + 16 * lane;
+            const v4i a0 = *reinterpret_cast<const v4i*>(frag);
+            const v4i a1 = *reinterpret_cast<const v4i*>(frag + (ONE ? 64 : 1024));
+#pragma unroll
+            for (int b = 0; b < NBK; ++b) {
+              v4i p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, lo[b], kBiasSeed, 0, 0, 0);
+              p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, hi[b], p, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[b][m][r] += sc[b] * unbias(p[r]);
+            }
+          }
+          if (++g == kn) {
+            g = 0;
+            if (last && a.kw == 0) {
+              emit(c);
+              ++c;
+#pragma unroll
+              for (int b = 0; b < NBK; ++b)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) acc[b][m][r] = 0.0f;
+            }
+          }
+        }
+        load(i, tb + i + D);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if (a.kw == 0) return;
+
+  // the wavefronts of a column, summed in group order
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem) + cw * KW * (NBK * MT * 256);
+#pragma unroll
+  for (int b = 0; b < NBK; ++b)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        red[kwi * (NBK * MT * 256) + ((b * MT + m) * 4 + r) * 64 + lane] = acc[b][m][r];
+  __syncthreads();
+  if (kwi != 0 || nc == 0) return;
+#pragma unroll
+  for (int b = 0; b < NBK; ++b)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        for (int k = 1; k < KW; ++k)
+          acc[b][m][r] += red[k * (NBK * MT * 256) + ((b * MT + m) * 4 + r) * 64 + lane];
+  emit(c0);
+}
+
+// ----------------------------------------------------------- many rows
+//
+// 256 rows x 256 channels per workgroup of eight wavefronts (64 x 128 each).
+// Per group of 128 inputs the activation tile (32 KiB) goes from memory
+// straight into LDS, the 16 code blocks are unpacked once to q - z bytes in
+// LDS, both double-buffered, one group ahead of the products.  The rows are
+// gathered: the LDS-direct loads take a byte offset per lane.  Rows past the
+// tile read as zeros without a request.
+//
+// The wavefronts lie 4 x 2 over the tile with rows (wave / 2) * 64, so that
+// wavefronts w and w + 4, which share a SIMD, hold rows 128 apart: a tile of at most
+// 128 rows leaves one working wavefront on every SIMD and takes about half
+// the time, as the others skip the products.
+//
+// kSwiglu: the 256 channels are 128 gate channels and their 128 up channels;
+// a wavefront's 8 blocks are 4 gate blocks and the matching up blocks.
+constexpr int kABytes = kTileRows * kGroup;                // [256][128], chunks swizzled by row
+constexpr int kBBytes = (kTileCols / 16) * 2 * kBlockBytes;  // [16][2][64 lanes][16 B]
+constexpr int kBufBytes = kABytes + kBBytes + kTileCols * 4;
+constexpr int kBOff = kABytes, kSOff = kABytes + kBBytes;
+
+__device__ __forceinline__ int a_chunk(int r, int c) { return c ^ (r & 7); }
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreads)
+rows_tile_kernel(RowsArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2][kBufBytes];
+  __shared__ int s_pair[kTileRows];
+  __shared__ float s_scale[kTileRows];
+  Where w;
+  if (!locate<kTileRows>(a, w)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int r16 = lane & 15, j = lane >> 4;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int G = a.K / kGroup;
+  const int gb = G * blockIdx.y / gridDim.y, ge = G * (blockIdx.y + 1) / gridDim.y;
+  const bool works = wm * 64 < w.rows;
+  const int NB = a.nbe;
+
+  for (int i = tid; i < w.rows; i += kThreads) {
+    const int p = pair_of(a, w, i);
+    s_pair[i] = p;
+    float sc = OUT == kSplit ? 1.0f : a.sa[p / a.div];
+    if constexpr (OUT == kParts) sc *= a.pw[p];
+    s_scale[i] = sc;
+  }
+
+  // block q (0..15) of the tile: wavefront column q / 8, its column u = q % 8
+  auto block_of = [&](int q) __attribute__((always_inline)) {
+    if constexpr (OUT == kSwiglu) {
+      const int u = q & 7;
+      return (u >> 2) * a.cols + w.strip * 8 + (q >> 3) * 4 + (u & 3);
+    } else {
+      return min(w.strip * 16 + q, NB - 1);  // past the end: columns that are never stored
+    }
+  };
+  const int64_t eb = (int64_t)w.expert * NB;
+  const uint8_t* codes = a.codes + eb * G * kBlockBytes;
+  const uint8_t* zeros = a.zeros + eb * G * kZeroBlockBytes;
+  const float* scales = a.scales + eb * G * 16;
+
+  uint32_t oa[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * (4 * wave + i) + (lane >> 3);
+    oa[i] = r < w.rows ? (uint32_t)(pair_of(a, w, r) / a.div) * a.K + 16 * a_chunk(r, lane & 7) : kOob;
+  }
+  const int b0 = block_of(wave), b1 = block_of(wave + 8), bs = block_of((tid >> 4) & 15);
+  const uint32_t ob[2] = {(uint32_t)b0 * G * kBlockBytes + lane * 16, (uint32_t)b1 * G * kBlockBytes + lane * 16};
+  const uint32_t oz[2] = {(uint32_t)b0 * G * 8 + (r16 >> 1), (uint32_t)b1 * G * 8 + (r16 >> 1)};
+  const uint32_t os = (uint32_t)bs * G * 16 + r16;
+  const int zshift = (lane & 1) * 4;
+  const __amdgpu_buffer_rsrc_t rqa = rsrc_of(a.qa, a.src_rows * a.K);
+
+  v4u_rows sb[2];
+  uint32_t sz[2];
+  float ss;
+  auto dma = [&](uint8_t* buf, int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rqa, (__attribute__((address_space(3))) void*)(buf + (4 * wave + i) * 1024), 16, oa[i],
+          (unsigned)uniform(g * kGroup), 0, 0);
+  };
+  auto fetch = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      sb[k] = *reinterpret_cast<const v4u_rows*>(codes + (int64_t)g * kBlockBytes + ob[k]);
+      sz[k] = (zeros + g * kZeroBlockBytes)[oz[k]];
+    }
+    ss = (scales + g * 16)[os];
+  };
+  auto store_block = [&](uint8_t* buf, int k) __attribute__((always_inline)) {
+    v4i lo, hi;
+    unpack_unit(sb[k], ((sz[k] >> zshift) & 0xFu) * 0x01010101u, lo, hi);
+    uint8_t* at = buf + kBOff + (wave + 8 * k) * 2 * kBlockBytes + lane * 16;
+    *reinterpret_cast<v4i*>(at) = lo;
+    *reinterpret_cast<v4i*>(at + kBlockBytes) = hi;
+  };
+  // scales as [16 channels][16 blocks]: a lane's eight are contiguous
+  auto store_scale = [&](uint8_t* buf) __attribute__((always_inline)) {
+    reinterpret_cast<float*>(buf + kSOff)[r16 * 16 + ((tid >> 4) & 15)] = ss;
+  };
+
+  float acc[4][8][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][u][r] = 0.0f;
+
+  // One group: per 16 x 16 tile an MFMA pair and, two tiles later, its
+  // rescale; the next group's blocks are unpacked between them.
+  auto compute = [&](const uint8_t* buf, uint8_t* next) __attribute__((always_inline)) {
+    v4i a0[4], a1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* arow = buf + (wm * 64 + i * 16 + r16) * kGroup;
+      a0[i] = *reinterpret_cast<const v4i*>(arow + 16 * a_chunk(r16, j));
+      a1[i] = *reinterpret_cast<const v4i*>(arow + 16 * a_chunk(r16, 4 + j));
+    }
+    float sv[8];
+    const float* srow = reinterpret_cast<const float*>(buf + kSOff) + r16 * 16 + wn * 8;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const v4i t = *reinterpret_cast<const v4i*>(srow + 4 * q);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sv[4 * q + u] = __int_as_float(t[u]);
+    }
+    v4i q0[8], q1[8];
+    auto load_b = [&](int u) __attribute__((always_inline)) {
+      const uint8_t* at = buf + kBOff + (wn * 8 + u) * 2 * kBlockBytes + lane * 16;
+      q0[u] = *reinterpret_cast<const v4i*>(at);
+      q1[u] = *reinterpret_cast<const v4i*>(at + kBlockBytes);
+    };
+    load_b(0);
+    v4i p[32];
+#pragma unroll
+    for (int t = 0; t < 34; ++t) {
+      if (t < 32) {
+        const int u = t >> 2, i = t & 3;
+        if (i == 0 && u + 1 < 8) load_b(u + 1);
+        if (next && t == 16) store_block(next, 0);
+        if (next && t == 22) store_block(next, 1);
+        if (next && t == 28) store_scale(next);
+        p[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0[i], q0[u], kBiasSeed, 0, 0, 0);
+        p[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1[i], q1[u], p[t], 0, 0, 0);
+      }
+      if (t >= 2) {
+        const int e = t - 2, u = e >> 2, i = e & 3;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][u][r] += sv[u] * unbias(p[e][r]);
+        if (t + 1 < 32) {  // keeps pairs and rescales interleaved (no instruction)
+          const int in = (t + 1) & 3;
+          asm volatile("" : "+v"(a0[in]) : "v"(acc[i][u][0]), "v"(acc[i][u][1]), "v"(acc[i][u][2]),
+                       "v"(acc[i][u][3]));
+        }
+      }
+    }
+  };
+
+  dma(smem[0], gb);
+  fetch(gb);
+  store_block(smem[0], 0);
+  store_block(smem[0], 1);
+  store_scale(smem[0]);
+  __syncthreads();
+  if (!works) {  // feeds the others; the same barriers
+    for (int g = gb; g < ge; ++g) {
+      if (g + 1 < ge) {
+        uint8_t* next = smem[(g - gb + 1) & 1];
+        dma(next, g + 1);
+        fetch(g + 1);
+        store_block(next, 0);
+        store_block(next, 1);
+        store_scale(next);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  for (int g = gb; g < ge; g += 2) {
+    if (g + 1 < ge) {  // buffer 1 was last read before the previous barrier
+      dma(smem[1], g + 1);
+      fetch(g + 1);
+    }
+    compute(smem[0], g + 1 < ge ? smem[1] : nullptr);
+    __syncthreads();
+    if (g + 1 >= ge) break;
+    if (g + 2 < ge) {
+      dma(smem[0], g + 2);
+      fetch(g + 2);
+    }
+    compute(smem[1], g + 2 < ge ? smem[0] : nullptr);
+    __syncthreads();
+  }
+
+  if constexpr (OUT == kAdapt) {
+    // sums scaled, then each adapter's product added on the bf16 matrix
+    // cores: per adapter present in a 16-row fragment, the scaled x A^T of its
+    // rows as two bf16 parts (16 significant bits) against B.  The product is
+    // made apart and added to the adapter's own rows only, so what B holds
+    // (an infinity, a NaN) reaches no other row.  The int8 and bf16 products
+    // share one result layout.
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = wm * 64 + i * 16 + 4 * j + r;
+        const float s = row < w.rows ? s_scale[row] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc[i][u][r] *= s;
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = wm * 64 + i * 16 + r16;
+      const int64_t m = w.first + row;
+      const int id = row < w.rows ? a.ad.ids[m] : -1;
+      const bool has = id >= 0 && id < a.ad.L;
+      uint64_t todo = __ballot(has) & 0xFFFFull;
+      while (todo) {
+        const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const bool mine = has && id == l;
+        const uint64_t rows = __ballot(mine) & 0xFFFFull;
+        todo &= ~rows;
+        const float sl = a.ad.scale[l];
+        for (int r0 = 0; r0 < a.ad.R; r0 += 32) {
+          const int rr = r0 + 8 * j;  // this lane's eight of the adapter's rank
+          v4i ah = {0, 0, 0, 0}, al = {0, 0, 0, 0};
+          if (mine && rr < a.ad.R) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float v = adapter_sum(a.ad, a.M, m, rr + e, sl);
+              const uint32_t hb = f32_to_bf16_rne(v);
+              const uint32_t lb = f32_to_bf16_rne(v - __uint_as_float(hb << 16));
+              ah[e >> 1] |= (int)(hb << (16 * (e & 1)));
+              al[e >> 1] |= (int)(lb << (16 * (e & 1)));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int nb = min(w.strip * 16 + wn * 8 + u, NB - 1);
+            v4i bv = {0, 0, 0, 0};
+            if (rr < a.ad.R)
+              bv = *reinterpret_cast<const v4i*>(
+                  a.ad.B + (((int64_t)l * NB + nb) * 16 + r16) * a.ad.R + rr);
+            v4f_rows c = {0.f, 0.f, 0.f, 0.f};
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, ah),
+                                                        __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, al),
+                                                        __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][u][r] += (rows >> (4 * j + r)) & 1 ? c[r] : 0.0f;
+          }
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = wm * 64 + i * 16 + 4 * j + r;
+      if (row >= w.rows) continue;
+      const float s = s_scale[row];
+      const int64_t p = s_pair[row];
+      if constexpr (OUT == kSwiglu) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          a.h[p * (16 * a.cols) + 16 * (w.strip * 8 + wn * 4 + u) + r16] =
+              f32_to_bf16_rne(silu_mul(s * acc[i][u][r], s * acc[i][u + 4][r]));
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int nb = w.strip * 16 + wn * 8 + u;
+          if (nb >= NB) continue;
+          const int64_t n = 16 * nb + r16;
+          if constexpr (OUT == kParts)
+            a.parts[p * (16 * NB) + n] = s * acc[i][u][r];
+          else if constexpr (OUT == kSplit)
+            a.parts[((int64_t)blockIdx.y * a.M + p) * (16 * NB) + n] = acc[i][u][r];
+          else
+            a.y[p * (16 * NB) + n] = f32_to_bf16_rne(acc[i][u][r]);
+        }
+      }
+    }
+}
+
+template <int MT, bool ONE, int ACT, int OUT>
+hipError_t stream_launch(const RowsArgs& a, int64_t blocks, int ksplit, hipStream_t st) {
+  const size_t groups = (size_t)(a.sg);
+  size_t lds = ONE ? groups * 128 : groups * MT * 2048;
+  const size_t red = a.kw ? (size_t)kWaves * (OUT == kSwiglu ? 2 : 1) * MT * 1024 : 0;
+  if (red > lds) lds = red;
+  hipLaunchKernelGGL((rows_stream_kernel<MT, ONE, ACT, OUT>), dim3((unsigned)blocks, (unsigned)ksplit),
+                     dim3(kThreads), lds, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rows_stream(const RowsArgs& a, int mt, int act, int out, int64_t blocks,
+                              int ksplit, hipStream_t st) {
+#define ROWS_CASE(MTV, ONEV, ACTV, OUTV) \
+  if (mt == MTV && (a.kind == kDirect) == ONEV && act == ACTV && out == OUTV) \
+    return stream_launch<MTV, ONEV, ACTV, OUTV>(a, blocks, ksplit, st);
+  ROWS_CASE(1, true, kRawBf16, kSwiglu)
+  ROWS_CASE(1, true, kRawF32, kSwiglu)
+  ROWS_CASE(1, false, kCodes, kSwiglu)
+  ROWS_CASE(2, false, kCodes, kSwiglu)
+  ROWS_CASE(4, false, kCodes, kSwiglu)
+  ROWS_CASE(1, false, kRawBf16, kParts)
+  ROWS_CASE(1, false, kCodes, kParts)
+  ROWS_CASE(2, false, kCodes, kParts)
+  ROWS_CASE(4, false, kCodes, kParts)
+  ROWS_CASE(1, false, kCodes, kSplit)
+  ROWS_CASE(2, false, kCodes, kSplit)
+  ROWS_CASE(3, false, kCodes, kSplit)
+  ROWS_CASE(4, false, kCodes, kSplit)
+  ROWS_CASE(1, false, kCodes, kAdapt)
+#undef ROWS_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_rows_tile(const RowsArgs& a, int out, int64_t blocks, int ksplit, hipStream_t st) {
+  const dim3 grid((unsigned)blocks, (unsigned)ksplit), block(kThreads);
+  if (out == kSwiglu)
+    hipLaunchKernelGGL((rows_tile_kernel<kSwiglu>), grid, block, 0, st, a);
+  else if (out == kParts)
+    hipLaunchKernelGGL((rows_tile_kernel<kParts>), grid, block, 0, st, a);
+  else if (out == kSplit)
+    hipLaunchKernelGGL((rows_tile_kernel<kSplit>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((rows_tile_kernel<kAdapt>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace w4a8
