@@ -197,14 +197,25 @@ combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids, int
   const int64_t m = t / per;
   const int n = (int)(t - m * per) * 8;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-  for (int s = 0; s < k; ++s) {
-    const int e = ids[m * k + s];
-    if (e < 0 || e >= E) continue;
-    const float4* p = reinterpret_cast<const float4*>(parts + (m * k + s) * N + n);
-    const float4 a = p[0], b = p[1];
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  constexpr int S = 4;  // slots whose loads go out together
+  for (int s0 = 0; s0 < k; s0 += S) {
+    float4 a[S], b[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int64_t q = m * k + s0 + i;
+      const int e = s0 + i < k ? ids[q] : -1;
+      a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e >= 0 && e < E) {
+        const float4* p = reinterpret_cast<const float4*>(parts + q * N + n);
+        a[i] = p[0];
+        b[i] = p[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      v[0] += a[i].x; v[1] += a[i].y; v[2] += a[i].z; v[3] += a[i].w;
+      v[4] += b[i].x; v[5] += b[i].y; v[6] += b[i].z; v[7] += b[i].w;
+    }
   }
   uint32_t o[4];
 #pragma unroll
@@ -285,7 +296,7 @@ static hipError_t moe_direct(const MoeArgs& m, const MoePlan& p, hipStream_t st)
   a.strips = a.cols;
   a.sg = (int)(m.K / kGroup);
   a.h = h;
-  hipError_t e = launch_rows_stream(a, 1, m.x_dtype == 0 ? kRawBf16 : kRawF32, kSwiglu,
+  hipError_t e = launch_rows_stream(a, 1, true, m.x_dtype == 0 ? kRawBf16 : kRawF32, kSwiglu,
                                     m.M * m.k * a.strips, 1, st);
   if (e != hipSuccess) return e;
   RowsArgs d{};
@@ -362,7 +373,7 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
     a.ncol = 1;
     a.strips = (a.cols + 7) / 8;
     a.sg = slice(G);
-    e = launch_rows_stream(a, mt, kCodes, kSwiglu, max_tiles * a.strips, 1, st);
+    e = launch_rows_stream(a, mt, false, kCodes, kSwiglu, max_tiles * a.strips, 1, st);
   }
   if (e != hipSuccess) return e;
 
@@ -397,7 +408,7 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
     d.ncol = d.sg == GI ? (24 + GI - 1) / GI : 1;
     const int per = 8 * d.ncol;
     d.strips = (d.cols + per - 1) / per;
-    e = launch_rows_stream(d, mt, raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st);
+    e = launch_rows_stream(d, mt, false, raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st);
   }
   if (e != hipSuccess) return e;
   const int64_t total = m.M * (m.K / 8);

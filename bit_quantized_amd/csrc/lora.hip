@@ -252,10 +252,10 @@ hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {
     a.kw = p.kw;
     a.ncol = 1;
     const int cw = 8 >> p.kw, per = (G + p.ksplit - 1) / p.ksplit;
-    const int most = 32 / p.mt, n = (per + most - 1) / most;
+    const int most = l.M == 1 ? 64 : 32 / p.mt, n = (per + most - 1) / most;
     a.strips = (a.cols + cw - 1) / cw;
     a.sg = (per + n - 1) / n;
-    e = launch_rows_stream(a, p.mt, kCodes, parts ? kSplit : kAdapt, a.strips, p.ksplit, st);
+    e = launch_rows_stream(a, p.mt, l.M == 1, kCodes, parts ? kSplit : kAdapt, a.strips, p.ksplit, st);
   } else {
     const int64_t tiles = (l.M + kTileRows - 1) / kTileRows;
     a.strips = (a.nbe + 15) / 16;

@@ -244,15 +244,24 @@ __device__ __forceinline__ float adapter_dot(const float* hx, const uint16_t* br
 }
 
 // Row m's scaled adapter sums: scale * sum over the slices of hx[.][m][r].
+// Eight slices' loads go out together.
 __device__ __forceinline__ float adapter_sum(const AdaptArgs& ad, int64_t M, int64_t m, int r, float s) {
+  const float* p = ad.hx + m * ad.R + r;
+  const int64_t step = M * ad.R;
   float v = 0.0f;
-  for (int k = 0; k < ad.slices; ++k) v += ad.hx[((int64_t)k * M + m) * ad.R + r];
+  for (int k = 0; k < ad.slices; k += 8) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = k + i < ad.slices ? p[(k + i) * step] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += t[i];
+  }
   return s * v;
 }
 
-// Launchers (rows.hip).  `raw`: RowAct of the input; mt: 16-row tiles per
-// workgroup (1..4) of the weight-streaming kernel.
-hipError_t launch_rows_stream(const RowsArgs& a, int mt, int act, int out, int64_t blocks,
+// Launchers (rows.hip).  act: RowAct of the input; mt: 16-row tiles per
+// workgroup (1..4) of the weight-streaming kernel; one: tiles of a single row.
+hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int out, int64_t blocks,
                               int ksplit, hipStream_t st);
 hipError_t launch_rows_tile(const RowsArgs& a, int out, int64_t blocks, int ksplit, hipStream_t st);
 // Rows per workgroup of launch_rows_tile, and its output channels.

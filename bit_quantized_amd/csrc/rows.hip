@@ -30,14 +30,29 @@ constexpr int kWaves = kThreads / 64;
 // written: an int8 product of any bytes is finite and belongs to no output.
 // ONE: the tile is a single row, kept as [groups][2][4][16 B] and read by all
 // rows of the operand.
+// Memory order: the activations' loads go first, then the first D weight
+// units, then whatever else the tile needs, so that the activations (waited
+// for first) do not queue behind the weights, and the weights stay in flight
+// across the barriers, which wait for LDS only.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+constexpr int kStageChunks = 8;  // 16-byte pieces of activations a thread stages per slice
+// Until at most N of this wavefront's memory requests are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "six bits of count");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
 template <int MT, bool ONE, int ACT, int OUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, MT > 2 || OUT == kAdapt ? 2 : 4)
 rows_stream_kernel(RowsArgs a) {
-  constexpr int BM = 16 * MT;
+  constexpr int BM = ONE ? 1 : 16 * MT;
   constexpr int NBK = OUT == kSwiglu ? 2 : 1;  // blocks per column
   constexpr int D = NBK == 2 ? 4 : 8;          // columns' units in flight
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int s_pair[BM], s_src[BM];
+  __shared__ int s_pair[BM];
   __shared__ float s_scale[BM], s_max[kWaves];
   __shared__ float s_hx[OUT == kAdapt ? BM * kMaxRank : 1];  // scaled x A^T of the rows
 
@@ -49,23 +64,23 @@ rows_stream_kernel(RowsArgs a) {
   const int KW = 1 << a.kw, CW = kWaves >> a.kw;
   const int kwi = wave & (KW - 1), cw = wave >> a.kw;
   const int c0 = (w.strip * CW + cw) * a.ncol;
-  const int nc = min(a.ncol, a.cols - c0) > 0 ? min(a.ncol, a.cols - c0) : 0;
+  const int nc = max(min(a.ncol, a.cols - c0), 0);
   const int gb = G * blockIdx.y / gridDim.y, ge = G * (blockIdx.y + 1) / gridDim.y;
 
-  // the tile's rows
+  // the source rows this thread stages (kCodes: rows 16 m + r16)
+  int src[MT];
+  if constexpr (ACT == kCodes) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = 16 * m + r16;
+      src[m] = ONE ? pair_of(a, w, 0) / a.div : row < w.rows ? pair_of(a, w, row) / a.div : -1;
+    }
+  }
+  const __amdgpu_buffer_rsrc_t rqa = rsrc_of(a.qa, ACT == kCodes ? a.src_rows * a.K : 0);
   if (tid < w.rows) {
     const int p = pair_of(a, w, tid);
-    const int src = p / a.div;
     s_pair[tid] = p;
-    s_src[tid] = src;
-    if constexpr (ACT == kCodes) s_scale[tid] = a.sa[src];
-  }
-  if constexpr (OUT == kAdapt) {
-    for (int i = tid; i < w.rows * a.ad.R; i += kThreads) {
-      const int row = i / a.ad.R, id = a.ad.ids[w.first + row];
-      if (id >= 0 && id < a.ad.L)
-        s_hx[i] = adapter_sum(a.ad, a.M, w.first + row, i - row * a.ad.R, a.ad.scale[id]);
-    }
+    if constexpr (ACT == kCodes) s_scale[tid] = a.sa[p / a.div];
   }
 
   float acc[NBK][MT][4];
@@ -106,13 +121,60 @@ rows_stream_kernel(RowsArgs a) {
       }
   };
 
+  // raw activations: 2^rl wavefronts per row, so that a lone row is not left
+  // to one of them; the first rows' chunks are held in registers
+  using RR = RawRow<ACT == kCodes ? kRawBf16 : ACT>;
+  constexpr int HC = ACT == kRawBf16 ? 2 : 1;
+  const int rl = w.rows <= 1 ? 3 : w.rows <= 2 ? 2 : w.rows <= 4 ? 1 : 0;
+  const int wpr = 1 << rl, nch = a.K / 8, sub = (wave & (wpr - 1)) * 64 + lane, step = 64 * wpr;
+  auto raw_row = [&](int row) __attribute__((always_inline)) {
+    return static_cast<const uint8_t*>(a.x) + (int64_t)(pair_of(a, w, row) / a.div) * a.K * RR::kBytes;
+  };
+
   const int64_t eb = (int64_t)w.expert * a.nbe;  // the expert's first block
   for (int s0 = gb; s0 < ge; s0 += a.sg) {
     const int sgn = min(a.sg, ge - s0);
     const bool last = s0 + sgn == ge;
-    // this wavefront's groups of the slice, and its run of units: nc columns
-    // of them (several columns only when they cover all groups, so the run
-    // is contiguous in the packed planes)
+    // ---- the activations' loads
+    v4u_rows xh[HC][RR::kLoads];
+    if constexpr (ACT == kCodes) {
+      // straight into LDS, 1 KiB per wavefront and load (rows past the tile:
+      // zeros, no request); the LDS has to be free
+      if (s0 != gb) lds_barrier();
+#pragma unroll
+      for (int i = 0; i < (ONE ? 1 : kStageChunks); ++i) {
+        const int c = tid + i * kThreads;
+        int off = kOob;
+        if constexpr (ONE) {
+          if (c < sgn * 8) off = src[0] * a.K + s0 * kGroup + 16 * c;
+        } else {
+          const int q = c >> 7, h = (c >> 6) & 1;
+          int m = 0, sr = src[0];
+#pragma unroll
+          for (int t = 1; t < MT; ++t) {
+            m += q >= t * sgn;
+            sr = m == t ? src[t] : sr;
+          }
+          if (sr >= 0) off = sr * a.K + (s0 + q - m * sgn) * kGroup + 64 * h + 16 * j;
+        }
+        if (uniform(c) < (ONE ? sgn * 8 : MT * sgn * 128))
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rqa, (__attribute__((address_space(3))) void*)(smem + uniform(c) * 16), 16, off, 0, 0, 0);
+      }
+    } else {
+      const int row = wave >> rl;
+      if (row < w.rows) {
+        const uint8_t* xr = raw_row(row);
+#pragma unroll
+        for (int i = 0; i < HC; ++i)
+          if (sub + i * step < nch) RR::load(xr, sub + i * step, xh[i]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- the first weight units.  This wavefront's groups of the slice, and
+    // its run of units: nc columns of them (several columns only when they
+    // cover all groups, so the run is contiguous in the packed planes)
     const int k0 = sgn * kwi / KW, kn = sgn * (kwi + 1) / KW - k0;
     const int T = kn * nc;
     __amdgpu_buffer_rsrc_t rc[NBK], rs[NBK], rz[NBK];
@@ -143,63 +205,74 @@ rows_stream_kernel(RowsArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
 
-    // ---- stage the activations
-    __syncthreads();  // the row tables; and the last slice's reads are done
+    // ---- activations -> LDS
     if constexpr (ACT == kCodes) {
-      const int n = MT * sgn * 128;
-#pragma unroll 4
-      for (int c = tid; c < n; c += kThreads) {
-        const int q = c >> 7, m = q / sgn, g = q - m * sgn;
-        const int h = (c >> 6) & 1, row = 16 * m + r16;
-        if (row < w.rows)
-          *reinterpret_cast<v4u_rows*>(smem + c * 16) = *reinterpret_cast<const v4u_rows*>(
-              a.qa + (int64_t)s_src[row] * a.K + (s0 + g) * kGroup + 64 * h + 16 * j);
-      }
+      wait_loads<3 * NBK * D>();
     } else {
-      // quantise the rows here (the rule of w4a8_quant_act): 2^rl wavefronts
-      // per row, so a lone row is not left to one of them
-      using RR = RawRow<ACT>;
-      const int rl = w.rows <= 1 ? 3 : w.rows <= 2 ? 2 : w.rows <= 4 ? 1 : 0;
-      const int wpr = 1 << rl, nch = a.K / 8, sub = (wave & (wpr - 1)) * 64 + lane;
+      // quantised here (the rule of w4a8_quant_act)
       for (int row0 = 0; row0 < w.rows; row0 += kWaves >> rl) {
         const int row = row0 + (wave >> rl);
-        const bool live = row < w.rows;
-        const uint8_t* xr =
-            static_cast<const uint8_t*>(a.x) + (int64_t)(live ? s_src[row] : 0) * a.K * RR::kBytes;
+        const bool live = row < w.rows, held = row0 == 0;
+        const uint8_t* xr = raw_row(live ? row : 0);
         float amax = 0.0f;
-        if (live)
-          for (int ch = sub; ch < nch; ch += 64 * wpr) {
-            v4u_rows raw[RR::kLoads];
-            RR::load(xr, ch, raw);
-            float v[8];
-            RR::widen(raw, v);
+        auto most = [&](const v4u_rows* r) __attribute__((always_inline)) {
+          float v[8];
+          RR::widen(r, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        };
+        if (live) {
+          if (held) {
+#pragma unroll
+            for (int i = 0; i < HC; ++i)
+              if (sub + i * step < nch) most(xh[i]);
           }
+          for (int ch = sub + (held ? HC * step : 0); ch < nch; ch += step) {
+            v4u_rows r[RR::kLoads];
+            RR::load(xr, ch, r);
+            most(r);
+          }
+        }
         amax = wave_max64(amax);
-        if (wpr > 1) {  // one pass of the row loop: at most 8 / wpr rows
+        if (wpr > 1) {  // (the only pass of the row loop: at most 8 / wpr rows)
           if (lane == 0) s_max[wave] = amax;
-          __syncthreads();
+          lds_barrier();
           for (int i = 0; i < wpr; ++i) amax = fmaxf(amax, s_max[(wave & ~(wpr - 1)) + i]);
         }
         if (live) {
           const float scale = amax / 127.0f, inv = 1.0f / scale;
           if (sub == 0) s_scale[row] = scale;
-          for (int ch = sub; ch < nch; ch += 64 * wpr) {
-            v4u_rows raw[RR::kLoads];
-            RR::load(xr, ch, raw);
+          auto put = [&](int ch, const v4u_rows* r) __attribute__((always_inline)) {
             float v[8];
-            RR::widen(raw, v);
+            RR::widen(r, v);
             const uint2 codes = amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
             const int g = ch >> 4, h = (ch >> 3) & 1, jj = (ch >> 1) & 3;
             const int at = ONE ? ((g * 2 + h) * 4 + jj) * 16
                                : (((row >> 4) * sgn + g) * 2 + h) * 1024 + (16 * jj + (row & 15)) * 16;
             *reinterpret_cast<uint2*>(smem + at + 8 * (ch & 1)) = codes;
+          };
+          if (held) {
+#pragma unroll
+            for (int i = 0; i < HC; ++i)
+              if (sub + i * step < nch) put(sub + i * step, xh[i]);
+          }
+          for (int ch = sub + (held ? HC * step : 0); ch < nch; ch += step) {
+            v4u_rows r[RR::kLoads];
+            RR::load(xr, ch, r);
+            put(ch, r);
           }
         }
       }
     }
-    __syncthreads();
+    if constexpr (OUT == kAdapt) {
+      if (s0 == gb)
+        for (int i = tid; i < w.rows * a.ad.R; i += kThreads) {
+          const int row = i / a.ad.R, id = a.ad.ids[w.first + row];
+          if (id >= 0 && id < a.ad.L)
+            s_hx[i] = adapter_sum(a.ad, a.M, w.first + row, i - row * a.ad.R, a.ad.scale[id]);
+        }
+    }
+    lds_barrier();
 
     // ---- stream the run
     int g = 0, c = c0;
@@ -251,7 +324,7 @@ rows_stream_kernel(RowsArgs a) {
   if (a.kw == 0) return;
 
   // the wavefronts of a column, summed in group order
-  __syncthreads();
+  lds_barrier();
   float* red = reinterpret_cast<float*>(smem) + cw * KW * (NBK * MT * 256);
 #pragma unroll
   for (int b = 0; b < NBK; ++b)
@@ -260,7 +333,7 @@ rows_stream_kernel(RowsArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         red[kwi * (NBK * MT * 256) + ((b * MT + m) * 4 + r) * 64 + lane] = acc[b][m][r];
-  __syncthreads();
+  lds_barrier();
   if (kwi != 0 || nc == 0) return;
 #pragma unroll
   for (int b = 0; b < NBK; ++b)
@@ -302,6 +375,7 @@ rows_tile_kernel(RowsArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[2][kBufBytes];
   __shared__ int s_pair[kTileRows];
   __shared__ float s_scale[kTileRows];
+  __shared__ int s_id[OUT == kAdapt ? kTileRows : 1];  // adapters of the rows, -1: none
   Where w;
   if (!locate<kTileRows>(a, w)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -318,6 +392,10 @@ rows_tile_kernel(RowsArgs a) {
     float sc = OUT == kSplit ? 1.0f : a.sa[p / a.div];
     if constexpr (OUT == kParts) sc *= a.pw[p];
     s_scale[i] = sc;
+    if constexpr (OUT == kAdapt) {
+      const int id = a.ad.ids[p];
+      s_id[i] = id >= 0 && id < a.ad.L ? id : -1;
+    }
   }
 
   // block q (0..15) of the tile: wavefront column q / 8, its column u = q % 8
@@ -453,9 +531,9 @@ rows_tile_kernel(RowsArgs a) {
       }
       __syncthreads();
     }
-    return;
+    if constexpr (OUT != kAdapt) return;
   }
-  for (int g = gb; g < ge; g += 2) {
+  if (works) for (int g = gb; g < ge; g += 2) {
     if (g + 1 < ge) {  // buffer 1 was last read before the previous barrier
       dma(smem[1], g + 1);
       fetch(g + 1);
@@ -487,50 +565,62 @@ rows_tile_kernel(RowsArgs a) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) acc[i][u][r] *= s;
       }
+    // The parts lie in the tile's LDS (the loop's last barrier has passed), 64
+    // ranks at a time: [2][256 rows][64 + 8], the pad keeping the rows of a
+    // fragment on different banks.
+    constexpr int kRanks = 64, kLd = kRanks + 8;
+    static_assert(2 * kTileRows * kLd * 2 <= 2 * kBufBytes, "fits the tile's buffers");
+    uint16_t* parts_lds = reinterpret_cast<uint16_t*>(&smem[0][0]);
+    for (int rb = 0; rb < a.ad.R; rb += kRanks) {
+      const int rn = min(kRanks, a.ad.R - rb);
+      if (rb) __syncthreads();  // the last ranks' reads are done
+      for (int q = tid; q < w.rows * rn; q += kThreads) {
+        const int row = q / rn, r = q - row * rn;
+        const int id = s_id[row];
+        if (id < 0) continue;
+        const float v = adapter_sum(a.ad, a.M, w.first + row, rb + r, a.ad.scale[id]);
+        const uint16_t hb = f32_to_bf16_rne(v);
+        parts_lds[row * kLd + r] = hb;
+        parts_lds[(kTileRows + row) * kLd + r] = f32_to_bf16_rne(v - __uint_as_float((uint32_t)hb << 16));
+      }
+      __syncthreads();
+      if (!works) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = wm * 64 + i * 16 + r16;
-      const int64_t m = w.first + row;
-      const int id = row < w.rows ? a.ad.ids[m] : -1;
-      const bool has = id >= 0 && id < a.ad.L;
-      uint64_t todo = __ballot(has) & 0xFFFFull;
-      while (todo) {
-        const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        const bool mine = has && id == l;
-        const uint64_t rows = __ballot(mine) & 0xFFFFull;
-        todo &= ~rows;
-        const float sl = a.ad.scale[l];
-        for (int r0 = 0; r0 < a.ad.R; r0 += 32) {
-          const int rr = r0 + 8 * j;  // this lane's eight of the adapter's rank
-          v4i ah = {0, 0, 0, 0}, al = {0, 0, 0, 0};
-          if (mine && rr < a.ad.R) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float v = adapter_sum(a.ad, a.M, m, rr + e, sl);
-              const uint32_t hb = f32_to_bf16_rne(v);
-              const uint32_t lb = f32_to_bf16_rne(v - __uint_as_float(hb << 16));
-              ah[e >> 1] |= (int)(hb << (16 * (e & 1)));
-              al[e >> 1] |= (int)(lb << (16 * (e & 1)));
+      for (int i = 0; i < 4; ++i) {
+        const int row = wm * 64 + i * 16 + r16;
+        const int id = row < w.rows ? s_id[row] : -1;
+        uint64_t todo = __ballot(id >= 0) & 0xFFFFull;
+        while (todo) {
+          const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+          const uint64_t rows = __ballot(id == l) & 0xFFFFull;
+          todo &= ~rows;
+          for (int r0 = 0; r0 < rn; r0 += 32) {
+            const int rr = r0 + 8 * j;  // this lane's eight ranks
+            v4i ah = {0, 0, 0, 0}, al = {0, 0, 0, 0};
+            if (id == l && rr < rn) {
+              ah = *reinterpret_cast<const v4i*>(parts_lds + row * kLd + rr);
+              al = *reinterpret_cast<const v4i*>(parts_lds + (kTileRows + row) * kLd + rr);
             }
-          }
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int nb = min(w.strip * 16 + wn * 8 + u, NB - 1);
-            v4i bv = {0, 0, 0, 0};
-            if (rr < a.ad.R)
-              bv = *reinterpret_cast<const v4i*>(
-                  a.ad.B + (((int64_t)l * NB + nb) * 16 + r16) * a.ad.R + rr);
-            v4f_rows c = {0.f, 0.f, 0.f, 0.f};
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, ah),
-                                                        __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, al),
-                                                        __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
+            for (int u = 0; u < 8; ++u) {
+              const int nb = min(w.strip * 16 + wn * 8 + u, NB - 1);
+              v4i bv = {0, 0, 0, 0};
+              if (rr < rn)
+                bv = *reinterpret_cast<const v4i*>(
+                    a.ad.B + (((int64_t)l * NB + nb) * 16 + r16) * a.ad.R + rb + rr);
+              v4f_rows c = {0.f, 0.f, 0.f, 0.f};
+              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, ah),
+                                                          __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
+              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, al),
+                                                          __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][u][r] += (rows >> (4 * j + r)) & 1 ? c[r] : 0.0f;
+              for (int r = 0; r < 4; ++r) acc[i][u][r] += (rows >> (4 * j + r)) & 1 ? c[r] : 0.0f;
+            }
           }
         }
       }
     }
+    if (!works) return;
   }
 
 #pragma unroll
@@ -566,7 +656,7 @@ rows_tile_kernel(RowsArgs a) {
 template <int MT, bool ONE, int ACT, int OUT>
 hipError_t stream_launch(const RowsArgs& a, int64_t blocks, int ksplit, hipStream_t st) {
   const size_t groups = (size_t)(a.sg);
-  size_t lds = ONE ? groups * 128 : groups * MT * 2048;
+  size_t lds = ONE ? (groups * 128 + 1023) / 1024 * 1024 : groups * MT * 2048;
   const size_t red = a.kw ? (size_t)kWaves * (OUT == kSwiglu ? 2 : 1) * MT * 1024 : 0;
   if (red > lds) lds = red;
   hipLaunchKernelGGL((rows_stream_kernel<MT, ONE, ACT, OUT>), dim3((unsigned)blocks, (unsigned)ksplit),
@@ -576,10 +666,13 @@ hipError_t stream_launch(const RowsArgs& a, int64_t blocks, int ksplit, hipStrea
 
 }  // namespace
 
-hipError_t launch_rows_stream(const RowsArgs& a, int mt, int act, int out, int64_t blocks,
+hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int out, int64_t blocks,
                               int ksplit, hipStream_t st) {
+  // what the kernel stages per slice
+  if (act == kCodes && a.sg * (one ? 8 : 128 * mt) > kThreads * (one ? 1 : kStageChunks))
+    return hipErrorInvalidValue;
 #define ROWS_CASE(MTV, ONEV, ACTV, OUTV) \
-  if (mt == MTV && (a.kind == kDirect) == ONEV && act == ACTV && out == OUTV) \
+  if (mt == MTV && one == ONEV && act == ACTV && out == OUTV) \
     return stream_launch<MTV, ONEV, ACTV, OUTV>(a, blocks, ksplit, st);
   ROWS_CASE(1, true, kRawBf16, kSwiglu)
   ROWS_CASE(1, true, kRawF32, kSwiglu)
@@ -590,6 +683,8 @@ hipError_t launch_rows_stream(const RowsArgs& a, int mt, int act, int out, int64
   ROWS_CASE(1, false, kCodes, kParts)
   ROWS_CASE(2, false, kCodes, kParts)
   ROWS_CASE(4, false, kCodes, kParts)
+  ROWS_CASE(1, true, kCodes, kSplit)
+  ROWS_CASE(1, true, kCodes, kAdapt)
   ROWS_CASE(1, false, kCodes, kSplit)
   ROWS_CASE(2, false, kCodes, kSplit)
   ROWS_CASE(3, false, kCodes, kSplit)
