@@ -85,6 +85,38 @@ struct RowsArgs {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// 16 bytes per lane from a buffer straight into LDS: lane i's go to lds + 16 i
+// (lds is the same for the wavefront).  An offset past the buffer stores
+// zeros without a request.  Written as an instruction because the compiler
+// makes every LDS read that follows its builtin wait for the load, whatever
+// buffer it reads; here nothing waits until loads_done() below, which has to
+// come before the barrier that hands the bytes over.  (No register is
+// written, and m0 has no other use in the kernels that call this; the compiler's own waits count at least the loads it knows of, and
+// loads retire in order, so they only become stricter.)
+struct LdsSource {
+  v4i words;  // raw byte buffer descriptor
+};
+__device__ __forceinline__ LdsSource lds_source(const void* base, int64_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return LdsSource{{uniform((int)(uint32_t)p), uniform((int)(uint32_t)(p >> 32) & 0xFFFF),
+                    uniform((int)bytes), kBufferWord3}};
+}
+__device__ __forceinline__ void load_to_lds(const LdsSource& src, uint8_t* lds, int offset, int base) {
+  const int at = uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(offset), "s"(src.words), "s"(uniform(base))
+               : "memory");
+}
+// Until at most N of this wavefront's memory requests are outstanding.
+template <int N>
+__device__ __forceinline__ void loads_done() {
+  static_assert(N < 64, "six bits of count");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+  asm volatile("" ::: "memory");
+}
+
 // Workgroups are dealt to the 8 XCDs round-robin; workgroup b of T takes item
 // xcd_run(b, T), so that each XCD has a contiguous run of items.
 __device__ __forceinline__ int xcd_run(int b, int T) {

@@ -38,12 +38,6 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 constexpr int kStageChunks = 8;  // 16-byte pieces of activations a thread stages per slice
-// Until at most N of this wavefront's memory requests are outstanding.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 64, "six bits of count");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
-}
 
 template <int MT, bool ONE, int ACT, int OUT>
 __global__ void __launch_bounds__(kThreads, MT > 2 || OUT == kAdapt ? 2 : 4)
@@ -76,7 +70,7 @@ rows_stream_kernel(RowsArgs a) {
       src[m] = ONE ? pair_of(a, w, 0) / a.div : row < w.rows ? pair_of(a, w, row) / a.div : -1;
     }
   }
-  const __amdgpu_buffer_rsrc_t rqa = rsrc_of(a.qa, ACT == kCodes ? a.src_rows * a.K : 0);
+  const LdsSource rqa = lds_source(a.qa, ACT == kCodes ? a.src_rows * a.K : 0);
   if (tid < w.rows) {
     const int p = pair_of(a, w, tid);
     s_pair[tid] = p;
@@ -158,8 +152,7 @@ rows_stream_kernel(RowsArgs a) {
           if (sr >= 0) off = sr * a.K + (s0 + q - m * sgn) * kGroup + 64 * h + 16 * j;
         }
         if (uniform(c) < (ONE ? sgn * 8 : MT * sgn * 128))
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rqa, (__attribute__((address_space(3))) void*)(smem + uniform(c) * 16), 16, off, 0, 0, 0);
+          load_to_lds(rqa, smem + uniform(c) * 16, off, 0);
       }
     } else {
       const int row = wave >> rl;
@@ -207,7 +200,7 @@ rows_stream_kernel(RowsArgs a) {
 
     // ---- activations -> LDS
     if constexpr (ACT == kCodes) {
-      wait_loads<3 * NBK * D>();
+      loads_done<3 * NBK * D>();
     } else {
       // quantised here (the rule of w4a8_quant_act)
       for (int row0 = 0; row0 < w.rows; row0 += kWaves >> rl) {
@@ -423,7 +416,7 @@ rows_tile_kernel(RowsArgs a) {
   const uint32_t oz[2] = {(uint32_t)b0 * G * 8 + (r16 >> 1), (uint32_t)b1 * G * 8 + (r16 >> 1)};
   const uint32_t os = (uint32_t)bs * G * 16 + r16;
   const int zshift = (lane & 1) * 4;
-  const __amdgpu_buffer_rsrc_t rqa = rsrc_of(a.qa, a.src_rows * a.K);
+  const LdsSource rqa = lds_source(a.qa, a.src_rows * a.K);
 
   v4u_rows sb[2];
   uint32_t sz[2];
@@ -431,9 +424,7 @@ rows_tile_kernel(RowsArgs a) {
   auto dma = [&](uint8_t* buf, int g) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rqa, (__attribute__((address_space(3))) void*)(buf + (4 * wave + i) * 1024), 16, oa[i],
-          (unsigned)uniform(g * kGroup), 0, 0);
+      load_to_lds(rqa, buf + (4 * wave + i) * 1024, oa[i], g * kGroup);
   };
   auto fetch = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
@@ -518,6 +509,7 @@ rows_tile_kernel(RowsArgs a) {
   store_block(smem[0], 0);
   store_block(smem[0], 1);
   store_scale(smem[0]);
+  loads_done<0>();
   __syncthreads();
   if (!works) {  // feeds the others; the same barriers
     for (int g = gb; g < ge; ++g) {
@@ -529,25 +521,27 @@ rows_tile_kernel(RowsArgs a) {
         store_block(next, 1);
         store_scale(next);
       }
+      loads_done<0>();
       __syncthreads();
     }
     if constexpr (OUT != kAdapt) return;
   }
-  if (works) for (int g = gb; g < ge; g += 2) {
-    if (g + 1 < ge) {  // buffer 1 was last read before the previous barrier
-      dma(smem[1], g + 1);
+  // One group from `cur` while the next one's operands go into `next`, which
+  // was last read before the previous barrier.
+  auto step = [&](const uint8_t* cur, uint8_t* next, int g) __attribute__((always_inline)) {
+    if (g + 1 < ge) {
+      dma(next, g + 1);
       fetch(g + 1);
     }
-    compute(smem[0], g + 1 < ge ? smem[1] : nullptr);
+    compute(cur, g + 1 < ge ? next : nullptr);
+    loads_done<0>();
     __syncthreads();
-    if (g + 1 >= ge) break;
-    if (g + 2 < ge) {
-      dma(smem[0], g + 2);
-      fetch(g + 2);
+  };
+  if (works)
+    for (int g = gb; g < ge; g += 2) {
+      step(smem[0], smem[1], g);
+      if (g + 1 < ge) step(smem[1], smem[0], g + 1);
     }
-    compute(smem[1], g + 2 < ge ? smem[0] : nullptr);
-    __syncthreads();
-  }
 
   if constexpr (OUT == kAdapt) {
     // sums scaled, then each adapter's product added on the bf16 matrix
