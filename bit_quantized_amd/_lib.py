@@ -127,13 +127,26 @@ def _p(t: torch.Tensor | None):
 
 
 def _stream(device=None):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The current stream's handle.  (A Stream object costs 2.0 us to make, the
+    handle alone 0.1: as much as the rest of a small call's checks.)"""
+    index = None if device is None else device.index
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if index is None else index))
 
 
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous and on the GPU")
+
+
+def _need_on(device: int, *ts):
+    """All contiguous and on this GPU."""
+    for t in ts:
+        if t is not None and (t.get_device() != device or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on one GPU")
+    if device < 0:
+        raise ValueError("tensors must be contiguous and on the GPU")
 
 
 @dataclass
@@ -566,19 +579,21 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.
     value: the sum of its group_top best).  An expert whose logit is minus
     infinity is never chosen; where fewer than k remain, ids are -1."""
     lib = load()
-    _need_cuda(logits, bias, ids, weights)
+    _need_on(logits.get_device(), logits, bias, ids, weights)
     if score not in SCORES:
         raise ValueError(f"unknown score function {score!r}")
-    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1]):
+    M, E = logits.shape
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise TypeError("bias must be float32 [E]")
     dt = _act_dtype(logits)
-    M, E = logits.shape
-    ids = torch.empty((M, k), dtype=torch.int32, device=logits.device) if ids is None else ids
-    weights = torch.empty((M, k), dtype=torch.float32, device=logits.device) if weights is None \
-        else weights
-    if ids.dtype != torch.int32 or weights.dtype != torch.float32 or \
-            tuple(ids.shape) != (M, k) or tuple(weights.shape) != (M, k):
-        raise TypeError("ids must be int32 and weights float32, both [M][k]")
+    if ids is None:
+        ids = logits.new_empty((M, k), dtype=torch.int32)
+    elif ids.dtype != torch.int32 or ids.shape != (M, k):
+        raise TypeError("ids must be int32 [M][k]")
+    if weights is None:
+        weights = logits.new_empty((M, k), dtype=torch.float32)
+    elif weights.dtype != torch.float32 or weights.shape != (M, k):
+        raise TypeError("weights must be float32 [M][k]")
     _check(lib.w4a8_moe_route(_p(logits), dt, _p(bias), M, E, k, SCORES[score], n_groups,
                               topk_groups, group_top, int(renormalize), scale, _p(ids), _p(weights),
                               _stream(logits.device)))
@@ -623,7 +638,7 @@ def moe_mlp(x: torch.Tensor, up: ExpertWeights, down: ExpertWeights, ids: torch.
     lib = load()
     up.packed.check()
     down.packed.check()
-    _need_cuda(x, ids, weights, out)
+    _need_on(x.get_device(), x, ids, weights, up.packed.buf, down.packed.buf, out, workspace)
     M, K = x.shape
     dt = _act_dtype(x)
     E, inter = up.n_experts, down.K
@@ -632,11 +647,10 @@ def moe_mlp(x: torch.Tensor, up: ExpertWeights, down: ExpertWeights, ids: torch.
                          f"[{down.N}][{down.K}] do not fit together")
     if ids.dtype != torch.int32 or weights.dtype != torch.float32:
         raise TypeError("ids must be int32 and weights float32")
-    k = ids.shape[1]
-    if tuple(ids.shape) != (M, k) or tuple(weights.shape) != (M, k):
+    if ids.dim() != 2 or ids.shape[0] != M or weights.shape != ids.shape:
         raise ValueError("ids and weights must be [M][k]")
-    out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if out is None else out
-    _need_out(out, M, K)
+    k = ids.shape[1]
+    out = _out(out, x, M, K)
     if workspace is None:
         workspace = torch.empty(max(moe_mlp_workspace_bytes(M, k, E, inter, K), 16),
                                 dtype=torch.uint8, device=x.device)
@@ -647,9 +661,12 @@ def moe_mlp(x: torch.Tensor, up: ExpertWeights, down: ExpertWeights, ids: torch.
     return out
 
 
-def _need_out(out: torch.Tensor, M: int, N: int):
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N):
+def _out(out: torch.Tensor | None, x: torch.Tensor, M: int, N: int) -> torch.Tensor:
+    if out is None:
+        return x.new_empty((M, N), dtype=torch.bfloat16)
+    if out.dtype != torch.bfloat16 or out.shape != (M, N):
         raise TypeError(f"out must be bfloat16 [{M}][{N}]")
+    return out
 
 
 @dataclass
@@ -681,17 +698,16 @@ def lora_linear(x: torch.Tensor, w: PackedWeight, adapters: LoraAdapters, ids: t
     a row whose id lies outside [0, L) has no adapter."""
     lib = load()
     w.check()
-    _need_cuda(x, ids, out)
+    _need_on(x.get_device(), x, ids, w.buf, adapters.A, adapters.B, adapters.scale, out, workspace)
     M, K = x.shape
     dt = _act_dtype(x)
     L, R, AK = adapters.A.shape
     if K != w.K or AK != K or adapters.B.shape[1] != w.N:
         raise ValueError(f"x [{M}][{K}], weight [{w.N}][{w.K}] and adapters [{L}][{R}][{AK}], "
                          f"[{L}][{adapters.B.shape[1]}][{R}] do not fit together")
-    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,):
+    if ids.dtype != torch.int32 or ids.shape != (M,):
         raise TypeError("ids must be int32 [M]")
-    out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device) if out is None else out
-    _need_out(out, M, w.N)
+    out = _out(out, x, M, w.N)
     if workspace is None:
         workspace = torch.empty(max(lora_linear_workspace_bytes(M, w.N, K, L, R), 16),
                                 dtype=torch.uint8, device=x.device)

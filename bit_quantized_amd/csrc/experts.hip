@@ -122,6 +122,7 @@ down_token_kernel(RowsArgs a, int k) {
       float sc[D];
       uint32_t z[D];
       auto load = [&](int i, int t) __attribute__((always_inline)) {
+        t = min(t, G);  // past the run: no memory request, zeros
         d[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, 16 * lane, (unsigned)uniform(t * kBlockBytes),
                                                      kNontemporal);
         sc[i] = __builtin_bit_cast(
@@ -360,11 +361,6 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
   a.cols = (int)(m.I / 16);
   a.h = h;
   const int G = (int)(m.K / kGroup), GI = (int)(m.I / kGroup);
-  // LDS of 64 KiB: 32 / mt groups at a time, in slices of equal length
-  auto slice = [&](int groups) {
-    const int most = 32 / mt, n = (groups + most - 1) / most;
-    return (groups + n - 1) / n;
-  };
   if (big) {
     a.strips = a.cols / 8;
     e = launch_rows_tile(a, kSwiglu, max_tiles * a.strips, 1, st);
@@ -372,8 +368,10 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
     a.kw = 0;
     a.ncol = 1;
     a.strips = (a.cols + 7) / 8;
-    a.sg = slice(G);
-    e = launch_rows_stream(a, mt, false, kCodes, kSwiglu, max_tiles * a.strips, 1, st);
+    a.sg = G;
+    e = G <= staged_groups(mt)
+            ? launch_rows_stream(a, mt, false, kCodes, kSwiglu, max_tiles * a.strips, 1, st)
+            : launch_rows_run(a, mt, kSwiglu, max_tiles * a.strips, 1, st);
   }
   if (e != hipSuccess) return e;
 
@@ -402,13 +400,15 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
     d.strips = (d.nbe + 15) / 16;
     e = launch_rows_tile(d, kParts, max_tiles * d.strips, 1, st);
   } else {
-    d.sg = raw ? GI : slice(GI);
+    d.sg = GI;
     d.kw = 0;
-    // runs of about 24 units per wavefront where one slice holds all groups
-    d.ncol = d.sg == GI ? (24 + GI - 1) / GI : 1;
+    // runs of about 24 units per wavefront
+    d.ncol = (24 + GI - 1) / GI;
     const int per = 8 * d.ncol;
     d.strips = (d.cols + per - 1) / per;
-    e = launch_rows_stream(d, mt, false, raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st);
+    e = raw || GI <= staged_groups(mt)
+            ? launch_rows_stream(d, mt, false, raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st)
+            : launch_rows_run(d, mt, kParts, max_tiles * d.strips, 1, st);
   }
   if (e != hipSuccess) return e;
   const int64_t total = m.M * (m.K / 8);

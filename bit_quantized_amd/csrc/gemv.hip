@@ -47,7 +47,7 @@
 //     exact int32 totals and one per-channel scale in the epilogue.
 #include <atomic>
 
-#include "w4a8_internal.h"
+#include "rows.h"
 
 namespace w4a8 {
 namespace {
@@ -182,8 +182,12 @@ __device__ __forceinline__ void wait_flag(uint32_t* s_sync) {
 // totals over the run, the scales applied once in the epilogue.
 // EARLY: the streamers' first code blocks go out beside the token's
 // requests instead of after the set-up barrier (chosen on the host).
+// ADAPT: y also gets the token's adapter product (GemmArgs::ad).  The scaled
+// x A^T is summed by the last wavefront while it would wait for the flag, the
+// product with B taken in the epilogue (M = 1, K = 3584 -> N = 18944, rank
+// 16: ADAPT_US against PLAIN_US without it).
 template <int XT, bool DEBUG, bool KSPLIT, int kQChunks, bool W8 = false, bool HAD = false,
-          bool EARLY = false, int DR = D>
+          bool EARLY = false, int DR = D, bool ADAPT = false>
 __global__ void __launch_bounds__(kThreads)
 gemv_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
             const uint8_t* __restrict__ zeros, const void* __restrict__ xin, int K, int cb_q,
@@ -194,6 +198,7 @@ gemv_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
   __shared__ float part[kMaxCb][kWaves][16];
   // [0] token absmax bits, [1] quantisers past the absmax, [2] quantisers done
   __shared__ unsigned s_sync[4];
+  __shared__ float s_hx[ADAPT ? kMaxRank : 1];  // scaled x A^T of the token
   const int G = K / kGroup, NB = (int)(a.N / kBlockCols);
   int8_t* qs = reinterpret_cast<int8_t*>(smem);               // [K] activation codes
   int* rs = reinterpret_cast<int*>(smem + K);                  // [4G] per-quarter code sums
@@ -425,6 +430,15 @@ gemv_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
     // ---- streamer: metadata and DR code blocks are in flight; the flag
     // (an unbounded spin that ends once all kQ quantisers or stagers have
     // made their one increment of s_sync[2])
+    if constexpr (ADAPT) {
+      if (wave == kWaves - 1) {
+        const int id = a.ad.ids[0];
+        const bool has = id >= 0 && id < a.ad.L;
+        const float sc = has ? a.ad.scale[id] : 0.0f;
+        if (has)
+          for (int r = lane; r < a.ad.R; r += 64) s_hx[r] = adapter_sum(a.ad, 1, 0, r, sc);
+      }
+    }
     if constexpr (XT == X_QUANTISED) scale = a.sa[0];
     wait_flag(s_sync);
     if constexpr (A16)
@@ -574,7 +588,17 @@ gemv_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) total += part[cbl][w][cc];
     const int64_t n = (int64_t)16 * (nb0 + cbl) + cc;
-    if (gridDim.y == 1) {
+    if constexpr (ADAPT) {
+      const int id = a.ad.ids[0];
+      float v = scale * total;
+      if (id >= 0 && id < a.ad.L) {
+        const uint16_t* brow = a.ad.B + ((int64_t)id * a.N + n) * a.ad.R;
+        AdapterRow b;
+        b.fetch(brow, 0, a.ad.R);
+        v += b.dot(s_hx, brow, a.ad.R);
+      }
+      a.y[n] = f32_to_bf16_rne(v);
+    } else if (gridDim.y == 1) {
       if (a.y) a.y[n] = f32_to_bf16_rne(scale * total);
     } else {
       a.workspace[(int64_t)blockIdx.y * a.N + n] = total;
@@ -599,6 +623,25 @@ hipError_t launch_ks(const GemmArgs& a, hipStream_t st) {
     }
   }
   if (a.hadamard) return hipErrorInvalidValue;
+  if constexpr ((XT == X_BF16 || XT == X_F32) && !W8 && !KSPLIT) {
+    if (a.ad.hx) {  // ring depth and order of the first loads as below
+      if (a.partials) return hipErrorInvalidValue;
+      const int64_t NB = a.N / kBlockCols;
+      const bool early = (int64_t)a.cb <= device_cus() && a.K <= 8192 && (NB + a.cb - 1) / a.cb * G >= 64;
+#define ADAPT_LAUNCH(EARLY_, DR_)                                                                     \
+  hipLaunchKernelGGL((gemv_kernel<XT, false, false, QC, false, false, EARLY_, DR_, true>), grid,      \
+                     dim3(kThreads), lds, st, a.w.codes, a.w.scales, a.w.zeros, xin, (int)a.K, a.cb_q, \
+                     a.cb_r, a)
+      if (a.K >= 16384)
+        ADAPT_LAUNCH(false, kDeepD);
+      else if (early)
+        ADAPT_LAUNCH(true, D);
+      else
+        ADAPT_LAUNCH(false, D);
+#undef ADAPT_LAUNCH
+      return hipGetLastError();
+    }
+  }
   if (a.partials) {
     hipLaunchKernelGGL((gemv_kernel<XT, true, KSPLIT, QC, W8>), grid, dim3(kThreads), lds, st, a.w.codes,
                        a.w.scales, a.w.zeros, xin, (int)a.K, a.cb_q, a.cb_r, a);

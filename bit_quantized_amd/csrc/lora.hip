@@ -14,7 +14,7 @@ constexpr int kWaves = kThreads / 64;
 
 // ----------------------------------------- quantisation and x A^T together
 //
-// Workgroups [0, M) quantise one row each.  The others take a fragment of 16
+// Workgroups [0, qrows) quantise one row each.  The others take a fragment of 16
 // rows, every `slots`-th of the distinct adapters among them, and a K slice,
 // which the wavefronts share: for an adapter, v_mfma_f32_16x16x32_bf16 of the
 // 16 rows (A operand) against its rows of A (B operand), float sums, and only
@@ -26,20 +26,20 @@ constexpr int kWaves = kThreads / 64;
 template <int ACT, int RT>
 __global__ void __launch_bounds__(kThreads)
 adapter_down_kernel(LoraArgs a, int8_t* __restrict__ qa, float* __restrict__ sa,
-                    float* __restrict__ hx, int slots, int slices) {
-  constexpr int U = RT >= 4 ? 2 : 4;  // steps of 32 inputs whose loads are in flight
+                    float* __restrict__ hx, int qrows, int slots, int slices) {
+  constexpr int U = RT >= 8 ? 2 : 4;  // steps of 32 inputs whose loads are in flight
   constexpr bool F32 = ACT == kRawF32;
   __shared__ float s_red[kWaves][RT * 4][64];
   __shared__ float s_max[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const uint8_t* x = static_cast<const uint8_t*>(a.x);
   const int K = (int)a.K;
-  if ((int64_t)blockIdx.x < a.M) {
+  if ((int)blockIdx.x < qrows) {
     const int64_t m = blockIdx.x;
     quantise_row<ACT, kThreads>(x + m * K * RawRow<ACT>::kBytes, K, qa + m * K, sa + m, s_max);
     return;
   }
-  const int b = (int)(blockIdx.x - a.M);
+  const int b = (int)blockIdx.x - qrows;
   const int slice = b % slices, slot = b / slices % slots;
   const int64_t m0 = (int64_t)(b / slices / slots) * 16;
   const int r16 = lane & 15, j = lane >> 4;
@@ -122,33 +122,53 @@ adapter_down_kernel(LoraArgs a, int8_t* __restrict__ qa, float* __restrict__ sa,
 }
 
 // --------------------------------- K slices summed, adapter product added
+//
+// One channel per thread.  The slices' sums and the first ranks of B are on
+// their way before the row's x A^T is summed, so a workgroup waits for memory
+// about once.
 __global__ void __launch_bounds__(256)
 adapt_reduce_kernel(const float* __restrict__ parts, int ksplit, const float* __restrict__ sa,
                     int64_t M, int N, AdaptArgs ad, uint16_t* __restrict__ y) {
   __shared__ float s_hx[kMaxRank];
   const int64_t m = blockIdx.y;
+  const int n = blockIdx.x * 256 + threadIdx.x;
   const int id = ad.ids[m];
   const bool has = id >= 0 && id < ad.L;
-  if (has)
-    for (int r = threadIdx.x; r < ad.R; r += 256) s_hx[r] = adapter_sum(ad, M, m, r, ad.scale[id]);
-  __syncthreads();
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
   float v = 0.0f;
-#pragma unroll 4
-  for (int k = 0; k < ksplit; ++k) v += parts[((int64_t)k * M + m) * N + n];
-  v *= sa[m];
-  if (has) v += adapter_dot(s_hx, ad.B + ((int64_t)id * N + n) * ad.R, ad.R);
-  y[m * N + n] = f32_to_bf16_rne(v);
+  if (n < N) {
+    const float* p = parts + m * N + n;
+    const int64_t step = M * N;
+    for (int k = 0; k < ksplit; k += 8) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = k + i < ksplit ? p[(k + i) * step] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += t[i];
+    }
+    v *= sa[m];
+  }
+  if (!has) {
+    if (n < N) y[m * N + n] = f32_to_bf16_rne(v);
+    return;
+  }
+  const uint16_t* brow = ad.B + ((int64_t)id * N + min(n, N - 1)) * ad.R;
+  AdapterRow b;
+  b.fetch(brow, 0, ad.R);
+  for (int r = threadIdx.x; r < ad.R; r += 256) s_hx[r] = adapter_sum(ad, M, m, r, ad.scale[id]);
+  __syncthreads();
+  if (n < N) y[m * N + n] = f32_to_bf16_rne(v + b.dot(s_hx, brow, ad.R));
 }
+
+constexpr int64_t kMaxPassRows = (int64_t)1 << 20;
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 template <int ACT, int RT>
 void down_launch(const LoraArgs& l, const LoraPlan& p, int8_t* qa, float* sa, float* hx, hipStream_t st) {
-  const int64_t blocks = l.M + (l.M + 15) / 16 * p.slots * p.slices;
+  const int qrows = p.gemv ? 0 : (int)l.M;  // (the GEMV quantises its row itself)
+  const int64_t blocks = qrows + (l.M + 15) / 16 * p.slots * p.slices;
   hipLaunchKernelGGL((adapter_down_kernel<ACT, RT>), dim3((unsigned)blocks), dim3(kThreads), 0, st, l, qa,
-                     sa, hx, p.slots, p.slices);
+                     sa, hx, qrows, p.slots, p.slices);
 }
 
 template <int ACT>
@@ -168,12 +188,19 @@ void down_rank(const LoraArgs& l, const LoraPlan& p, int8_t* qa, float* sa, floa
 LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   LoraPlan p;
   const int64_t cus = device_cus(), G = K / kGroup, cols = N / kBlockCols;
+  // rows of one pass: 32-bit offsets into the codes, and a grid of at most
+  // 2^32 threads for the step that has a workgroup per row
   int64_t mc = kPrefillMaxBytes / K;
+  if (mc > kMaxPassRows) mc = kMaxPassRows;
   if (mc >= kTileRows) mc = mc / kTileRows * kTileRows;
   if (mc > M) mc = M;
   p.rows = mc;
   if (mc < 1) return p;
-  if (mc <= 64) {
+  const GemvShape gs = gemv_shape(N, K);
+  p.gemv = M == 1 && K <= kGemvMaxK && gemv_shape_ok(N, K, gs);
+  if (p.gemv) {
+    p.ksplit = gs.ksplit;
+  } else if (mc <= 64) {
     p.mt = (int)((mc + 15) / 16);
     if (mc <= 16) {  // whole K per workgroup, one launch, while the columns fill the machine
       while (p.kw < 3 && cols / (8 >> p.kw) < cus) ++p.kw;
@@ -187,7 +214,6 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
       int64_t ks = 2 * cus / strips;
       if (ks > G / 4) ks = G / 4;
       p.ksplit = (int)(ks > 1 ? ks : 1);
-      if (p.ksplit == 1) p.ksplit = 1;
     }
   } else {
     const int64_t tiles = (mc + kTileRows - 1) / kTileRows * ((N + kTileCols - 1) / kTileCols);
@@ -198,7 +224,9 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   const int64_t frags = (mc + 15) / 16;
   p.slots = (int)(mc > 256 ? 1 : mc < 16 ? mc : 16);
   if (p.slots > L) p.slots = L;
-  int64_t sl = 4 * cus / (frags * p.slots), most = (K / 32 + kWaves - 1) / kWaves;
+  // several rounds of workgroups where every wavefront still gets a few steps;
+  // one where the product's tiles sum the slices again for every strip
+  int64_t sl = (mc > 256 ? 1 : 4) * cus / (frags * p.slots), most = (K / 32 + kWaves - 1) / kWaves;
   if (sl > most) sl = most;
   if (sl > 16) sl = 16;
   p.slices = (int)(sl > 1 ? sl : 1);
@@ -248,14 +276,35 @@ hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {
   a.y = l.y;
   a.ad = AdaptArgs{hx, l.B, l.scale, l.ids, p.slices, l.L, l.R};
   const int G = (int)(l.K / kGroup);
-  if (p.mt) {
+  if (p.gemv) {
+    GemmArgs g{};
+    g.x = l.x;
+    g.x_dtype = l.x_dtype;
+    g.w = l.w;
+    g.M = 1;
+    g.N = l.N;
+    g.K = l.K;
+    g.y = l.y;
+    g.workspace = parts;
+    g.sa_ws = parts ? sa : nullptr;
+    const GemvShape gs = gemv_shape(l.N, l.K);
+    g.cb = gs.cb;
+    g.ks = gs.ks;
+    g.ksplit = gs.ksplit;
+    if (!parts) g.ad = a.ad;
+    e = launch_gemv(g, st);
+  } else if (p.mt) {
     a.kw = p.kw;
     a.ncol = 1;
     const int cw = 8 >> p.kw, per = (G + p.ksplit - 1) / p.ksplit;
-    const int most = l.M == 1 ? 64 : 32 / p.mt, n = (per + most - 1) / most;
     a.strips = (a.cols + cw - 1) / cw;
-    a.sg = (per + n - 1) / n;
-    e = launch_rows_stream(a, p.mt, l.M == 1, kCodes, parts ? kSplit : kAdapt, a.strips, p.ksplit, st);
+    if (parts && per > staged_groups(p.mt)) {
+      e = launch_rows_run(a, p.mt, kSplit, a.strips, p.ksplit, st);
+    } else {
+      const int most = staged_groups(p.mt), n = (per + most - 1) / most;
+      a.sg = (per + n - 1) / n;
+      e = launch_rows_stream(a, p.mt, false, kCodes, parts ? kSplit : kAdapt, a.strips, p.ksplit, st);
+    }
   } else {
     const int64_t tiles = (l.M + kTileRows - 1) / kTileRows;
     a.strips = (a.nbe + 15) / 16;

@@ -19,6 +19,7 @@ struct RouteArgs {
   float scale;
   int* ids;
   float* weights;
+  int gl = 0;  // log2 lanes per group (set by the launcher)
 };
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);

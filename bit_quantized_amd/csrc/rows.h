@@ -42,17 +42,6 @@ struct RowTile {
   int expert, first, rows, place;
 };
 
-// The adapters of a call: y[m] += scale[l] * (x[m] A[l]^T) B[l]^T, l = ids[m];
-// rows whose id lies outside [0, L) have none.  hx: the sums x A^T of the
-// call, [slices][M][R], not yet scaled.
-struct AdaptArgs {
-  const float* hx;
-  const uint16_t* B;
-  const float* scale;
-  const int* ids;
-  int slices, L, R;
-};
-
 struct RowsArgs {
   const int8_t* qa;  // activation codes [source rows][K] and their scales
   const float* sa;
@@ -261,19 +250,35 @@ __device__ __forceinline__ void unpack_unit(const v4u_rows& d, uint32_t zz, v4i&
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// sum_r hx[r] B[n][r] over one adapter, hx already scaled (LDS or global).
-__device__ __forceinline__ float adapter_dot(const float* hx, const uint16_t* brow, int R) {
-  float v = 0.0f;
-  for (int r = 0; r < R; r += 8) {
-    const v4u_rows d = *reinterpret_cast<const v4u_rows*>(brow + r);
+// sum_r hx[r] B[n][r] over one adapter, hx already scaled (LDS), 32 ranks'
+// loads at a time.  fetch() may run long before dot(): the loads of the first
+// ranks then return beside whatever the wavefront waits for in between.
+struct AdapterRow {
+  static constexpr int kAhead = 4;  // chunks of eight ranks
+  v4u_rows d[kAhead];
+  __device__ __forceinline__ void fetch(const uint16_t* brow, int r0, int R) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v += hx[r + 2 * i] * __uint_as_float(d[i] << 16);
-      v += hx[r + 2 * i + 1] * __uint_as_float(d[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < kAhead; ++i)
+      d[i] = *reinterpret_cast<const v4u_rows*>(brow + min(r0 + 8 * i, R - 8));
   }
-  return v;
-}
+  __device__ __forceinline__ float dot(const float* hx, const uint16_t* brow, int R) {
+    float v = 0.0f;
+    for (int r0 = 0; r0 < R; r0 += 8 * kAhead) {
+      if (r0) fetch(brow, r0, R);
+#pragma unroll
+      for (int c = 0; c < kAhead; ++c)
+        if (r0 + 8 * c < R) {
+          const float* h = hx + r0 + 8 * c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v += h[2 * i] * __uint_as_float(d[c][i] << 16);
+            v += h[2 * i + 1] * __uint_as_float(d[c][i] & 0xFFFF0000u);
+          }
+        }
+    }
+    return v;
+  }
+};
 
 // Row m's scaled adapter sums: scale * sum over the slices of hx[.][m][r].
 // Eight slices' loads go out together.
@@ -295,10 +300,14 @@ __device__ __forceinline__ float adapter_sum(const AdaptArgs& ad, int64_t M, int
 // workgroup (1..4) of the weight-streaming kernel; one: tiles of a single row.
 hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int out, int64_t blocks,
                               int ksplit, hipStream_t st);
+// mt, out (kSwiglu, kParts, kSplit) as above; codes only, eight columns of
+// a.ncol each per workgroup (kw = 0); more than one column only unsplit.
+hipError_t launch_rows_run(const RowsArgs& a, int mt, int out, int64_t blocks, int ksplit, hipStream_t st);
 hipError_t launch_rows_tile(const RowsArgs& a, int out, int64_t blocks, int ksplit, hipStream_t st);
 // Rows per workgroup of launch_rows_tile, and its output channels.
 constexpr int kTileRows = 256;
 constexpr int kTileCols = 256;
-constexpr int kMaxRank = 128;  // of an adapter
+// Groups of 16 mt rows of activations that fit 64 KiB of LDS.
+constexpr int staged_groups(int mt) { return 32 / mt; }
 
 }  // namespace w4a8

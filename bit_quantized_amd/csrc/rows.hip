@@ -28,8 +28,8 @@ constexpr int kWaves = kThreads / 64;
 // holding row r, input channels 128 g + 64 h + 16 j .. + 15, so a fragment is
 // one conflict-free 16-byte read per lane.  Rows past the tile are never
 // written: an int8 product of any bytes is finite and belongs to no output.
-// ONE: the tile is a single row, kept as [groups][2][4][16 B] and read by all
-// rows of the operand.
+// ONE: the tile is a single raw row, kept as [groups][2][4][16 B] and read by
+// all rows of the operand.
 // Memory order: the activations' loads go first, then the first D weight
 // units, then whatever else the tile needs, so that the activations (waited
 // for first) do not queue behind the weights, and the weights stay in flight
@@ -37,18 +37,24 @@ constexpr int kWaves = kThreads / 64;
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
+// Groups whose activations fit the 64 KiB that rows_stream_kernel stages at
+// once; past them rows_run_kernel, whose buffers hold run_groups() each.
+constexpr int run_groups(int mt, int out) { return mt <= 2 && out != kSwiglu ? 8 : 4; }
 constexpr int kStageChunks = 8;  // 16-byte pieces of activations a thread stages per slice
 
 template <int MT, bool ONE, int ACT, int OUT>
 __global__ void __launch_bounds__(kThreads, MT > 2 || OUT == kAdapt ? 2 : 4)
 rows_stream_kernel(RowsArgs a) {
+  static_assert(!ONE || ACT != kCodes, "a lone row is quantised here");
   constexpr int BM = ONE ? 1 : 16 * MT;
   constexpr int NBK = OUT == kSwiglu ? 2 : 1;  // blocks per column
   constexpr int D = NBK == 2 ? 4 : 8;          // columns' units in flight
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int s_pair[BM];
   __shared__ float s_scale[BM], s_max[kWaves];
-  __shared__ float s_hx[OUT == kAdapt ? BM * kMaxRank : 1];  // scaled x A^T of the rows
+  // kAdapt: scaled x A^T of the rows, and the rows' adapter products
+  __shared__ float s_hx[OUT == kAdapt ? BM * kMaxRank : 1];
+  __shared__ float s_dot[OUT == kAdapt ? kWaves : 1][OUT == kAdapt ? 4 : 1][64];
 
   Where w;
   if (!locate<BM>(a, w)) return;
@@ -67,10 +73,25 @@ rows_stream_kernel(RowsArgs a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = 16 * m + r16;
-      src[m] = ONE ? pair_of(a, w, 0) / a.div : row < w.rows ? pair_of(a, w, row) / a.div : -1;
+      src[m] = row < w.rows ? pair_of(a, w, row) / a.div : -1;
     }
   }
   const LdsSource rqa = lds_source(a.qa, ACT == kCodes ? a.src_rows * a.K : 0);
+  // kAdapt: the column's 2^kw wavefronts deal its result rows 4 j + r out, r =
+  // kwi, kwi + 2^kw, ...; the first one's B row is fetched ahead
+  int aid[OUT == kAdapt ? 4 : 1];
+  if constexpr (OUT == kAdapt) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * j + r;
+      const int id = row < w.rows ? a.ad.ids[w.first + row] : -1;
+      aid[r] = nc > 0 && (r & (KW - 1)) == kwi && id >= 0 && id < a.ad.L ? id : -1;
+    }
+  }
+  auto brow = [&](int r) __attribute__((always_inline)) {
+    return a.ad.B + ((int64_t)aid[OUT == kAdapt ? r : 0] * (16 * a.nbe) + 16 * c0 + r16) * a.ad.R;
+  };
+  AdapterRow bh;
   if (tid < w.rows) {
     const int p = pair_of(a, w, tid);
     s_pair[tid] = p;
@@ -104,13 +125,8 @@ rows_stream_kernel(RowsArgs a) {
           a.parts[((int64_t)blockIdx.y * a.M + w.first + row) * (16 * a.nbe) + 16 * c + r16] =
               acc[0][m][r];
         } else {
-          const int64_t row_m = w.first + row, n = 16 * c + r16;
-          const int id = a.ad.ids[row_m];
-          float v = s_scale[row] * acc[0][m][r];
-          if (id >= 0 && id < a.ad.L)
-            v += adapter_dot(s_hx + row * a.ad.R, a.ad.B + ((int64_t)id * (16 * a.nbe) + n) * a.ad.R,
-                             a.ad.R);
-          a.y[row_m * (16 * a.nbe) + n] = f32_to_bf16_rne(v);
+          a.y[(int64_t)(w.first + row) * (16 * a.nbe) + 16 * c + r16] =
+              f32_to_bf16_rne(s_scale[row] * acc[0][m][r] + s_dot[cw][r][lane]);
         }
       }
   };
@@ -136,23 +152,17 @@ rows_stream_kernel(RowsArgs a) {
       // zeros, no request); the LDS has to be free
       if (s0 != gb) lds_barrier();
 #pragma unroll
-      for (int i = 0; i < (ONE ? 1 : kStageChunks); ++i) {
+      for (int i = 0; i < kStageChunks; ++i) {
         const int c = tid + i * kThreads;
-        int off = kOob;
-        if constexpr (ONE) {
-          if (c < sgn * 8) off = src[0] * a.K + s0 * kGroup + 16 * c;
-        } else {
-          const int q = c >> 7, h = (c >> 6) & 1;
-          int m = 0, sr = src[0];
+        const int q = c >> 7, h = (c >> 6) & 1;
+        int off = kOob, m = 0, sr = src[0];
 #pragma unroll
-          for (int t = 1; t < MT; ++t) {
-            m += q >= t * sgn;
-            sr = m == t ? src[t] : sr;
-          }
-          if (sr >= 0) off = sr * a.K + (s0 + q - m * sgn) * kGroup + 64 * h + 16 * j;
+        for (int t = 1; t < MT; ++t) {
+          m += q >= t * sgn;
+          sr = m == t ? src[t] : sr;
         }
-        if (uniform(c) < (ONE ? sgn * 8 : MT * sgn * 128))
-          load_to_lds(rqa, smem + uniform(c) * 16, off, 0);
+        if (sr >= 0) off = sr * a.K + (s0 + q - m * sgn) * kGroup + 64 * h + 16 * j;
+        if (uniform(c) < MT * sgn * 128) load_to_lds(rqa, smem + uniform(c) * 16, off, 0);
       }
     } else {
       const int row = wave >> rl;
@@ -181,8 +191,9 @@ rows_stream_kernel(RowsArgs a) {
     v4u_rows d[D][NBK];
     float s[D][NBK];
     uint32_t z[D][NBK];
-    // past the run: no memory request, zeros
+    // past the run (the descriptors' end): no memory request, zeros
     auto load = [&](int i, int t) __attribute__((always_inline)) {
+      t = min(t, T);
 #pragma unroll
       for (int b = 0; b < NBK; ++b) {
         d[i][b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], 16 * lane, (unsigned)uniform(t * kBlockBytes),
@@ -258,14 +269,34 @@ rows_stream_kernel(RowsArgs a) {
       }
     }
     if constexpr (OUT == kAdapt) {
-      if (s0 == gb)
+      if (s0 == gb) {
+        if (kwi < 4) {
+          const int f = kwi == 0 ? aid[0] : kwi == 1 ? aid[1] : kwi == 2 ? aid[2] : aid[3];
+          if (f >= 0)
+            bh.fetch(a.ad.B + ((int64_t)f * (16 * a.nbe) + 16 * c0 + r16) * a.ad.R, 0, a.ad.R);
+        }
         for (int i = tid; i < w.rows * a.ad.R; i += kThreads) {
           const int row = i / a.ad.R, id = a.ad.ids[w.first + row];
           if (id >= 0 && id < a.ad.L)
             s_hx[i] = adapter_sum(a.ad, a.M, w.first + row, i - row * a.ad.R, a.ad.scale[id]);
         }
+      }
     }
     lds_barrier();
+    if constexpr (OUT == kAdapt) {
+      if (s0 == gb) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if ((r & (KW - 1)) == kwi) {
+            float v = 0.0f;
+            if (aid[r] >= 0) {
+              if (r != kwi) bh.fetch(brow(r), 0, a.ad.R);
+              v = bh.dot(s_hx + (4 * j + r) * a.ad.R, brow(r), a.ad.R);
+            }
+            s_dot[cw][r][lane] = v;
+          }
+      }
+    }
 
     // ---- stream the run
     int g = 0, c = c0;
@@ -337,6 +368,177 @@ rows_stream_kernel(RowsArgs a) {
         for (int k = 1; k < KW; ++k)
           acc[b][m][r] += red[k * (NBK * MT * 256) + ((b * MT + m) * 4 + r) * 64 + lane];
   emit(c0);
+}
+
+// ------------------------------------------- few rows, many groups
+//
+// The same product where a tile's activations exceed 64 KiB of LDS: they pass
+// through two LDS buffers of SG groups each, the next slice's loads going out
+// when the current slice begins.  A wavefront's weights (ncol columns, all
+// their groups: one run of the packed planes) flow through a ring of SG units
+// that the slices do not interrupt: slot i holds unit i of a slice and is
+// refilled with unit i of the next one.  Slices have L <= SG units each (the
+// last of a column may have fewer); a slot without a unit loads nothing.
+// (517 tokens, 32 experts, 3584 -> 2 x 1280: RUN_US, against 73 us when every
+// slice drained the ring and waited for its activations.)
+template <int MT, int OUT>
+__global__ void __launch_bounds__(kThreads, 4)
+rows_run_kernel(RowsArgs a) {
+  constexpr int BM = 16 * MT;
+  constexpr int NBK = OUT == kSwiglu ? 2 : 1;
+  constexpr int SG = run_groups(MT, OUT);
+  constexpr int kSlice = SG * MT * 2048;  // bytes of a buffer
+  constexpr int kDma = kSlice / (kThreads * 16);
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int s_pair[BM];
+  __shared__ float s_scale[BM];
+
+  Where w;
+  if (!locate<BM>(a, w)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int r16 = lane & 15, j = lane >> 4;
+  const int G = a.K / kGroup;
+  const int gb = G * blockIdx.y / gridDim.y, Gs = G * (blockIdx.y + 1) / gridDim.y - gb;
+  const int c0 = (w.strip * kWaves + wave) * a.ncol;
+  const int nc = max(min(a.ncol, a.cols - c0), 0);
+  const int columns = min(a.ncol, a.cols - w.strip * kWaves * a.ncol);  // of the first wavefront
+  const int S = (Gs + SG - 1) / SG, L = (Gs + S - 1) / S;
+
+  int src[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + r16;
+    src[m] = row < w.rows ? pair_of(a, w, row) / a.div : -1;
+  }
+  const LdsSource rqa = lds_source(a.qa, a.src_rows * a.K);
+  if (tid < w.rows) {
+    const int p = pair_of(a, w, tid);
+    s_pair[tid] = p;
+    s_scale[tid] = a.sa[p / a.div];
+  }
+  // slice s of the activations into a buffer: [MT][SG][2 halves][64 lanes][16 B]
+  auto stage = [&](uint8_t* buf, int s) __attribute__((always_inline)) {
+    const int live = min(L, Gs - s * L);
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      const int c = wave + i * kWaves;  // KiB of the buffer
+      const int h = c & 1, g = (c >> 1) % SG, m = (c >> 1) / SG;
+      int sr = src[0];
+#pragma unroll
+      for (int t = 1; t < MT; ++t) sr = m == t ? src[t] : sr;
+      const int off = sr >= 0 && g < live ? sr * a.K + (gb + s * L + g) * kGroup + 64 * h + 16 * j : kOob;
+      load_to_lds(rqa, buf + c * 1024, off, 0);
+    }
+  };
+
+  // the run's planes; unit t of the run is group t % G of column t / G (one
+  // column where K is split)
+  __amdgpu_buffer_rsrc_t rc[NBK], rs[NBK], rz[NBK];
+  const int T = nc > 1 ? nc * G : nc * Gs;
+#pragma unroll
+  for (int b = 0; b < NBK; ++b) {
+    const int64_t b0 = ((int64_t)w.expert * a.nbe + b * a.cols + (nc > 0 ? c0 : 0)) * G + gb;
+    rc[b] = rsrc_of(a.codes + b0 * kBlockBytes, (int64_t)T * kBlockBytes);
+    rs[b] = rsrc_of(a.scales + b0 * 16, (int64_t)T * 64);
+    rz[b] = rsrc_of(a.zeros + b0 * kZeroBlockBytes, (int64_t)T * kZeroBlockBytes);
+  }
+  v4u_rows d[SG][NBK];
+  float s[SG][NBK];
+  uint32_t z[SG][NBK];
+  auto load = [&](int i, int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < NBK; ++b) {
+      d[i][b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], 16 * lane, (unsigned)uniform(t * kBlockBytes),
+                                                      kNontemporal);
+      s[i][b] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(rs[b], 4 * r16, (unsigned)uniform(t * 64), 0));
+      z[i][b] = __builtin_amdgcn_raw_buffer_load_b8(rz[b], r16 >> 1, (unsigned)uniform(t * kZeroBlockBytes), 0);
+    }
+  };
+
+  float acc[NBK][MT][4];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < NBK; ++b)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[b][m][r] = 0.0f;
+  };
+  clear();
+  stage(smem, 0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < SG; ++i) {
+    load(i, i < min(L, Gs) ? i : T);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  int col = 0, sl = 0;
+  for (int q = 0; q < columns * S; ++q) {
+    // the slice after this one
+    const bool wrap = sl + 1 == S;
+    const int nsl = wrap ? 0 : sl + 1, ncol = wrap ? col + 1 : col;
+    const int live = min(L, Gs - sl * L), nlive = ncol < nc ? min(L, Gs - nsl * L) : 0;
+    const int nt = ncol * G + nsl * L;
+    uint8_t* buf = smem + (q & 1) * kSlice;
+    loads_done<3 * NBK * SG>();  // this slice's activations
+    lds_barrier();
+    if (q + 1 < columns * S) stage(smem + ((q + 1) & 1) * kSlice, nsl);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < SG; ++i) {
+      if (i < live && col < nc) {
+        v4i lo[NBK], hi[NBK];
+        float sc[NBK];
+#pragma unroll
+        for (int b = 0; b < NBK; ++b) {
+          const uint32_t zz = ((z[i][b] >> (4 * (r16 & 1))) & 0xFu) * 0x01010101u;
+          unpack_unit(d[i][b], zz, lo[b], hi[b]);
+          sc[b] = s[i][b];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint8_t* frag = buf + (m * SG + i) * 2048 + 16 * lane;
+          const v4i a0 = *reinterpret_cast<const v4i*>(frag);
+          const v4i a1 = *reinterpret_cast<const v4i*>(frag + 1024);
+#pragma unroll
+          for (int b = 0; b < NBK; ++b) {
+            v4i p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, lo[b], kBiasSeed, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, hi[b], p, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[b][m][r] += sc[b] * unbias(p[r]);
+          }
+        }
+      }
+      load(i, i < nlive ? nt + i : T);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (wrap) {
+      if (col < nc) {
+        const int c = c0 + col;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * m + 4 * j + r;
+            if (row >= w.rows) continue;
+            if constexpr (OUT == kSwiglu)
+              a.h[(int64_t)s_pair[row] * (16 * a.cols) + 16 * c + r16] = f32_to_bf16_rne(
+                  silu_mul(s_scale[row] * acc[0][m][r], s_scale[row] * acc[1][m][r]));
+            else if constexpr (OUT == kParts)
+              a.parts[(int64_t)s_pair[row] * (16 * a.nbe) + 16 * c + r16] =
+                  s_scale[row] * a.pw[s_pair[row]] * acc[0][m][r];
+            else
+              a.parts[((int64_t)blockIdx.y * a.M + w.first + row) * (16 * a.nbe) + 16 * c + r16] =
+                  acc[0][m][r];
+          }
+        clear();
+      }
+    }
+    sl = nsl;
+    col = ncol;
+  }
 }
 
 // ----------------------------------------------------------- many rows
@@ -663,8 +865,7 @@ hipError_t stream_launch(const RowsArgs& a, int64_t blocks, int ksplit, hipStrea
 hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int out, int64_t blocks,
                               int ksplit, hipStream_t st) {
   // what the kernel stages per slice
-  if (act == kCodes && a.sg * (one ? 8 : 128 * mt) > kThreads * (one ? 1 : kStageChunks))
-    return hipErrorInvalidValue;
+  if (act == kCodes && a.sg * 128 * mt > kThreads * kStageChunks) return hipErrorInvalidValue;
 #define ROWS_CASE(MTV, ONEV, ACTV, OUTV) \
   if (mt == MTV && one == ONEV && act == ACTV && out == OUTV) \
     return stream_launch<MTV, ONEV, ACTV, OUTV>(a, blocks, ksplit, st);
@@ -677,14 +878,33 @@ hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int 
   ROWS_CASE(1, false, kCodes, kParts)
   ROWS_CASE(2, false, kCodes, kParts)
   ROWS_CASE(4, false, kCodes, kParts)
-  ROWS_CASE(1, true, kCodes, kSplit)
-  ROWS_CASE(1, true, kCodes, kAdapt)
   ROWS_CASE(1, false, kCodes, kSplit)
   ROWS_CASE(2, false, kCodes, kSplit)
   ROWS_CASE(3, false, kCodes, kSplit)
   ROWS_CASE(4, false, kCodes, kSplit)
   ROWS_CASE(1, false, kCodes, kAdapt)
 #undef ROWS_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_rows_run(const RowsArgs& a, int mt, int out, int64_t blocks, int ksplit, hipStream_t st) {
+#define RUN_CASE(MTV, OUTV)                                                                      \
+  if (mt == MTV && out == OUTV) {                                                                \
+    hipLaunchKernelGGL((rows_run_kernel<MTV, OUTV>), dim3((unsigned)blocks, (unsigned)ksplit),   \
+                       dim3(kThreads), 2 * (size_t)run_groups(MTV, OUTV) * MTV * 2048, st, a);   \
+    return hipGetLastError();                                                                    \
+  }
+  RUN_CASE(1, kSwiglu)
+  RUN_CASE(2, kSwiglu)
+  RUN_CASE(4, kSwiglu)
+  RUN_CASE(1, kParts)
+  RUN_CASE(2, kParts)
+  RUN_CASE(4, kParts)
+  RUN_CASE(1, kSplit)
+  RUN_CASE(2, kSplit)
+  RUN_CASE(3, kSplit)
+  RUN_CASE(4, kSplit)
+#undef RUN_CASE
   return hipErrorInvalidValue;
 }
 

@@ -219,6 +219,19 @@ hipError_t launch_w8_pack(const int8_t* qw, const float* sw, int64_t N, int64_t 
 hipError_t launch_w8_unpack(const uint8_t* packed, int64_t N, int64_t K, int8_t* qw, float* sw,
                             hipStream_t st);
 
+// The adapters of a call: y[m] += scale[l] * (x[m] A[l]^T) B[l]^T, l = ids[m];
+// rows whose id lies outside [0, L) have none.  hx: the sums x A^T of the
+// call, [slices][M][R], not yet scaled.
+struct AdaptArgs {
+  const float* hx;
+  const uint16_t* B;
+  const float* scale;
+  const int* ids;
+  int slices, L, R;
+};
+
+constexpr int kMaxRank = 128;  // of an adapter
+
 struct GemmArgs {
   const int8_t* qa;       // quantised activations [M][K] (null when x is quantised in-kernel)
   const float* sa;        // per-token scales [M]
@@ -251,6 +264,9 @@ struct GemmArgs {
   // qa in the [K / 16][16 rows][16 B] layout of launch_quant_tiled (skinny
   // kernel, 12 <= M <= 16, no debug)
   bool qa_tiled = false;
+  // the GEMV's fused token with a low-rank adapter added in the epilogue
+  // (ad.hx set); with ksplit > 1 the reduction adds it instead
+  AdaptArgs ad = {};
 };
 
 // Largest K the GEMV keeps in LDS (activation codes + per-quarter sums).
