@@ -52,6 +52,7 @@ rows_stream_kernel(RowsArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int s_pair[BM];
   __shared__ float s_scale[BM], s_max[kWaves];
+  __shared__ float s_weight[OUT == kParts ? BM : 1];  // of the pairs
   // kAdapt: scaled x A^T of the rows, and the rows' adapter products
   __shared__ float s_hx[OUT == kAdapt ? BM * kMaxRank : 1];
   __shared__ float s_dot[OUT == kAdapt ? kWaves : 1][OUT == kAdapt ? 4 : 1][64];
@@ -96,6 +97,9 @@ rows_stream_kernel(RowsArgs a) {
     const int p = pair_of(a, w, tid);
     s_pair[tid] = p;
     if constexpr (ACT == kCodes) s_scale[tid] = a.sa[p / a.div];
+    // (here, not where a column ends: a load there waits for the weights that
+    // are in flight by then; expert down product of 64 tokens 24 -> DOWN64_US)
+    if constexpr (OUT == kParts) s_weight[tid] = a.pw[p];
   }
 
   float acc[NBK][MT][4];
@@ -120,7 +124,7 @@ rows_stream_kernel(RowsArgs a) {
               f32_to_bf16_rne(silu_mul(s * acc[0][m][r], s * acc[1][m][r]));
         } else if constexpr (OUT == kParts) {
           a.parts[(int64_t)s_pair[row] * (16 * a.nbe) + 16 * c + r16] =
-              s_scale[row] * a.pw[s_pair[row]] * acc[0][m][r];
+              s_scale[row] * s_weight[row] * acc[0][m][r];
         } else if constexpr (OUT == kSplit) {
           a.parts[((int64_t)blockIdx.y * a.M + w.first + row) * (16 * a.nbe) + 16 * c + r16] =
               acc[0][m][r];
@@ -381,20 +385,16 @@ rows_stream_kernel(RowsArgs a) {
 // last of a column may have fewer); a slot without a unit loads nothing.
 // (517 tokens, 32 experts, 3584 -> 2 x 1280: RUN_US, against 73 us when every
 // slice drained the ring and waited for its activations.)
-template <int MT, int OUT>
-__global__ void __launch_bounds__(kThreads, 4)
-rows_run_kernel(RowsArgs a) {
-  constexpr int BM = 16 * MT;
+// ML: the 16-row fragments that the tile's rows reach (a tile of at most 16
+// MT rows often has fewer).
+template <int ML, int MT, int OUT>
+__device__ __forceinline__ void run_tile(const RowsArgs& a, const Where& w, uint8_t* smem, int* s_pair,
+                                         uint32_t* s_off, float* s_scale) {
+  constexpr int BM = 16 * ML;
   constexpr int NBK = OUT == kSwiglu ? 2 : 1;
   constexpr int SG = run_groups(MT, OUT);
   constexpr int kSlice = SG * MT * 2048;  // bytes of a buffer
-  constexpr int kDma = kSlice / (kThreads * 16);
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int s_pair[BM];
-  __shared__ float s_scale[BM];
-
-  Where w;
-  if (!locate<BM>(a, w)) return;
+  static_assert(SG % 4 == 0, "a whole number of loads per wavefront");
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int r16 = lane & 15, j = lane >> 4;
   const int G = a.K / kGroup;
@@ -404,30 +404,34 @@ rows_run_kernel(RowsArgs a) {
   const int columns = min(a.ncol, a.cols - w.strip * kWaves * a.ncol);  // of the first wavefront
   const int S = (Gs + SG - 1) / SG, L = (Gs + S - 1) / S;
 
-  int src[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = 16 * m + r16;
-    src[m] = row < w.rows ? pair_of(a, w, row) / a.div : -1;
-  }
+  // slice s of the activations into a buffer, [MT][SG][2 halves][64 lanes]
+  // [16 B]: of the 2 SG KiB of 16 rows this wavefront loads KiB wave, wave + 8
+  // (the rows' offsets wait in LDS: kept in registers they were spilled, and
+  // a reload from memory queues behind the weights in flight)
+  constexpr int kPer = SG / 4;
   const LdsSource rqa = lds_source(a.qa, a.src_rows * a.K);
-  if (tid < w.rows) {
-    const int p = pair_of(a, w, tid);
-    s_pair[tid] = p;
-    s_scale[tid] = a.sa[p / a.div];
+  if (tid < BM) {
+    int off = kOob;
+    if (tid < w.rows) {
+      const int p = pair_of(a, w, tid), src = p / a.div;
+      off = src * a.K + gb * kGroup;
+      s_pair[tid] = p;
+      s_scale[tid] = OUT == kParts ? a.sa[src] * a.pw[p] : a.sa[src];
+    }
+    s_off[tid] = off;
   }
-  // slice s of the activations into a buffer: [MT][SG][2 halves][64 lanes][16 B]
   auto stage = [&](uint8_t* buf, int s) __attribute__((always_inline)) {
-    const int live = min(L, Gs - s * L);
+    const int live = 2 * min(L, Gs - s * L);
+    uint32_t off[ML];
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) {
-      const int c = wave + i * kWaves;  // KiB of the buffer
-      const int h = c & 1, g = (c >> 1) % SG, m = (c >> 1) / SG;
-      int sr = src[0];
+    for (int m = 0; m < ML; ++m) off[m] = s_off[16 * m + r16] + 64 * wave + 16 * j;
 #pragma unroll
-      for (int t = 1; t < MT; ++t) sr = m == t ? src[t] : sr;
-      const int off = sr >= 0 && g < live ? sr * a.K + (gb + s * L + g) * kGroup + 64 * h + 16 * j : kOob;
-      load_to_lds(rqa, buf + c * 1024, off, 0);
+    for (int i = 0; i < kPer; ++i) {
+      const int c = wave + i * kWaves;
+      if (c >= live) break;
+#pragma unroll
+      for (int m = 0; m < ML; ++m)
+        load_to_lds(rqa, buf + (m * 2 * SG + c) * 1024, (int)off[m], s * L * kGroup + i * kWaves * 64);
     }
   };
 
@@ -456,16 +460,17 @@ rows_run_kernel(RowsArgs a) {
     }
   };
 
-  float acc[NBK][MT][4];
+  float acc[NBK][ML][4];
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < NBK; ++b)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < ML; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[b][m][r] = 0.0f;
   };
   clear();
+  lds_barrier();
   stage(smem, 0);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -498,7 +503,7 @@ rows_run_kernel(RowsArgs a) {
           sc[b] = s[i][b];
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < ML; ++m) {
           const uint8_t* frag = buf + (m * SG + i) * 2048 + 16 * lane;
           const v4i a0 = *reinterpret_cast<const v4i*>(frag);
           const v4i a1 = *reinterpret_cast<const v4i*>(frag + 1024);
@@ -517,18 +522,19 @@ rows_run_kernel(RowsArgs a) {
     if (wrap) {
       if (col < nc) {
         const int c = c0 + col;
+        int first = 4 * j;
+        asm volatile("" : "+v"(first));  // nothing of the rows' addresses is kept over the loop
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < ML; ++m)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int row = 16 * m + 4 * j + r;
+            const int row = 16 * m + first + r;
             if (row >= w.rows) continue;
             if constexpr (OUT == kSwiglu)
               a.h[(int64_t)s_pair[row] * (16 * a.cols) + 16 * c + r16] = f32_to_bf16_rne(
                   silu_mul(s_scale[row] * acc[0][m][r], s_scale[row] * acc[1][m][r]));
             else if constexpr (OUT == kParts)
-              a.parts[(int64_t)s_pair[row] * (16 * a.nbe) + 16 * c + r16] =
-                  s_scale[row] * a.pw[s_pair[row]] * acc[0][m][r];
+              a.parts[(int64_t)s_pair[row] * (16 * a.nbe) + 16 * c + r16] = s_scale[row] * acc[0][m][r];
             else
               a.parts[((int64_t)blockIdx.y * a.M + w.first + row) * (16 * a.nbe) + 16 * c + r16] =
                   acc[0][m][r];
@@ -539,6 +545,25 @@ rows_run_kernel(RowsArgs a) {
     sl = nsl;
     col = ncol;
   }
+}
+
+template <int MT, int OUT>
+__global__ void __launch_bounds__(kThreads, 4)
+rows_run_kernel(RowsArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int s_pair[16 * MT];
+  __shared__ uint32_t s_off[16 * MT];
+  __shared__ float s_scale[16 * MT];
+  Where w;
+  if (!locate<16 * MT>(a, w)) return;
+  if (MT == 1 || w.rows <= 16)
+    run_tile<1, MT, OUT>(a, w, smem, s_pair, s_off, s_scale);
+  else if (MT == 2 || w.rows <= 32)
+    run_tile<MT < 2 ? MT : 2, MT, OUT>(a, w, smem, s_pair, s_off, s_scale);
+  else if (MT == 3 || w.rows <= 48)
+    run_tile<MT < 3 ? MT : 3, MT, OUT>(a, w, smem, s_pair, s_off, s_scale);
+  else
+    run_tile<MT, MT, OUT>(a, w, smem, s_pair, s_off, s_scale);
 }
 
 // ----------------------------------------------------------- many rows

@@ -1,0 +1,99 @@
+"""GPU: the expert MLP and the adapter linear where a tile's activations pass
+through LDS in slices: many groups of input channels for every tile height,
+with slices that do not divide them, several columns to a wavefront, rows that
+leave parts of a tile empty, and columns past the last strip.
+
+Tolerances as in test_gpu_rows.py, whose definitions and checks these use.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_rows import (acts, check_lora, check_moe, lora_case, moe_case, moe_ref, pack,  # noqa: E402
+                           w4)  # noqa: F401
+
+MOE = [
+    # M, k, E, I, K: up to 16, 32 and 64 rows a tile
+    (20, 2, 8, 128, 4352), (12, 1, 3, 4224, 256), (23, 2, 6, 4352, 4224),
+    (60, 2, 8, 128, 2304), (60, 2, 8, 2304, 128), (41, 3, 7, 2176, 2432),
+    (100, 3, 6, 128, 1280), (100, 3, 6, 1152, 128), (75, 4, 8, 1408, 1664), (130, 2, 5, 1280, 2688),
+]
+
+
+@pytest.mark.parametrize("M,k,E,I,K", MOE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_moe_sliced(w4, M, k, E, I, K, dtype):  # noqa: F811
+    x, up, down, ids, wt = moe_case(M + K, M, k, E, I, K, dtype, drop=0.2, skew=M % 2 == 1)
+    y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
+    check_moe(y, *moe_ref(x, up, down, ids, wt, E))
+
+
+LORA = [
+    # M, K, N, L, R, seg: two, three and four 16-row fragments, K in two slices
+    (20, 4608, 32784, 3, 8, 1), (45, 2816, 32784, 4, 72, 3), (61, 2304, 32784, 5, 32, 1),
+    # the single token: K whole, K split over workgroups, a long token, many channels
+    (1, 3584, 3584, 3, 128, 1), (1, 18944, 3584, 2, 72, 1), (1, 8192, 512, 2, 8, 1), (1, 256, 50000, 2, 40, 1),
+    (1, 36864, 256, 2, 16, 1),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,R,seg", LORA)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_lora_sliced(w4, M, K, N, L, R, seg, dtype):  # noqa: F811
+    x, w, A, B, sc, ids = lora_case(M + N, M, K, N, L, R, dtype, seg)
+    if M == 1:
+        ids.clamp_(min=0)
+    W = w4.pack_weights(*w)
+    check_lora(w4.lora_linear(x, W, w4.LoraAdapters(A, B, sc), ids), x, w, A, B, sc, ids)
+    if M == 1:
+        ids.fill_(-1)
+        check_lora(w4.lora_linear(x, W, w4.LoraAdapters(A, B, sc), ids), x, w, A, B, sc, ids)
+
+
+def near_scores(g, M, E, kind):
+    """Logits whose sigmoids, with the bias, lie next to each other: equal ones,
+    neighbours in float32, and ones that round to one float32."""
+    base = torch.randn(M, 1, generator=g, device="cuda")
+    if kind == "equal":
+        l = base.expand(M, E).clone()
+    elif kind == "neighbours":
+        l = base.repeat(1, E)
+        step = torch.randint(0, 3, (M, E), generator=g, device="cuda").float()
+        l = l * (1 + step * 2.0 ** -23)
+    else:
+        l = base + torch.rand(M, E, generator=g, device="cuda") * 1e-5
+    return l.contiguous()
+
+
+@pytest.mark.parametrize("kind", ["equal", "neighbours", "close"])
+@pytest.mark.parametrize("E,n_groups,group_top", [(64, 1, 1), (96, 4, 2), (63, 7, 2), (250, 10, 2), (1023, 33, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_next_to_a_border(w4, kind, E, n_groups, group_top, score):  # noqa: F811
+    """Choices that float32 scores cannot decide; the definition of
+    test_gpu_rows.py decides them in 64 bits.  Sums of two scores that differ
+    by less than 64-bit rounding cannot occur: the inputs are float32."""
+    from test_gpu_rows import route_ref
+    M, k = 9, 5
+    g = torch.Generator(device="cuda").manual_seed(E)
+    l = near_scores(g, M, E, kind)
+    # a bias of a few values, exact in every sum
+    bias = torch.randint(0, 2, (E,), generator=g, device="cuda").float() * 0.25
+    if kind != "equal" and score == "softmax":
+        # the 64-bit softmax of the definition and the kernel's may round the
+        # last bit apart; spread the logits so that no choice hangs on it
+        l = l + torch.arange(E, device="cuda") % 7 * 2.0 ** -12
+    kw = dict(score=score, n_groups=n_groups, topk_groups=max(1, n_groups // 2), group_top=group_top,
+              renormalize=True, scale=1.0)
+    ids, w = w4.moe_route(l, k, bias=bias, **kw)
+    rid, rw = route_ref(l, k, score, bias, n_groups, kw["topk_groups"], group_top, True, 1.0)
+    if kind == "equal":
+        assert torch.equal(ids.cpu(), rid)
+    else:
+        # the chosen values in order, as the definition's; equal values may sit
+        # at other indices only where 64-bit scores agree to the last bits
+        p = torch.softmax(l.double().cpu(), 1) if score == "softmax" else torch.sigmoid(l.double().cpu())
+        c = p + bias.double().cpu()
+        a, b = c.gather(1, ids.cpu().long()), c.gather(1, rid.long())
+        assert ((a - b).abs() <= 2.0 ** -50).all()
+    assert ((w.cpu().double() - rw).abs() <= (E + 16) * 2.0 ** -24 * rw.abs()).all()
