@@ -25,9 +25,10 @@ struct LoraPlan {
   int mt = 0;      // 16-row tiles of the streaming kernel; 0: the 256-row tile kernel
   int kw = 0;      // streaming kernel: log2 wavefronts per column
   int ksplit = 1;  // K slices across workgroups (float sums, then a reduction)
+  bool sorted = false;  // rows taken in the order of their adapters
   int slots = 1;   // workgroups that share a 16-row fragment's adapters
   int slices = 1;  // K slices of x A^T
-  int64_t qa = 0, sa = 0, hx = 0, parts = 0;
+  int64_t qa = 0, sa = 0, hx = 0, order = 0, hi = 0, lo = 0, parts = 0;
   int64_t bytes = 0;
 };
 

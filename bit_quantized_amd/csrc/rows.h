@@ -51,7 +51,7 @@ struct RowsArgs {
   const float* scales;
   const int* ntiles;     // kPlanned
   const RowTile* tiles;
-  const int* list;
+  const int* list;       // null: the pairs (rows) as they are
   const int* ids;        // kDirect: the pairs' experts
   int n_experts;
   int kind;
@@ -157,7 +157,7 @@ __device__ __forceinline__ bool locate(const RowsArgs& a, Where& w) {
 
 // Pair (or row) i of the tile.
 __device__ __forceinline__ int pair_of(const RowsArgs& a, const Where& w, int i) {
-  return a.kind == kPlanned ? a.list[w.first + i] : w.first + i;
+  return a.list ? a.list[w.first + i] : w.first + i;
 }
 
 // Eight consecutive raw activations as float.

@@ -98,7 +98,7 @@ rows_stream_kernel(RowsArgs a) {
     s_pair[tid] = p;
     if constexpr (ACT == kCodes) s_scale[tid] = a.sa[p / a.div];
     // (here, not where a column ends: a load there waits for the weights that
-    // are in flight by then; expert down product of 64 tokens 24 -> DOWN64_US)
+    // are in flight by then; expert down product of 64 tokens 24 -> 22 us)
     if constexpr (OUT == kParts) s_weight[tid] = a.pw[p];
   }
 
@@ -383,7 +383,7 @@ rows_stream_kernel(RowsArgs a) {
 // that the slices do not interrupt: slot i holds unit i of a slice and is
 // refilled with unit i of the next one.  Slices have L <= SG units each (the
 // last of a column may have fewer); a slot without a unit loads nothing.
-// (517 tokens, 32 experts, 3584 -> 2 x 1280: RUN_US, against 73 us when every
+// (517 tokens, 32 experts, 3584 -> 2 x 1280: 53 us, against 73 when every
 // slice drained the ring and waited for its activations.)
 // ML: the 16-row fragments that the tile's rows reach (a tile of at most 16
 // MT rows often has fewer).
@@ -751,7 +751,7 @@ rows_tile_kernel(RowsArgs a) {
       loads_done<0>();
       __syncthreads();
     }
-    if constexpr (OUT != kAdapt) return;
+    return;
   }
   // One group from `cur` while the next one's operands go into `next`, which
   // was last read before the previous barrier.
@@ -764,11 +764,10 @@ rows_tile_kernel(RowsArgs a) {
     loads_done<0>();
     __syncthreads();
   };
-  if (works)
-    for (int g = gb; g < ge; g += 2) {
-      step(smem[0], smem[1], g);
-      if (g + 1 < ge) step(smem[1], smem[0], g + 1);
-    }
+  for (int g = gb; g < ge; g += 2) {
+    step(smem[0], smem[1], g);
+    if (g + 1 < ge) step(smem[1], smem[0], g + 1);
+  }
 
   if constexpr (OUT == kAdapt) {
     // sums scaled, then each adapter's product added on the bf16 matrix
@@ -776,7 +775,9 @@ rows_tile_kernel(RowsArgs a) {
     // rows as two bf16 parts (16 significant bits) against B.  The product is
     // made apart and added to the adapter's own rows only, so what B holds
     // (an infinity, a NaN) reaches no other row.  The int8 and bf16 products
-    // share one result layout.
+    // share one result layout.  (2048 rows, 16 adapters of rank 32, 3584 ->
+    // 18944: 238 us, of which the epilogue is about 25; 270 us with x A^T
+    // summed and split here, by every strip of channels again.)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -786,62 +787,55 @@ rows_tile_kernel(RowsArgs a) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) acc[i][u][r] *= s;
       }
-    // The parts lie in the tile's LDS (the loop's last barrier has passed), 64
-    // ranks at a time: [2][256 rows][64 + 8], the pad keeping the rows of a
-    // fragment on different banks.
-    constexpr int kRanks = 64, kLd = kRanks + 8;
-    static_assert(2 * kTileRows * kLd * 2 <= 2 * kBufBytes, "fits the tile's buffers");
-    uint16_t* parts_lds = reinterpret_cast<uint16_t*>(&smem[0][0]);
-    for (int rb = 0; rb < a.ad.R; rb += kRanks) {
-      const int rn = min(kRanks, a.ad.R - rb);
-      if (rb) __syncthreads();  // the last ranks' reads are done
-      for (int q = tid; q < w.rows * rn; q += kThreads) {
-        const int row = q / rn, r = q - row * rn;
-        const int id = s_id[row];
-        if (id < 0) continue;
-        const float v = adapter_sum(a.ad, a.M, w.first + row, rb + r, a.ad.scale[id]);
-        const uint16_t hb = f32_to_bf16_rne(v);
-        parts_lds[row * kLd + r] = hb;
-        parts_lds[(kTileRows + row) * kLd + r] = f32_to_bf16_rne(v - __uint_as_float((uint32_t)hb << 16));
-      }
-      __syncthreads();
-      if (!works) continue;
+    for (int r0 = 0; r0 < a.ad.R; r0 += 32) {
+      const int rr = r0 + 8 * j;  // this lane's eight ranks
+      int held = -1;              // the adapter whose B is in bv
+      v4i bv[8], ah[4], al[4];
+      int id[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = wm * 64 + i * 16 + r16;
-        const int id = row < w.rows ? s_id[row] : -1;
-        uint64_t todo = __ballot(id >= 0) & 0xFFFFull;
+        id[i] = row < w.rows ? s_id[row] : -1;
+        ah[i] = al[i] = v4i{0, 0, 0, 0};
+        if (id[i] >= 0 && rr < a.ad.R) {
+          const int64_t at = (int64_t)s_pair[row] * a.ad.R + rr;
+          ah[i] = *reinterpret_cast<const v4i*>(a.ad.hi + at);
+          al[i] = *reinterpret_cast<const v4i*>(a.ad.lo + at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint64_t todo = __ballot(id[i] >= 0) & 0xFFFFull;
         while (todo) {
-          const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-          const uint64_t rows = __ballot(id == l) & 0xFFFFull;
+          const int l = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
+          const uint64_t rows = __ballot(id[i] == l) & 0xFFFFull;
           todo &= ~rows;
-          for (int r0 = 0; r0 < rn; r0 += 32) {
-            const int rr = r0 + 8 * j;  // this lane's eight ranks
-            v4i ah = {0, 0, 0, 0}, al = {0, 0, 0, 0};
-            if (id == l && rr < rn) {
-              ah = *reinterpret_cast<const v4i*>(parts_lds + row * kLd + rr);
-              al = *reinterpret_cast<const v4i*>(parts_lds + (kTileRows + row) * kLd + rr);
-            }
+          if (l != held) {  // (the rows come in the order of their adapters)
+            held = l;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const int nb = min(w.strip * 16 + wn * 8 + u, NB - 1);
-              v4i bv = {0, 0, 0, 0};
-              if (rr < rn)
-                bv = *reinterpret_cast<const v4i*>(
-                    a.ad.B + (((int64_t)l * NB + nb) * 16 + r16) * a.ad.R + rb + rr);
-              v4f_rows c = {0.f, 0.f, 0.f, 0.f};
-              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, ah),
-                                                          __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
-              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, al),
-                                                          __builtin_bit_cast(v8bf_rows, bv), c, 0, 0, 0);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i][u][r] += (rows >> (4 * j + r)) & 1 ? c[r] : 0.0f;
+              bv[u] = v4i{0, 0, 0, 0};
+              if (rr < a.ad.R)
+                bv[u] = *reinterpret_cast<const v4i*>(
+                    a.ad.B + (((int64_t)l * NB + nb) * 16 + r16) * a.ad.R + rr);
             }
+          }
+          const v4i zero = {0, 0, 0, 0};
+          const v4i h = id[i] == l ? ah[i] : zero, lw = id[i] == l ? al[i] : zero;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            v4f_rows c = {0.f, 0.f, 0.f, 0.f};
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, h),
+                                                        __builtin_bit_cast(v8bf_rows, bv[u]), c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, lw),
+                                                        __builtin_bit_cast(v8bf_rows, bv[u]), c, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][u][r] += (rows >> (4 * j + r)) & 1 ? c[r] : 0.0f;
           }
         }
       }
     }
-    if (!works) return;
   }
 
 #pragma unroll

@@ -221,9 +221,11 @@ hipError_t launch_w8_unpack(const uint8_t* packed, int64_t N, int64_t K, int8_t*
 
 // The adapters of a call: y[m] += scale[l] * (x[m] A[l]^T) B[l]^T, l = ids[m];
 // rows whose id lies outside [0, L) have none.  hx: the sums x A^T of the
-// call, [slices][M][R], not yet scaled.
+// call, [slices][M][R], not yet scaled; hi, lo: scaled, as two bf16 planes
+// [M][R] (rows taken in the order of their adapters only).
 struct AdaptArgs {
   const float* hx;
+  const uint16_t *hi, *lo;
   const uint16_t* B;
   const float* scale;
   const int* ids;

@@ -32,6 +32,12 @@ def test_moe_sliced(w4, M, k, E, I, K, dtype):  # noqa: F811
 LORA = [
     # M, K, N, L, R, seg: two, three and four 16-row fragments, K in two slices
     (20, 4608, 32784, 3, 8, 1), (45, 2816, 32784, 4, 72, 3), (61, 2304, 32784, 5, 32, 1),
+    # rows taken in the order of their adapters: more adapters than buckets of that order, few
+    # rows over many channels, ranks past 64, all with K whole and in slices
+    (90, 256, 272, 2000, 8, 1), (300, 1152, 272, 1500, 16, 1), (64, 256, 18960, 64, 64, 1),
+    (700, 256, 4112, 9, 72, 1), (300, 1024, 1040, 16, 128, 1), (517, 384, 2064, 3, 128, 11),
+    # eight wavefronts to a column, with rows that end inside the fragment
+    (16, 3584, 2064, 5, 72, 1), (11, 1152, 3584, 16, 128, 1), (2, 4096, 4096, 2, 8, 1), (9, 4224, 2304, 4, 24, 1),
     # the single token: K whole, K split over workgroups, a long token, many channels
     (1, 3584, 3584, 3, 128, 1), (1, 18944, 3584, 2, 72, 1), (1, 8192, 512, 2, 8, 1), (1, 256, 50000, 2, 40, 1),
     (1, 36864, 256, 2, 16, 1),
