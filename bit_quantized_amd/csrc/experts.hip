@@ -11,45 +11,61 @@ constexpr int kWaves = kThreads / 64;
 
 // ------------------------------------------------ grouping + quantisation
 //
-// Workgroup 0 groups the pairs: a histogram of the experts in LDS, prefix
-// sums, the tiles of at most BM pairs of one expert each, then the pairs in
-// expert order.  The place of a pair inside its expert follows the order of
-// LDS atomics and may differ between calls; no output depends on it (rows.h).
-// The other workgroups quantise one token each (w4a8_quant_act's rule).
-template <int ACT>
-__global__ void __launch_bounds__(kThreads)
-group_kernel(const void* __restrict__ x, const int* __restrict__ ids, int P, int E, int bm, int K,
-             int8_t* __restrict__ qa, float* __restrict__ sa, int* __restrict__ ntiles,
-             RowTile* __restrict__ tiles, int* __restrict__ list, int* __restrict__ rank) {
-  __shared__ float red[kWaves];
-  __shared__ int s_count[kMaxExperts], s_first[kMaxExperts], s_tile[kMaxExperts];
-  const int tid = threadIdx.x, lane = tid & 63;
-  if (blockIdx.x > 0) {
-    const int64_t m = blockIdx.x - 1;
-    quantise_row<ACT, kThreads>(static_cast<const uint8_t*>(x) + m * K * RawRow<ACT>::kBytes, K, qa + m * K,
-                      sa + m, red);
-    return;
-  }
-  for (int e = tid; e < E; e += kThreads) s_count[e] = 0;
+// The pairs in expert order, and the tiles of at most bm pairs of one expert
+// each.  Up to kOnePlace pairs a single workgroup does it: a histogram of the
+// experts in LDS, prefix sums, tiles and list.  More pairs are counted by
+// `counters` workgroups, a run of pairs each, and placed by as many of a second
+// launch, which sum the counts before theirs (24576 pairs: 18 us with the
+// quantisation beside it, against 29 with one workgroup).  The place of a
+// pair inside its expert follows the order of LDS atomics and may differ
+// between calls; no output depends on it (rows.h).  The other workgroups
+// quantise one token each (w4a8_quant_act's rule).
+constexpr int64_t kOnePlace = 4096;
+constexpr int kMostCounters = 64;
+int counters_of(int64_t P) {
+  const int64_t n = P <= kOnePlace ? 1 : (P + 1023) / 1024;
+  return (int)(n < kMostCounters ? n : kMostCounters);
+}
+
+struct GroupArgs {
+  const int* ids;
+  int P, E, bm, counters;
+  int* ntiles;
+  RowTile* tiles;
+  int *list, *rank;
+  int* counts;  // [counters][E]
+};
+
+// Counts of pairs [p0, p1) into s_count, and each one's place among them.
+constexpr int kAtOnce = 8;
+__device__ __forceinline__ void count_pairs(const GroupArgs& g, int p0, int p1, int* s_count) {
+  for (int e = threadIdx.x; e < g.E; e += kThreads) s_count[e] = 0;
   __syncthreads();
-  constexpr int kAtOnce = 8;
-  for (int p0 = tid; p0 < P; p0 += kAtOnce * kThreads) {
+  for (int p = p0 + threadIdx.x; p < p1; p += kAtOnce * kThreads) {
     int e[kAtOnce], r[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) e[i] = p0 + i * kThreads < P ? ids[p0 + i * kThreads] : -1;
+    for (int i = 0; i < kAtOnce; ++i) e[i] = p + i * kThreads < p1 ? g.ids[p + i * kThreads] : -1;
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) r[i] = e[i] >= 0 && e[i] < E ? atomicAdd(&s_count[e[i]], 1) : 0;
+    for (int i = 0; i < kAtOnce; ++i) r[i] = e[i] >= 0 && e[i] < g.E ? atomicAdd(&s_count[e[i]], 1) : 0;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-      if (p0 + i * kThreads < P) rank[p0 + i * kThreads] = r[i];
+      if (p + i * kThreads < p1) g.rank[p + i * kThreads] = r[i];
   }
   __syncthreads();
+}
+
+// From the experts' counts: first places and tiles (written where `write`);
+// then the list entries of pairs [p0, p1), whose run has s_before[e] pairs of
+// expert e before it (null: none).
+__device__ __forceinline__ void place_pairs(const GroupArgs& g, int p0, int p1, bool write, const int* s_count,
+                                            const int* s_before, int* s_first, int* s_tile) {
+  const int tid = threadIdx.x, lane = tid & 63;
   if (tid < 64) {  // prefix sums of pairs and tiles, E / 64 experts per lane
-    const int per = (E + 63) / 64, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+    const int per = (g.E + 63) / 64, e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
     int pairs = 0, nt = 0;
     for (int e = e0; e < e1; ++e) {
       pairs += s_count[e];
-      nt += (s_count[e] + bm - 1) / bm;
+      nt += (s_count[e] + g.bm - 1) / g.bm;
     }
     int ps = pairs, ts = nt;
 #pragma unroll
@@ -60,34 +76,117 @@ group_kernel(const void* __restrict__ x, const int* __restrict__ ids, int P, int
         ts += b;
       }
     }
-    if (lane == 63) ntiles[0] = ts;
+    if (write && lane == 63) g.ntiles[0] = ts;
     ps -= pairs;
     ts -= nt;
     for (int e = e0; e < e1; ++e) {
       s_first[e] = ps;
       s_tile[e] = ts;
       ps += s_count[e];
-      ts += (s_count[e] + bm - 1) / bm;
+      ts += (s_count[e] + g.bm - 1) / g.bm;
     }
   }
   __syncthreads();
-  for (int e = tid >> 6; e < E; e += kWaves) {
-    const int c = s_count[e], n = (c + bm - 1) / bm;
-    for (int i = lane; i < n; i += 64)
-      tiles[s_tile[e] + i] = RowTile{e, s_first[e] + i * bm, min(bm, c - i * bm), i | (n << 16)};
-  }
-  for (int p0 = tid; p0 < P; p0 += kAtOnce * kThreads) {
+  if (write)
+    for (int e = tid >> 6; e < g.E; e += kWaves) {
+      const int c = s_count[e], n = (c + g.bm - 1) / g.bm;
+      for (int i = lane; i < n; i += 64)
+        g.tiles[s_tile[e] + i] = RowTile{e, s_first[e] + i * g.bm, min(g.bm, c - i * g.bm), i | (n << 16)};
+    }
+  for (int p = p0 + tid; p < p1; p += kAtOnce * kThreads) {
     int e[kAtOnce], r[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const int p = p0 + i * kThreads;
-      e[i] = p < P ? ids[p] : -1;
-      r[i] = p < P ? rank[p] : 0;
+      const int q = p + i * kThreads;
+      e[i] = q < p1 ? g.ids[q] : -1;
+      r[i] = q < p1 ? g.rank[q] : 0;
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-      if (e[i] >= 0 && e[i] < E) list[s_first[e[i]] + r[i]] = p0 + i * kThreads;
+      if (e[i] >= 0 && e[i] < g.E)
+        g.list[s_first[e[i]] + (s_before ? s_before[e[i]] : 0) + r[i]] = p + i * kThreads;
   }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kThreads)
+group_kernel(const void* __restrict__ x, int K, int8_t* __restrict__ qa, float* __restrict__ sa, GroupArgs g) {
+  __shared__ float red[kWaves];
+  __shared__ int s_count[kMaxExperts], s_first[kMaxExperts], s_tile[kMaxExperts];
+  if ((int)blockIdx.x >= g.counters) {
+    const int64_t m = blockIdx.x - g.counters;
+    quantise_row<ACT, kThreads>(static_cast<const uint8_t*>(x) + m * K * RawRow<ACT>::kBytes, K, qa + m * K,
+                                sa + m, red);
+    return;
+  }
+  const int b = blockIdx.x, per = (g.P + g.counters - 1) / g.counters;
+  const int p0 = min(b * per, g.P), p1 = min(p0 + per, g.P);
+  count_pairs(g, p0, p1, s_count);
+  if (g.counters == 1) {
+    place_pairs(g, p0, p1, true, s_count, nullptr, s_first, s_tile);
+  } else {
+    for (int e = threadIdx.x; e < g.E; e += kThreads) g.counts[b * g.E + e] = s_count[e];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) place_kernel(GroupArgs g) {
+  __shared__ int s_count[kMaxExperts], s_before[kMaxExperts], s_first[kMaxExperts], s_tile[kMaxExperts];
+  const int b = blockIdx.x, per = (g.P + g.counters - 1) / g.counters;
+  const int p0 = min(b * per, g.P), p1 = min(p0 + per, g.P);
+  for (int e = threadIdx.x; e < g.E; e += kThreads) {
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int c = 0; c < g.counters; ++c) {
+      const int v = g.counts[c * g.E + e];
+      all += v;
+      before += c < b ? v : 0;
+    }
+    s_count[e] = all;
+    s_before[e] = before;
+  }
+  __syncthreads();
+  place_pairs(g, p0, p1, b == 0, s_count, s_before, s_first, s_tile);
+}
+
+// ----------------------------------------------- quantisation of h rows
+//
+// One wavefront per pair, its row of at most 64 * 8 * kRowHeld values in
+// registers (w4a8_quant_act's rule); slots of experts held elsewhere are
+// skipped.  24576 rows of 1280: 20 us, against 36 with a workgroup per row.
+constexpr int kRowHeld = 4;
+__global__ void __launch_bounds__(kThreads)
+quant_pairs_kernel(const uint16_t* __restrict__ h, const int* __restrict__ ids, int64_t P, int E, int I,
+                   int8_t* __restrict__ hq, float* __restrict__ hs) {
+  const int lane = threadIdx.x & 63, nch = I / 8;
+  const int64_t p = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6);
+  if (p >= P) return;
+  const int e = uniform(ids[p]);
+  if (e < 0 || e >= E) return;
+  const uint8_t* row = reinterpret_cast<const uint8_t*>(h + p * I);
+  v4u_rows raw[kRowHeld][1];
+#pragma unroll
+  for (int i = 0; i < kRowHeld; ++i)
+    if (lane + 64 * i < nch) RawRow<kRawBf16>::load(row, lane + 64 * i, raw[i]);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRowHeld; ++i)
+    if (lane + 64 * i < nch) {
+      float v[8];
+      RawRow<kRawBf16>::widen(raw[i], v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) amax = fmaxf(amax, fabsf(v[q]));
+    }
+  amax = wave_max64(amax);
+  const float scale = amax / 127.0f, inv = 1.0f / scale;
+  if (lane == 0) hs[p] = scale;
+#pragma unroll
+  for (int i = 0; i < kRowHeld; ++i)
+    if (lane + 64 * i < nch) {
+      float v[8];
+      RawRow<kRawBf16>::widen(raw[i], v);
+      *reinterpret_cast<uint2*>(hq + p * I + 8 * (lane + 64 * i)) =
+          amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+    }
 }
 
 // ------------------------------------------------- down, single tokens
@@ -269,6 +368,7 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
     p.tiles = take(p.max_tiles * (int64_t)sizeof(RowTile));
     p.list = take(P * 4);
     p.rank = take(P * 4);
+    p.counts = take((int64_t)counters_of(P) * E * 4);
     p.hq = take(P * I);
     p.hs = take(P * 4);
     p.parts = take(P * K * 4);
@@ -331,12 +431,14 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
   float* parts = reinterpret_cast<float*>(m.ws + p.parts);
   const int64_t max_tiles = P / p.bm + (m.E < P ? m.E : P);
 
+  const GroupArgs g{m.ids, (int)P, m.E, p.bm, counters_of(P), count, tiles, list, rank,
+                    reinterpret_cast<int*>(m.ws + p.counts)};
+  const dim3 blocks((unsigned)(g.counters + m.M));
   if (m.x_dtype == 0)
-    hipLaunchKernelGGL((group_kernel<kRawBf16>), dim3((unsigned)(1 + m.M)), dim3(kThreads), 0, st, m.x,
-                       m.ids, (int)P, m.E, p.bm, (int)m.K, qa, sa, count, tiles, list, rank);
+    hipLaunchKernelGGL((group_kernel<kRawBf16>), blocks, dim3(kThreads), 0, st, m.x, (int)m.K, qa, sa, g);
   else
-    hipLaunchKernelGGL((group_kernel<kRawF32>), dim3((unsigned)(1 + m.M)), dim3(kThreads), 0, st, m.x,
-                       m.ids, (int)P, m.E, p.bm, (int)m.K, qa, sa, count, tiles, list, rank);
+    hipLaunchKernelGGL((group_kernel<kRawF32>), blocks, dim3(kThreads), 0, st, m.x, (int)m.K, qa, sa, g);
+  if (g.counters > 1) hipLaunchKernelGGL(place_kernel, dim3(g.counters), dim3(kThreads), 0, st, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
@@ -378,7 +480,13 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
   // the down product quantises its rows itself where few rows share a tile
   const bool raw = p.bm == 16 && GI <= 32;
   if (!raw) {
-    e = launch_quant(h, 0, P, m.I, hq, hs, st);
+    if (m.I <= 64 * 8 * kRowHeld) {
+      hipLaunchKernelGGL(quant_pairs_kernel, dim3((unsigned)((P + kWaves - 1) / kWaves)), dim3(kThreads), 0, st,
+                         h, m.ids, P, m.E, (int)m.I, hq, hs);
+      e = hipGetLastError();
+    } else {
+      e = launch_quant(h, 0, P, m.I, hq, hs, st);
+    }
     if (e != hipSuccess) return e;
   }
   RowsArgs d = a;

@@ -507,7 +507,8 @@ hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {
   } else {
     const int64_t tiles = (l.M + kTileRows - 1) / kTileRows;
     a.strips = (a.nbe + 15) / 16;
-    e = launch_rows_tile(a, parts ? kSplit : kAdapt, tiles * a.strips, p.ksplit, st);
+    if (!parts) a.halves = half_strips(tiles, a.strips, device_cus());
+    e = launch_rows_tile(a, parts ? kSplit : kAdapt, tiles * (a.strips + a.halves), p.ksplit, st);
   }
   if (e != hipSuccess || !parts) return e;
   if (order)

@@ -62,6 +62,7 @@ struct RowsArgs {
   int div;               // source row of pair p is p / div
   int cols;              // column units per expert: blocks, or gate/up block pairs
   int strips;            // workgroups per tile along the columns
+  int halves;            // of them the last ones as two half tiles (kAdapt tiles)
   int kw;                // log2 of the wavefronts that share a column's groups
   int ncol;              // consecutive columns per wavefront
   int sg;                // groups of input channels staged at a time
@@ -147,7 +148,7 @@ __device__ __forceinline__ bool locate(const RowsArgs& a, Where& w) {
     return w.expert >= 0 && w.expert < a.n_experts;
   }
   const int tiles = (int)((a.M + BM - 1) / BM);
-  const int at = xcd_run(b, tiles * a.strips);
+  const int at = xcd_run(b, tiles * (a.strips - a.halves));
   w.strip = at / tiles;
   w.first = (at % tiles) * BM;
   w.rows = (int)(a.M - w.first < BM ? a.M - w.first : BM);
@@ -304,6 +305,12 @@ hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int 
 // a.ncol each per workgroup (kw = 0); more than one column only unsplit.
 hipError_t launch_rows_run(const RowsArgs& a, int mt, int out, int64_t blocks, int ksplit, hipStream_t st);
 hipError_t launch_rows_tile(const RowsArgs& a, int out, int64_t blocks, int ksplit, hipStream_t st);
+// Strips of an unsplit product that run as half tiles: those past the whole
+// rounds of the compute units, where their halves fit one more round.
+inline int half_strips(int64_t tiles, int64_t strips, int64_t cus) {
+  const int64_t whole = tiles * strips / cus * cus / tiles, rest = strips - whole;
+  return whole > 0 && 2 * rest * tiles <= cus ? (int)rest : 0;
+}
 // Rows per workgroup of launch_rows_tile, and its output channels.
 constexpr int kTileRows = 256;
 constexpr int kTileCols = 256;

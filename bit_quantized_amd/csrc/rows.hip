@@ -589,15 +589,13 @@ constexpr int kBOff = kABytes, kSOff = kABytes + kBBytes;
 
 __device__ __forceinline__ int a_chunk(int r, int c) { return c ^ (r & 7); }
 
-template <int OUT>
-__global__ void __launch_bounds__(kThreads)
-rows_tile_kernel(RowsArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2][kBufBytes];
-  __shared__ int s_pair[kTileRows];
-  __shared__ float s_scale[kTileRows];
-  __shared__ int s_id[OUT == kAdapt ? kTileRows : 1];  // adapters of the rows, -1: none
-  Where w;
-  if (!locate<kTileRows>(a, w)) return;
+// NU = 8: a whole tile of 16 blocks from cb; 4: a half tile of 8.  s_id: the
+// rows' adapters, -1 for none.
+template <int OUT, int NU>
+__device__ __forceinline__ void row_tile(const RowsArgs& a, const Where& w, int cb,
+                                         uint8_t (&smem)[2][kBufBytes], int* s_pair, float* s_scale,
+                                         int* s_id) {
+  constexpr int T = 4 * NU;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int r16 = lane & 15, j = lane >> 4;
   const int wm = wave >> 1, wn = wave & 1;
@@ -618,13 +616,13 @@ rows_tile_kernel(RowsArgs a) {
     }
   }
 
-  // block q (0..15) of the tile: wavefront column q / 8, its column u = q % 8
+  // block q of the tile: wavefront column q / NU, its column u = q % NU
   auto block_of = [&](int q) __attribute__((always_inline)) {
     if constexpr (OUT == kSwiglu) {
       const int u = q & 7;
       return (u >> 2) * a.cols + w.strip * 8 + (q >> 3) * 4 + (u & 3);
     } else {
-      return min(w.strip * 16 + q, NB - 1);  // past the end: columns that are never stored
+      return min(cb + q, NB - 1);  // past the end: columns that are never stored
     }
   };
   const int64_t eb = (int64_t)w.expert * NB;
@@ -638,7 +636,7 @@ rows_tile_kernel(RowsArgs a) {
     const int r = 8 * (4 * wave + i) + (lane >> 3);
     oa[i] = r < w.rows ? (uint32_t)(pair_of(a, w, r) / a.div) * a.K + 16 * a_chunk(r, lane & 7) : kOob;
   }
-  const int b0 = block_of(wave), b1 = block_of(wave + 8), bs = block_of((tid >> 4) & 15);
+  const int b0 = block_of(wave), b1 = block_of(wave + 8), bs = block_of((tid >> 4) & (2 * NU - 1));
   const uint32_t ob[2] = {(uint32_t)b0 * G * kBlockBytes + lane * 16, (uint32_t)b1 * G * kBlockBytes + lane * 16};
   const uint32_t oz[2] = {(uint32_t)b0 * G * 8 + (r16 >> 1), (uint32_t)b1 * G * 8 + (r16 >> 1)};
   const uint32_t os = (uint32_t)bs * G * 16 + r16;
@@ -655,7 +653,7 @@ rows_tile_kernel(RowsArgs a) {
   };
   auto fetch = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < NU / 4; ++k) {
       sb[k] = *reinterpret_cast<const v4u_rows*>(codes + (int64_t)g * kBlockBytes + ob[k]);
       sz[k] = (zeros + g * kZeroBlockBytes)[oz[k]];
     }
@@ -670,14 +668,14 @@ rows_tile_kernel(RowsArgs a) {
   };
   // scales as [16 channels][16 blocks]: a lane's eight are contiguous
   auto store_scale = [&](uint8_t* buf) __attribute__((always_inline)) {
-    reinterpret_cast<float*>(buf + kSOff)[r16 * 16 + ((tid >> 4) & 15)] = ss;
+    reinterpret_cast<float*>(buf + kSOff)[r16 * 16 + ((tid >> 4) & (2 * NU - 1))] = ss;
   };
 
-  float acc[4][8][4];
+  float acc[4][NU][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u = 0; u < NU; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[i][u][r] = 0.0f;
 
@@ -691,30 +689,30 @@ rows_tile_kernel(RowsArgs a) {
       a0[i] = *reinterpret_cast<const v4i*>(arow + 16 * a_chunk(r16, j));
       a1[i] = *reinterpret_cast<const v4i*>(arow + 16 * a_chunk(r16, 4 + j));
     }
-    float sv[8];
-    const float* srow = reinterpret_cast<const float*>(buf + kSOff) + r16 * 16 + wn * 8;
+    float sv[NU];
+    const float* srow = reinterpret_cast<const float*>(buf + kSOff) + r16 * 16 + wn * NU;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < NU / 4; ++q) {
       const v4i t = *reinterpret_cast<const v4i*>(srow + 4 * q);
 #pragma unroll
       for (int u = 0; u < 4; ++u) sv[4 * q + u] = __int_as_float(t[u]);
     }
-    v4i q0[8], q1[8];
+    v4i q0[NU], q1[NU];
     auto load_b = [&](int u) __attribute__((always_inline)) {
-      const uint8_t* at = buf + kBOff + (wn * 8 + u) * 2 * kBlockBytes + lane * 16;
+      const uint8_t* at = buf + kBOff + (wn * NU + u) * 2 * kBlockBytes + lane * 16;
       q0[u] = *reinterpret_cast<const v4i*>(at);
       q1[u] = *reinterpret_cast<const v4i*>(at + kBlockBytes);
     };
     load_b(0);
-    v4i p[32];
+    v4i p[T];
 #pragma unroll
-    for (int t = 0; t < 34; ++t) {
-      if (t < 32) {
+    for (int t = 0; t < T + 2; ++t) {
+      if (t < T) {
         const int u = t >> 2, i = t & 3;
-        if (i == 0 && u + 1 < 8) load_b(u + 1);
-        if (next && t == 16) store_block(next, 0);
-        if (next && t == 22) store_block(next, 1);
-        if (next && t == 28) store_scale(next);
+        if (i == 0 && u + 1 < NU) load_b(u + 1);
+        if (next && t == T / 2) store_block(next, 0);
+        if (NU == 8 && next && t == 22) store_block(next, 1);
+        if (next && t == T - 4) store_scale(next);
         p[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0[i], q0[u], kBiasSeed, 0, 0, 0);
         p[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1[i], q1[u], p[t], 0, 0, 0);
       }
@@ -722,7 +720,7 @@ rows_tile_kernel(RowsArgs a) {
         const int e = t - 2, u = e >> 2, i = e & 3;
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][u][r] += sv[u] * unbias(p[e][r]);
-        if (t + 1 < 32) {  // keeps pairs and rescales interleaved (no instruction)
+        if (t + 1 < T) {  // keeps pairs and rescales interleaved (no instruction)
           const int in = (t + 1) & 3;
           asm volatile("" : "+v"(a0[in]) : "v"(acc[i][u][0]), "v"(acc[i][u][1]), "v"(acc[i][u][2]),
                        "v"(acc[i][u][3]));
@@ -734,7 +732,7 @@ rows_tile_kernel(RowsArgs a) {
   dma(smem[0], gb);
   fetch(gb);
   store_block(smem[0], 0);
-  store_block(smem[0], 1);
+  if (NU == 8) store_block(smem[0], 1);
   store_scale(smem[0]);
   loads_done<0>();
   __syncthreads();
@@ -745,7 +743,7 @@ rows_tile_kernel(RowsArgs a) {
         dma(next, g + 1);
         fetch(g + 1);
         store_block(next, 0);
-        store_block(next, 1);
+        if (NU == 8) store_block(next, 1);
         store_scale(next);
       }
       loads_done<0>();
@@ -785,12 +783,12 @@ rows_tile_kernel(RowsArgs a) {
         const int row = wm * 64 + i * 16 + 4 * j + r;
         const float s = row < w.rows ? s_scale[row] : 0.0f;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) acc[i][u][r] *= s;
+        for (int u = 0; u < NU; ++u) acc[i][u][r] *= s;
       }
     for (int r0 = 0; r0 < a.ad.R; r0 += 32) {
       const int rr = r0 + 8 * j;  // this lane's eight ranks
       int held = -1;              // the adapter whose B is in bv
-      v4i bv[8], ah[4], al[4];
+      v4i bv[NU], ah[4], al[4];
       int id[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -813,8 +811,8 @@ rows_tile_kernel(RowsArgs a) {
           if (l != held) {  // (the rows come in the order of their adapters)
             held = l;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int nb = min(w.strip * 16 + wn * 8 + u, NB - 1);
+            for (int u = 0; u < NU; ++u) {
+              const int nb = min(cb + wn * NU + u, NB - 1);
               bv[u] = v4i{0, 0, 0, 0};
               if (rr < a.ad.R)
                 bv[u] = *reinterpret_cast<const v4i*>(
@@ -824,7 +822,7 @@ rows_tile_kernel(RowsArgs a) {
           const v4i zero = {0, 0, 0, 0};
           const v4i h = id[i] == l ? ah[i] : zero, lw = id[i] == l ? al[i] : zero;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
+          for (int u = 0; u < NU; ++u) {
             v4f_rows c = {0.f, 0.f, 0.f, 0.f};
             c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_rows, h),
                                                         __builtin_bit_cast(v8bf_rows, bv[u]), c, 0, 0, 0);
@@ -853,8 +851,8 @@ rows_tile_kernel(RowsArgs a) {
               f32_to_bf16_rne(silu_mul(s * acc[i][u][r], s * acc[i][u + 4][r]));
       } else {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int nb = w.strip * 16 + wn * 8 + u;
+        for (int u = 0; u < NU; ++u) {
+          const int nb = cb + wn * NU + u;
           if (nb >= NB) continue;
           const int64_t n = 16 * nb + r16;
           if constexpr (OUT == kParts)
@@ -866,6 +864,34 @@ rows_tile_kernel(RowsArgs a) {
         }
       }
     }
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreads)
+rows_tile_kernel(RowsArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2][kBufBytes];
+  __shared__ int s_pair[kTileRows];
+  __shared__ float s_scale[kTileRows];
+  __shared__ int s_id[OUT == kAdapt ? kTileRows : 1];
+  Where w;
+  if constexpr (OUT == kAdapt) {
+    // the last strips may come as half tiles: they fill a last round of the
+    // compute units that whole ones would leave partly idle (half_strips)
+    const int tiles = (int)((a.M + kTileRows - 1) / kTileRows), whole = tiles * (a.strips - a.halves);
+    const int b = blockIdx.x;
+    if (b >= whole) {
+      const int at = xcd_run(b - whole, tiles * 2 * a.halves);
+      w.expert = 0;
+      w.strip = 0;
+      w.first = at % tiles * kTileRows;
+      w.rows = (int)(a.M - w.first < kTileRows ? a.M - w.first : kTileRows);
+      const int cb = (a.strips - a.halves) * 16 + at / tiles * 8;
+      if (cb < a.nbe) row_tile<OUT, 4>(a, w, cb, smem, s_pair, s_scale, s_id);
+      return;
+    }
+  }
+  if (!locate<kTileRows>(a, w)) return;
+  row_tile<OUT, 8>(a, w, w.strip * 16, smem, s_pair, s_scale, s_id);
 }
 
 template <int MT, bool ONE, int ACT, int OUT>

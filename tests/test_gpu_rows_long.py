@@ -29,6 +29,19 @@ def test_moe_sliced(w4, M, k, E, I, K, dtype):  # noqa: F811
     check_moe(y, *moe_ref(x, up, down, ids, wt, E))
 
 
+@pytest.mark.parametrize("P", [4095, 4096, 4097, 9000])
+@pytest.mark.parametrize("E,k", [(5, 1), (200, 3)])
+def test_moe_many_pairs(w4, P, E, k):  # noqa: F811
+    """Pairs counted by one workgroup and by several, with experts of no pair
+    and one of very many, slots of other experts, repeated ids in a token."""
+    M, I, K = P // k, 128, 128
+    x, up, down, ids, wt = moe_case(P, M, k, E, I, K, torch.bfloat16, drop=0.1, skew=True)
+    g = torch.Generator(device="cuda").manual_seed(P)
+    ids = torch.where(torch.rand(M, k, generator=g, device="cuda") < 0.3, 2, ids).contiguous()
+    y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
+    check_moe(y, *moe_ref(x, up, down, ids, wt, E))
+
+
 LORA = [
     # M, K, N, L, R, seg: two, three and four 16-row fragments, K in two slices
     (20, 4608, 32784, 3, 8, 1), (45, 2816, 32784, 4, 72, 3), (61, 2304, 32784, 5, 32, 1),
@@ -36,6 +49,8 @@ LORA = [
     # rows over many channels, ranks past 64, all with K whole and in slices
     (90, 256, 272, 2000, 8, 1), (300, 1152, 272, 1500, 16, 1), (64, 256, 18960, 64, 64, 1),
     (700, 256, 4112, 9, 72, 1), (300, 1024, 1040, 16, 128, 1), (517, 384, 2064, 3, 128, 11),
+    # 256 x 256 tiles past a whole round of the compute units: half tiles, an odd number of them
+    (1000, 256, 17424, 6, 40, 1), (2048, 128, 9232, 4, 16, 300), (300, 384, 33040, 3, 8, 2),
     # eight wavefronts to a column, with rows that end inside the fragment
     (16, 3584, 2064, 5, 72, 1), (11, 1152, 3584, 16, 128, 1), (2, 4096, 4096, 2, 8, 1), (9, 4224, 2304, 4, 24, 1),
     # the single token: K whole, K split over workgroups, a long token, many channels
