@@ -209,10 +209,19 @@ down_token_kernel(RowsArgs a, int k) {
   float total = 0.0f;
   for (int s0 = 0; s0 < k; s0 += kWaves) {
     const int slot = s0 + wave;
-    const int e = slot < k ? uniform(a.ids[m * k + slot]) : -1;
+    // the slot's h row goes out beside its expert's id, ahead of the weights:
+    // it is quantised while they arrive
+    const int64_t p = m * k + min(slot, k - 1);
+    const uint8_t* hr = reinterpret_cast<const uint8_t*>(a.x) + p * a.K * 2;
+    const int ev = a.ids[p];
+    v4u_rows held[kRowHeld][1];
+#pragma unroll
+    for (int i = 0; i < kRowHeld; ++i)
+      if (lane + 64 * i < nch) RawRow<kRawBf16>::load(hr, lane + 64 * i, held[i]);
+    __builtin_amdgcn_sched_barrier(0);
+    const int e = slot < k ? uniform(ev) : -1;
     float v = 0.0f;
     if (e >= 0 && e < a.n_experts) {
-      const int64_t p = m * k + slot;
       const int64_t b0 = ((int64_t)e * a.nbe + nb) * G;
       const __amdgpu_buffer_rsrc_t rc = rsrc_of(a.codes + b0 * kBlockBytes, (int64_t)G * kBlockBytes);
       const __amdgpu_buffer_rsrc_t rs = rsrc_of(a.scales + b0 * 16, (int64_t)G * 64);
@@ -231,25 +240,36 @@ down_token_kernel(RowsArgs a, int k) {
 #pragma unroll
       for (int i = 0; i < D; ++i) load(i, i);
       __builtin_amdgcn_sched_barrier(0);
-      const uint8_t* hr = reinterpret_cast<const uint8_t*>(a.x) + p * a.K * 2;
       float amax = 0.0f;
-      for (int ch = lane; ch < nch; ch += 64) {
-        v4u_rows raw[1];
+      auto most = [&](const v4u_rows* raw) __attribute__((always_inline)) {
         float t[8];
-        RawRow<kRawBf16>::load(hr, ch, raw);
         RawRow<kRawBf16>::widen(raw, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(t[i]));
+      };
+#pragma unroll
+      for (int i = 0; i < kRowHeld; ++i)
+        if (lane + 64 * i < nch) most(held[i]);
+      for (int ch = lane + 64 * kRowHeld; ch < nch; ch += 64) {
+        v4u_rows raw[1];
+        RawRow<kRawBf16>::load(hr, ch, raw);
+        most(raw);
       }
       amax = wave_max64(amax);
       const float scale = amax / 127.0f, inv = 1.0f / scale;
-      for (int ch = lane; ch < nch; ch += 64) {
-        v4u_rows raw[1];
+      auto put = [&](int ch, const v4u_rows* raw) __attribute__((always_inline)) {
         float t[8];
-        RawRow<kRawBf16>::load(hr, ch, raw);
         RawRow<kRawBf16>::widen(raw, t);
         *reinterpret_cast<uint2*>(q + 8 * ch) =
             amax != 0.0f ? quant8_codes(t, scale, inv) : make_uint2(0u, 0u);
+      };
+#pragma unroll
+      for (int i = 0; i < kRowHeld; ++i)
+        if (lane + 64 * i < nch) put(lane + 64 * i, held[i]);
+      for (int ch = lane + 64 * kRowHeld; ch < nch; ch += 64) {
+        v4u_rows raw[1];
+        RawRow<kRawBf16>::load(hr, ch, raw);
+        put(ch, raw);
       }
       // the wavefront's own LDS writes, read by its other lanes
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -140,13 +140,6 @@ __device__ __forceinline__ bool locate(const RowsArgs& a, Where& w) {
     w.rows = uniform(t.rows);
     return true;
   }
-  if (a.kind == kDirect) {
-    w.first = b / a.strips;
-    w.strip = b % a.strips;
-    w.rows = 1;
-    w.expert = uniform(a.ids[w.first]);
-    return w.expert >= 0 && w.expert < a.n_experts;
-  }
   const int tiles = (int)((a.M + BM - 1) / BM);
   const int at = xcd_run(b, tiles * (a.strips - a.halves));
   w.strip = at / tiles;

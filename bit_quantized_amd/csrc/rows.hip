@@ -58,9 +58,34 @@ rows_stream_kernel(RowsArgs a) {
   __shared__ float s_dot[OUT == kAdapt ? kWaves : 1][OUT == kAdapt ? 4 : 1][64];
 
   Where w;
-  if (!locate<BM>(a, w)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int r16 = lane & 15, j = lane >> 4;
+  // raw activations: 2^rl wavefronts per row, so that a lone row is not left
+  // to one of them; the first rows' chunks are held in registers
+  using RR = RawRow<ACT == kCodes ? kRawBf16 : ACT>;
+  constexpr int HC = ACT == kRawBf16 ? 2 : 1;
+  const int nch = a.K / 8;
+  v4u_rows xh[HC][RR::kLoads];
+  auto raw_row = [&](int row) __attribute__((always_inline)) {
+    return static_cast<const uint8_t*>(a.x) + (int64_t)(pair_of(a, w, row) / a.div) * a.K * RR::kBytes;
+  };
+  if constexpr (ONE) {  // (kDirect) the row's loads go out beside its expert's
+    w.first = blockIdx.x / a.strips;
+    w.strip = blockIdx.x % a.strips;
+    w.rows = 1;
+    const int e = a.ids[w.first];
+    const uint8_t* xr = raw_row(0);
+#pragma unroll
+    for (int i = 0; i < HC; ++i)
+      if (tid + i * kThreads < nch) RR::load(xr, tid + i * kThreads, xh[i]);
+    __builtin_amdgcn_sched_barrier(0);
+    w.expert = uniform(e);
+    if (w.expert < 0 || w.expert >= a.n_experts) return;
+  } else {
+    if (!locate<BM>(a, w)) return;
+  }
+  const int rl = w.rows <= 1 ? 3 : w.rows <= 2 ? 2 : w.rows <= 4 ? 1 : 0;
+  const int wpr = 1 << rl, sub = (wave & (wpr - 1)) * 64 + lane, step = 64 * wpr;
   const int G = a.K / kGroup;
   const int KW = 1 << a.kw, CW = kWaves >> a.kw;
   const int kwi = wave & (KW - 1), cw = wave >> a.kw;
@@ -135,22 +160,11 @@ rows_stream_kernel(RowsArgs a) {
       }
   };
 
-  // raw activations: 2^rl wavefronts per row, so that a lone row is not left
-  // to one of them; the first rows' chunks are held in registers
-  using RR = RawRow<ACT == kCodes ? kRawBf16 : ACT>;
-  constexpr int HC = ACT == kRawBf16 ? 2 : 1;
-  const int rl = w.rows <= 1 ? 3 : w.rows <= 2 ? 2 : w.rows <= 4 ? 1 : 0;
-  const int wpr = 1 << rl, nch = a.K / 8, sub = (wave & (wpr - 1)) * 64 + lane, step = 64 * wpr;
-  auto raw_row = [&](int row) __attribute__((always_inline)) {
-    return static_cast<const uint8_t*>(a.x) + (int64_t)(pair_of(a, w, row) / a.div) * a.K * RR::kBytes;
-  };
-
   const int64_t eb = (int64_t)w.expert * a.nbe;  // the expert's first block
   for (int s0 = gb; s0 < ge; s0 += a.sg) {
     const int sgn = min(a.sg, ge - s0);
     const bool last = s0 + sgn == ge;
     // ---- the activations' loads
-    v4u_rows xh[HC][RR::kLoads];
     if constexpr (ACT == kCodes) {
       // straight into LDS, 1 KiB per wavefront and load (rows past the tile:
       // zeros, no request); the LDS has to be free
@@ -168,7 +182,7 @@ rows_stream_kernel(RowsArgs a) {
         if (sr >= 0) off = sr * a.K + (s0 + q - m * sgn) * kGroup + 64 * h + 16 * j;
         if (uniform(c) < MT * sgn * 128) load_to_lds(rqa, smem + uniform(c) * 16, off, 0);
       }
-    } else {
+    } else if constexpr (!ONE) {
       const int row = wave >> rl;
       if (row < w.rows) {
         const uint8_t* xr = raw_row(row);
