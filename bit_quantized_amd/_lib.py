@@ -93,6 +93,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_layout = None  # the library's packed layout version
 
 
 class W4A8Error(RuntimeError):
@@ -102,7 +103,7 @@ class W4A8Error(RuntimeError):
 
 
 def load() -> ctypes.CDLL:
-    global _lib
+    global _lib, _layout
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -112,6 +113,7 @@ def load() -> ctypes.CDLL:
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args
+    _layout = lib.w4a8_layout_version()
     _lib = lib
     return lib
 
@@ -159,9 +161,9 @@ class PackedWeight:
     layout_version: int
 
     def check(self):
-        v = load().w4a8_layout_version()
-        if self.layout_version != v:
-            raise ValueError(f"packed with layout {self.layout_version}, library has {v}")
+        load()
+        if self.layout_version != _layout:
+            raise ValueError(f"packed with layout {self.layout_version}, library has {_layout}")
 
 
 def packed_weight_bytes(N: int, K: int, group: int = GROUP) -> int:

@@ -118,3 +118,25 @@ def test_route_next_to_a_border(w4, kind, E, n_groups, group_top, score):  # noq
         a, b = c.gather(1, ids.cpu().long()), c.gather(1, rid.long())
         assert ((a - b).abs() <= 2.0 ** -50).all()
     assert ((w.cpu().double() - rw).abs() <= (E + 16) * 2.0 ** -24 * rw.abs()).all()
+
+
+def test_host_tensors_are_refused(w4):  # noqa: F811
+    """A tensor in host memory, the workspace among them, never reaches a kernel."""
+    x, w, A, B, sc, ids = lora_case(1, 4, 256, 272, 2, 8, torch.bfloat16)
+    W, ad = w4.pack_weights(*w), w4.LoraAdapters(A, B, sc)
+    host = torch.empty(w4.lora_linear_workspace_bytes(4, 272, 256, 2, 8), dtype=torch.uint8)
+    for kw in (dict(workspace=host), dict(out=torch.empty(4, 272, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            w4.lora_linear(x, W, ad, ids, **kw)
+    with pytest.raises(ValueError):
+        w4.lora_linear(x, W, ad, ids.cpu())
+    with pytest.raises(ValueError):
+        w4.lora_linear(x.repeat(1, 2)[:, ::2], W, ad, ids)       # not contiguous
+    xm, up, down, eid, wt = moe_case(1, 4, 2, 3, 128, 256, torch.bfloat16)
+    ups = pack(w4, up, down, 3)
+    with pytest.raises(ValueError):
+        w4.moe_mlp(xm, *ups, eid, wt, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        w4.moe_mlp(xm, *ups, eid, wt.cpu())
+    with pytest.raises(ValueError):
+        w4.moe_route(torch.zeros(2, 8, device="cuda"), 2, bias=torch.zeros(8))
