@@ -3,6 +3,9 @@
 // sum over a token's experts.
 #include "experts.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace w4a8 {
 namespace {
 
@@ -349,10 +352,22 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 // Rows a tile of the planned kernels holds: the smallest of 16, 32, 64 and
-// 256 that holds an expert's even share of the pairs with room to spare.
-static int tile_rows(int64_t P, int E) {
+// 256 that holds an expert's even share of the pairs with room to spare; of
+// 64 and 256 past that the one that takes less time by what they measured a
+// group of inputs: a round of 256-row tiles 3.0 us, 64-row ones 1.3 us where
+// they lie one to a compute unit and that much more for every further one
+// (768 tokens, 5 experts, 3200 -> 2 x 256: 66 us against 92 on 256 rows;
+// 4096 tokens, 64 experts, 3584 -> 2 x 1280 stay on 256).
+static int tile_rows(int64_t P, int E, int64_t I, int64_t K) {
   const double share = (double)P / E;
-  return share <= 10 ? 16 : share <= 22 ? 32 : share <= 96 ? 64 : kTileRows;
+  if (share <= 96) return share <= 10 ? 16 : share <= 22 ? 32 : 64;
+  const double cus = device_cus(), part = E / 2.0;  // an expert's last tile is half full
+  const double G = K / kGroup, GI = I / kGroup, up = I / 128.0, down = K / 256.0;
+  auto rounds = [](double n) { return n <= 1 ? 1.0 : std::ceil(n); };
+  const double big = P / 256.0 + part, small = P / 64.0 + part;
+  const double tile = 3.0 * (G * rounds(big * up / cus) + GI * rounds(big * down / cus));
+  const double run = 1.3 * (G * std::max(1.0, small * up / cus) + GI * std::max(1.0, small * down / cus));
+  return run < tile ? 64 : kTileRows;
 }
 
 // Single tokens (a few pairs) skip the grouping: each pair is a tile.
@@ -372,7 +387,7 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
   if (mc < 1) return p;
   const int64_t P = mc * k;
   p.direct = direct(M * k, I, K);
-  p.bm = tile_rows(P, E);
+  p.bm = tile_rows(P, E, I, K);
   p.max_tiles = P / p.bm + (E < P ? E : P);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {

@@ -376,6 +376,7 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   if (mc > M) mc = M;
   p.rows = mc;
   if (mc < 1) return p;
+  bool few = false;
   const GemvShape gs = gemv_shape(N, K);
   p.gemv = M == 1 && K <= kGemvMaxK && gemv_shape_ok(N, K, gs);
   if (p.gemv) {
@@ -398,6 +399,7 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
     int64_t ks = cus / tiles;
     if (ks > G / 4) ks = G / 4;
     p.ksplit = (int)(ks > 1 ? ks : 1);
+    few = tiles < cus / 2;
   }
   const int64_t frags = (mc + 15) / 16;
   // (few rows: sorted where reading B once per row would cost more than the
@@ -425,8 +427,9 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
     p.hi = take(mc * R * 2);
     p.lo = take(mc * R * 2);
   }
-  // (the streaming kernels go through the sums unless a column is whole)
-  const bool sums = p.ksplit > 1 || (p.mt && p.kw == 0);
+  // (the streaming kernels go through the sums unless a column is whole, few
+  // tiles so that the adapters' part runs on more compute units than they)
+  const bool sums = p.ksplit > 1 || (p.mt && p.kw == 0) || few;
   if (sums) p.parts = take((int64_t)p.ksplit * mc * N * 4);
   else p.parts = -1;
   p.bytes = at;
