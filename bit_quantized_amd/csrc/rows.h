@@ -81,8 +81,10 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // makes every LDS read that follows its builtin wait for the load, whatever
 // buffer it reads; here nothing waits until loads_done() below, which has to
 // come before the barrier that hands the bytes over.  (No register is
-// written, and m0 has no other use in the kernels that call this; the compiler's own waits count at least the loads it knows of, and
-// loads retire in order, so they only become stricter.)
+// written; m0, a register the compiler never keeps a value in, has no other
+// use in the kernels that call this.  The compiler's own waits count the
+// loads it knows of, and loads retire in order, so they only become
+// stricter.)
 struct LdsSource {
   v4i words;  // raw byte buffer descriptor
 };
