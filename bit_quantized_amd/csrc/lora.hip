@@ -503,8 +503,7 @@ hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {
     if (parts && per > staged_groups(p.mt)) {
       e = launch_rows_run(a, p.mt, kSplit, a.strips, p.ksplit, st);
     } else {
-      const int most = staged_groups(p.mt), n = (per + most - 1) / most;
-      a.sg = (per + n - 1) / n;
+      a.sg = per;
       e = launch_rows_stream(a, p.mt, false, kCodes, parts ? kSplit : kAdapt, a.strips, p.ksplit, st);
     }
   } else {

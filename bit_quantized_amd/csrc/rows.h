@@ -65,7 +65,7 @@ struct RowsArgs {
   int halves;            // of them the last ones as two half tiles (kAdapt tiles)
   int kw;                // log2 of the wavefronts that share a column's groups
   int ncol;              // consecutive columns per wavefront
-  int sg;                // groups of input channels staged at a time
+  int sg;                // groups of input channels that are staged
   const float* pw;       // weights of the pairs (kParts)
   uint16_t* h;           // kSwiglu output [pairs][16 * cols]
   float* parts;          // kParts [pairs][16 nbe]; kSplit [slices][M][16 nbe]

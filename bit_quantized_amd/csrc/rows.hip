@@ -40,7 +40,7 @@ __device__ __forceinline__ void lds_barrier() {
 // Groups whose activations fit the 64 KiB that rows_stream_kernel stages at
 // once; past them rows_run_kernel, whose buffers hold run_groups() each.
 constexpr int run_groups(int mt, int out) { return mt <= 2 && out != kSwiglu ? 8 : 4; }
-constexpr int kStageChunks = 8;  // 16-byte pieces of activations a thread stages per slice
+constexpr int kStageChunks = 8;  // 16-byte pieces of activations a thread stages
 
 template <int MT, bool ONE, int ACT, int OUT>
 __global__ void __launch_bounds__(kThreads, MT > 2 || OUT == kAdapt ? 2 : 4)
@@ -161,206 +161,198 @@ rows_stream_kernel(RowsArgs a) {
   };
 
   const int64_t eb = (int64_t)w.expert * a.nbe;  // the expert's first block
-  for (int s0 = gb; s0 < ge; s0 += a.sg) {
-    const int sgn = min(a.sg, ge - s0);
-    const bool last = s0 + sgn == ge;
-    // ---- the activations' loads
-    if constexpr (ACT == kCodes) {
-      // straight into LDS, 1 KiB per wavefront and load (rows past the tile:
-      // zeros, no request); the LDS has to be free
-      if (s0 != gb) lds_barrier();
+  const int sgn = ge - gb;
+  // ---- the activations' loads
+  if constexpr (ACT == kCodes) {
+    // straight into LDS, 1 KiB per wavefront and load (rows past the tile:
+    // zeros, no request)
 #pragma unroll
-      for (int i = 0; i < kStageChunks; ++i) {
-        const int c = tid + i * kThreads;
-        const int q = c >> 7, h = (c >> 6) & 1;
-        int off = kOob, m = 0, sr = src[0];
+    for (int i = 0; i < kStageChunks; ++i) {
+      const int c = tid + i * kThreads;
+      const int q = c >> 7, h = (c >> 6) & 1;
+      int off = kOob, m = 0, sr = src[0];
 #pragma unroll
-        for (int t = 1; t < MT; ++t) {
-          m += q >= t * sgn;
-          sr = m == t ? src[t] : sr;
-        }
-        if (sr >= 0) off = sr * a.K + (s0 + q - m * sgn) * kGroup + 64 * h + 16 * j;
-        if (uniform(c) < MT * sgn * 128) load_to_lds(rqa, smem + uniform(c) * 16, off, 0);
+      for (int t = 1; t < MT; ++t) {
+        m += q >= t * sgn;
+        sr = m == t ? src[t] : sr;
       }
-    } else if constexpr (!ONE) {
-      const int row = wave >> rl;
-      if (row < w.rows) {
-        const uint8_t* xr = raw_row(row);
-#pragma unroll
-        for (int i = 0; i < HC; ++i)
-          if (sub + i * step < nch) RR::load(xr, sub + i * step, xh[i]);
-      }
+      if (sr >= 0) off = sr * a.K + (gb + q - m * sgn) * kGroup + 64 * h + 16 * j;
+      if (uniform(c) < MT * sgn * 128) load_to_lds(rqa, smem + uniform(c) * 16, off, 0);
     }
-    __builtin_amdgcn_sched_barrier(0);
+  } else if constexpr (!ONE) {
+    const int row = wave >> rl;
+    if (row < w.rows) {
+      const uint8_t* xr = raw_row(row);
+#pragma unroll
+      for (int i = 0; i < HC; ++i)
+        if (sub + i * step < nch) RR::load(xr, sub + i * step, xh[i]);
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
 
-    // ---- the first weight units.  This wavefront's groups of the slice, and
-    // its run of units: nc columns of them (several columns only when they
-    // cover all groups, so the run is contiguous in the packed planes)
-    const int k0 = sgn * kwi / KW, kn = sgn * (kwi + 1) / KW - k0;
-    const int T = kn * nc;
-    __amdgpu_buffer_rsrc_t rc[NBK], rs[NBK], rz[NBK];
+  // ---- the first weight units.  This wavefront's groups, and its run of
+  // units: nc columns of them (several columns only when they cover all
+  // groups, so the run is contiguous in the packed planes)
+  const int k0 = sgn * kwi / KW, kn = sgn * (kwi + 1) / KW - k0;
+  const int T = kn * nc;
+  __amdgpu_buffer_rsrc_t rc[NBK], rs[NBK], rz[NBK];
+#pragma unroll
+  for (int b = 0; b < NBK; ++b) {
+    const int64_t b0 = (eb + b * a.cols + (nc > 0 ? c0 : 0)) * G + gb + k0;
+    rc[b] = rsrc_of(a.codes + b0 * kBlockBytes, (int64_t)T * kBlockBytes);
+    rs[b] = rsrc_of(a.scales + b0 * 16, (int64_t)T * 64);
+    rz[b] = rsrc_of(a.zeros + b0 * kZeroBlockBytes, (int64_t)T * kZeroBlockBytes);
+  }
+  v4u_rows d[D][NBK];
+  float s[D][NBK];
+  uint32_t z[D][NBK];
+  // past the run (the descriptors' end): no memory request, zeros
+  auto load = [&](int i, int t) __attribute__((always_inline)) {
+    t = min(t, T);
 #pragma unroll
     for (int b = 0; b < NBK; ++b) {
-      const int64_t b0 = (eb + b * a.cols + (nc > 0 ? c0 : 0)) * G + s0 + k0;
-      rc[b] = rsrc_of(a.codes + b0 * kBlockBytes, (int64_t)T * kBlockBytes);
-      rs[b] = rsrc_of(a.scales + b0 * 16, (int64_t)T * 64);
-      rz[b] = rsrc_of(a.zeros + b0 * kZeroBlockBytes, (int64_t)T * kZeroBlockBytes);
+      d[i][b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], 16 * lane, (unsigned)uniform(t * kBlockBytes),
+                                                      kNontemporal);
+      s[i][b] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(rs[b], 4 * r16, (unsigned)uniform(t * 64), 0));
+      z[i][b] = __builtin_amdgcn_raw_buffer_load_b8(rz[b], r16 >> 1, (unsigned)uniform(t * kZeroBlockBytes), 0);
     }
-    v4u_rows d[D][NBK];
-    float s[D][NBK];
-    uint32_t z[D][NBK];
-    // past the run (the descriptors' end): no memory request, zeros
-    auto load = [&](int i, int t) __attribute__((always_inline)) {
-      t = min(t, T);
+  };
 #pragma unroll
-      for (int b = 0; b < NBK; ++b) {
-        d[i][b] = __builtin_amdgcn_raw_buffer_load_b128(rc[b], 16 * lane, (unsigned)uniform(t * kBlockBytes),
-                                                        kNontemporal);
-        s[i][b] = __builtin_bit_cast(
-            float, __builtin_amdgcn_raw_buffer_load_b32(rs[b], 4 * r16, (unsigned)uniform(t * 64), 0));
-        z[i][b] = __builtin_amdgcn_raw_buffer_load_b8(rz[b], r16 >> 1, (unsigned)uniform(t * kZeroBlockBytes), 0);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      load(i, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+  for (int i = 0; i < D; ++i) {
+    load(i, i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
-    // ---- activations -> LDS
-    if constexpr (ACT == kCodes) {
-      loads_done<3 * NBK * D>();
-    } else {
-      // quantised here (the rule of w4a8_quant_act)
-      for (int row0 = 0; row0 < w.rows; row0 += kWaves >> rl) {
-        const int row = row0 + (wave >> rl);
-        const bool live = row < w.rows, held = row0 == 0;
-        const uint8_t* xr = raw_row(live ? row : 0);
-        float amax = 0.0f;
-        auto most = [&](const v4u_rows* r) __attribute__((always_inline)) {
+  // ---- activations -> LDS
+  if constexpr (ACT == kCodes) {
+    loads_done<3 * NBK * D>();
+  } else {
+    // quantised here (the rule of w4a8_quant_act)
+    for (int row0 = 0; row0 < w.rows; row0 += kWaves >> rl) {
+      const int row = row0 + (wave >> rl);
+      const bool live = row < w.rows, held = row0 == 0;
+      const uint8_t* xr = raw_row(live ? row : 0);
+      float amax = 0.0f;
+      auto most = [&](const v4u_rows* r) __attribute__((always_inline)) {
+        float v[8];
+        RR::widen(r, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      };
+      if (live) {
+        if (held) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i)
+            if (sub + i * step < nch) most(xh[i]);
+        }
+        for (int ch = sub + (held ? HC * step : 0); ch < nch; ch += step) {
+          v4u_rows r[RR::kLoads];
+          RR::load(xr, ch, r);
+          most(r);
+        }
+      }
+      amax = wave_max64(amax);
+      if (wpr > 1) {  // (the only pass of the row loop: at most 8 / wpr rows)
+        if (lane == 0) s_max[wave] = amax;
+        lds_barrier();
+        for (int i = 0; i < wpr; ++i) amax = fmaxf(amax, s_max[(wave & ~(wpr - 1)) + i]);
+      }
+      if (live) {
+        const float scale = amax / 127.0f, inv = 1.0f / scale;
+        if (sub == 0) s_scale[row] = scale;
+        auto put = [&](int ch, const v4u_rows* r) __attribute__((always_inline)) {
           float v[8];
           RR::widen(r, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+          const uint2 codes = amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+          const int g = ch >> 4, h = (ch >> 3) & 1, jj = (ch >> 1) & 3;
+          const int at = ONE ? ((g * 2 + h) * 4 + jj) * 16
+                             : (((row >> 4) * sgn + g) * 2 + h) * 1024 + (16 * jj + (row & 15)) * 16;
+          *reinterpret_cast<uint2*>(smem + at + 8 * (ch & 1)) = codes;
         };
-        if (live) {
-          if (held) {
+        if (held) {
 #pragma unroll
-            for (int i = 0; i < HC; ++i)
-              if (sub + i * step < nch) most(xh[i]);
-          }
-          for (int ch = sub + (held ? HC * step : 0); ch < nch; ch += step) {
-            v4u_rows r[RR::kLoads];
-            RR::load(xr, ch, r);
-            most(r);
-          }
+          for (int i = 0; i < HC; ++i)
+            if (sub + i * step < nch) put(sub + i * step, xh[i]);
         }
-        amax = wave_max64(amax);
-        if (wpr > 1) {  // (the only pass of the row loop: at most 8 / wpr rows)
-          if (lane == 0) s_max[wave] = amax;
-          lds_barrier();
-          for (int i = 0; i < wpr; ++i) amax = fmaxf(amax, s_max[(wave & ~(wpr - 1)) + i]);
-        }
-        if (live) {
-          const float scale = amax / 127.0f, inv = 1.0f / scale;
-          if (sub == 0) s_scale[row] = scale;
-          auto put = [&](int ch, const v4u_rows* r) __attribute__((always_inline)) {
-            float v[8];
-            RR::widen(r, v);
-            const uint2 codes = amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
-            const int g = ch >> 4, h = (ch >> 3) & 1, jj = (ch >> 1) & 3;
-            const int at = ONE ? ((g * 2 + h) * 4 + jj) * 16
-                               : (((row >> 4) * sgn + g) * 2 + h) * 1024 + (16 * jj + (row & 15)) * 16;
-            *reinterpret_cast<uint2*>(smem + at + 8 * (ch & 1)) = codes;
-          };
-          if (held) {
-#pragma unroll
-            for (int i = 0; i < HC; ++i)
-              if (sub + i * step < nch) put(sub + i * step, xh[i]);
-          }
-          for (int ch = sub + (held ? HC * step : 0); ch < nch; ch += step) {
-            v4u_rows r[RR::kLoads];
-            RR::load(xr, ch, r);
-            put(ch, r);
-          }
+        for (int ch = sub + (held ? HC * step : 0); ch < nch; ch += step) {
+          v4u_rows r[RR::kLoads];
+          RR::load(xr, ch, r);
+          put(ch, r);
         }
       }
     }
-    if constexpr (OUT == kAdapt) {
-      if (s0 == gb) {
-        if (kwi < 4) {
-          const int f = kwi == 0 ? aid[0] : kwi == 1 ? aid[1] : kwi == 2 ? aid[2] : aid[3];
-          if (f >= 0)
-            bh.fetch(a.ad.B + ((int64_t)f * (16 * a.nbe) + 16 * c0 + r16) * a.ad.R, 0, a.ad.R);
-        }
-        for (int i = tid; i < w.rows * a.ad.R; i += kThreads) {
-          const int row = i / a.ad.R, id = a.ad.ids[w.first + row];
-          if (id >= 0 && id < a.ad.L)
-            s_hx[i] = adapter_sum(a.ad, a.M, w.first + row, i - row * a.ad.R, a.ad.scale[id]);
-        }
-      }
+  }
+  if constexpr (OUT == kAdapt) {
+    if (kwi < 4) {
+      const int f = kwi == 0 ? aid[0] : kwi == 1 ? aid[1] : kwi == 2 ? aid[2] : aid[3];
+      if (f >= 0)
+        bh.fetch(a.ad.B + ((int64_t)f * (16 * a.nbe) + 16 * c0 + r16) * a.ad.R, 0, a.ad.R);
     }
-    lds_barrier();
-    if constexpr (OUT == kAdapt) {
-      if (s0 == gb) {
+    for (int i = tid; i < w.rows * a.ad.R; i += kThreads) {
+      const int row = i / a.ad.R, id = a.ad.ids[w.first + row];
+      if (id >= 0 && id < a.ad.L)
+        s_hx[i] = adapter_sum(a.ad, a.M, w.first + row, i - row * a.ad.R, a.ad.scale[id]);
+    }
+  }
+  lds_barrier();
+  if constexpr (OUT == kAdapt) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if ((r & (KW - 1)) == kwi) {
-            float v = 0.0f;
-            if (aid[r] >= 0) {
-              if (r != kwi) bh.fetch(brow(r), 0, a.ad.R);
-              v = bh.dot(s_hx + (4 * j + r) * a.ad.R, brow(r), a.ad.R);
-            }
-            s_dot[cw][r][lane] = v;
-          }
+    for (int r = 0; r < 4; ++r)
+      if ((r & (KW - 1)) == kwi) {
+        float v = 0.0f;
+        if (aid[r] >= 0) {
+          if (r != kwi) bh.fetch(brow(r), 0, a.ad.R);
+          v = bh.dot(s_hx + (4 * j + r) * a.ad.R, brow(r), a.ad.R);
+        }
+        s_dot[cw][r][lane] = v;
       }
-    }
+  }
 
-    // ---- stream the run
-    int g = 0, c = c0;
-    for (int tb = 0; tb < T; tb += D) {
+  // ---- stream the run
+  int g = 0, c = c0;
+  for (int tb = 0; tb < T; tb += D) {
 #pragma unroll
-      for (int i = 0; i < D; ++i) {
-        if (tb + i < T) {
-          v4i lo[NBK], hi[NBK];
-          float sc[NBK];
+    for (int i = 0; i < D; ++i) {
+      if (tb + i < T) {
+        v4i lo[NBK], hi[NBK];
+        float sc[NBK];
+#pragma unroll
+        for (int b = 0; b < NBK; ++b) {
+          const uint32_t zz = ((z[i][b] >> (4 * (r16 & 1))) & 0xFu) * 0x01010101u;
+          unpack_unit(d[i][b], zz, lo[b], hi[b]);
+          sc[b] = s[i][b];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint8_t* frag = ONE ? smem + (k0 + g) * 128 + 16 * j
+                                    : smem + (m * sgn + k0 + g) * 2048 + 16 * lane;
+          const v4i a0 = *reinterpret_cast<const v4i*>(frag);
+          const v4i a1 = *reinterpret_cast<const v4i*>(frag + (ONE ? 64 : 1024));
 #pragma unroll
           for (int b = 0; b < NBK; ++b) {
-            const uint32_t zz = ((z[i][b] >> (4 * (r16 & 1))) & 0xFu) * 0x01010101u;
-            unpack_unit(d[i][b], zz, lo[b], hi[b]);
-            sc[b] = s[i][b];
-          }
+            v4i p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, lo[b], kBiasSeed, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, hi[b], p, 0, 0, 0);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint8_t* frag = ONE ? smem + (k0 + g) * 128 + 16 * j
-                                      : smem + (m * sgn + k0 + g) * 2048 + 16 * lane;
-            const v4i a0 = *reinterpret_cast<const v4i*>(frag);
-            const v4i a1 = *reinterpret_cast<const v4i*>(frag + (ONE ? 64 : 1024));
-#pragma unroll
-            for (int b = 0; b < NBK; ++b) {
-              v4i p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, lo[b], kBiasSeed, 0, 0, 0);
-              p = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, hi[b], p, 0, 0, 0);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[b][m][r] += sc[b] * unbias(p[r]);
-            }
-          }
-          if (++g == kn) {
-            g = 0;
-            if (last && a.kw == 0) {
-              emit(c);
-              ++c;
-#pragma unroll
-              for (int b = 0; b < NBK; ++b)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) acc[b][m][r] = 0.0f;
-            }
+            for (int r = 0; r < 4; ++r) acc[b][m][r] += sc[b] * unbias(p[r]);
           }
         }
-        load(i, tb + i + D);
-        __builtin_amdgcn_sched_barrier(0);
+        if (++g == kn) {
+          g = 0;
+          if (a.kw == 0) {
+            emit(c);
+            ++c;
+#pragma unroll
+            for (int b = 0; b < NBK; ++b)
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[b][m][r] = 0.0f;
+          }
+        }
       }
+      load(i, tb + i + D);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (a.kw == 0) return;
@@ -923,7 +915,7 @@ hipError_t stream_launch(const RowsArgs& a, int64_t blocks, int ksplit, hipStrea
 
 hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int out, int64_t blocks,
                               int ksplit, hipStream_t st) {
-  // what the kernel stages per slice
+  // what the kernel stages
   if (act == kCodes && a.sg * 128 * mt > kThreads * kStageChunks) return hipErrorInvalidValue;
 #define ROWS_CASE(MTV, ONEV, ACTV, OUTV) \
   if (mt == MTV && one == ONEV && act == ACTV && out == OUTV) \
@@ -934,7 +926,6 @@ hipError_t launch_rows_stream(const RowsArgs& a, int mt, bool one, int act, int 
   ROWS_CASE(2, false, kCodes, kSwiglu)
   ROWS_CASE(4, false, kCodes, kSwiglu)
   ROWS_CASE(1, false, kRawBf16, kParts)
-  ROWS_CASE(1, false, kCodes, kParts)
   ROWS_CASE(2, false, kCodes, kParts)
   ROWS_CASE(4, false, kCodes, kParts)
   ROWS_CASE(1, false, kCodes, kSplit)
