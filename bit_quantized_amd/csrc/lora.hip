@@ -150,9 +150,9 @@ adapter_down_kernel(LoraArgs a, int8_t* __restrict__ qa, float* __restrict__ sa,
           RawRow<ACT>::widen(xr[u], v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t h0 = f32_to_bf16_rne(v[2 * e]), h1 = f32_to_bf16_rne(v[2 * e + 1]);
-            const uint32_t l0 = f32_to_bf16_rne(v[2 * e] - __uint_as_float(h0 << 16));
-            const uint32_t l1 = f32_to_bf16_rne(v[2 * e + 1] - __uint_as_float(h1 << 16));
+            uint32_t h0, h1, l0, l1;
+            bf16_parts(v[2 * e], h0, l0);
+            bf16_parts(v[2 * e + 1], h1, l1);
             hi[e] = (int)(h0 | (h1 << 16));
             lo[e] = (int)(l0 | (l1 << 16));
           }
@@ -251,9 +251,9 @@ adapter_parts_kernel(AdaptArgs ad, int64_t M, uint16_t* __restrict__ hi, uint16_
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float v0 = s * (e < 2 ? a[2 * e] : b[2 * e - 4]), v1 = s * (e < 2 ? a[2 * e + 1] : b[2 * e - 3]);
-    const uint32_t h0 = f32_to_bf16_rne(v0), h1 = f32_to_bf16_rne(v1);
-    const uint32_t l0 = f32_to_bf16_rne(v0 - __uint_as_float(h0 << 16));
-    const uint32_t l1 = f32_to_bf16_rne(v1 - __uint_as_float(h1 << 16));
+    uint32_t h0, h1, l0, l1;
+    bf16_parts(v0, h0, l0);
+    bf16_parts(v1, h1, l1);
     h[e] = (int)(h0 | (h1 << 16));
     l[e] = (int)(l0 | (l1 << 16));
   }

@@ -244,6 +244,15 @@ __device__ __forceinline__ void unpack_unit(const v4u_rows& d, uint32_t zz, v4i&
   }
 }
 
+// v as two bf16 parts: the rounded value and the rounded rest, 16 significant
+// bits together.  The first part stops at bf16's largest value, so that a
+// finite v above it stays finite (the rest is then below 2^121).
+__device__ __forceinline__ void bf16_parts(float v, uint32_t& hi, uint32_t& lo) {
+  constexpr float kTop = 0x1.FEp127f;
+  hi = f32_to_bf16_rne(__builtin_amdgcn_fmed3f(v, -kTop, kTop));
+  lo = f32_to_bf16_rne(v - __uint_as_float(hi << 16));
+}
+
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // sum_r hx[r] B[n][r] over one adapter, hx already scaled (LDS), 32 ranks'
