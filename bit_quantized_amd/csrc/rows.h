@@ -80,11 +80,15 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // zeros without a request.  Written as an instruction because the compiler
 // makes every LDS read that follows its builtin wait for the load, whatever
 // buffer it reads; here nothing waits until loads_done() below, which has to
-// come before the barrier that hands the bytes over.  (No register is
-// written; m0, a register the compiler never keeps a value in, has no other
-// use in the kernels that call this.  The compiler's own waits count the
-// loads it knows of, and loads retire in order, so they only become
-// stricter.)
+// come before the barrier that hands the bytes over.  (The compiler's own
+// waits count the loads it knows of, and loads retire in order, so they only
+// become stricter.)
+// The compiler does not look for hazards inside: the load comes five wait
+// states after whatever precedes the block, the rest that a memory request
+// needs after a vector instruction wrote one of its scalar operands (src,
+// base), and more than m0 needs.  m0 is reserved: the compiler sets it right
+// before each use of its own, of which these kernels have none, and refuses it
+// in a clobber list.  tests/test_rows_asm_cpu.py holds the built code to this.
 struct LdsSource {
   v4i words;  // raw byte buffer descriptor
 };
@@ -95,7 +99,7 @@ __device__ __forceinline__ LdsSource lds_source(const void* base, int64_t bytes)
 }
 __device__ __forceinline__ void load_to_lds(const LdsSource& src, uint8_t* lds, int offset, int base) {
   const int at = uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(at), "v"(offset), "s"(src.words), "s"(uniform(base))
                : "memory");
