@@ -627,6 +627,7 @@ def pack_experts(q: torch.Tensor, z: torch.Tensor | None, s: torch.Tensor, n_exp
 
 
 def moe_mlp_workspace_bytes(M: int, k: int, n_experts: int, intermediate: int, hidden: int) -> int:
+    """Bytes of a workspace for M tokens or any smaller number of them."""
     return int(load().w4a8_moe_mlp_workspace_bytes(M, k, n_experts, intermediate, hidden))
 
 
@@ -690,6 +691,7 @@ class LoraAdapters:
 
 
 def lora_linear_workspace_bytes(M: int, N: int, K: int, L: int, R: int) -> int:
+    """Bytes of a workspace for M rows or any smaller number of them."""
     return int(load().w4a8_lora_linear_workspace_bytes(M, N, K, L, R))
 
 

@@ -25,7 +25,6 @@ struct MoePlan {
   int64_t tokens = 0;
   bool direct = false;
   int bm = 0;
-  int64_t max_tiles = 0;
   int64_t qa = 0, sa = 0, count = 0, tiles = 0, list = 0, rank = 0, counts = 0, h = 0, hq = 0, hs = 0, parts = 0;
   int64_t bytes = 0;
 };

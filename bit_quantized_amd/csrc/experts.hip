@@ -388,7 +388,9 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
   const int64_t P = mc * k;
   p.direct = direct(M * k, I, K);
   p.bm = tile_rows(P, E, I, K);
-  p.max_tiles = P / p.bm + (E < P ? E : P);
+  // (room for tiles of the least height, so that the workspace of a batch
+  // serves every smaller one, whatever height that takes)
+  const int64_t max_tiles = P / 16 + (E < P ? E : P);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -400,7 +402,7 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
     p.qa = take(mc * K);
     p.sa = take(mc * 4);
     p.count = take(4);
-    p.tiles = take(p.max_tiles * (int64_t)sizeof(RowTile));
+    p.tiles = take(max_tiles * (int64_t)sizeof(RowTile));
     p.list = take(P * 4);
     p.rank = take(P * 4);
     p.counts = take((int64_t)counters_of(P) * E * 4);

@@ -33,6 +33,8 @@ struct LoraPlan {
 };
 
 LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R);
+// Bytes that the plans of every row count up to M fit in.
+int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int L, int R);
 hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st);
 
 }  // namespace w4a8

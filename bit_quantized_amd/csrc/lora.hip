@@ -10,6 +10,8 @@
 // order of the call.
 #include "lora.h"
 
+#include <algorithm>
+
 namespace w4a8 {
 namespace {
 
@@ -336,6 +338,7 @@ adapt_reduce_sorted_kernel(const float* __restrict__ parts, int ksplit, const fl
 
 constexpr int64_t kMaxPassRows = (int64_t)1 << 20;
 constexpr int64_t kSortBytes = (int64_t)64 << 20;
+constexpr int64_t kMaxSlices = 16;
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -377,10 +380,13 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   p.rows = mc;
   if (mc < 1) return p;
   bool few = false;
-  const GemvShape gs = gemv_shape(N, K);
-  p.gemv = M == 1 && K <= kGemvMaxK && gemv_shape_ok(N, K, gs);
+  if (M == 1 && K <= kGemvMaxK) {
+    const GemvShape gs = gemv_shape(N, K);
+    p.gemv = gemv_shape_ok(N, K, gs);
+    if (p.gemv) p.ksplit = gs.ksplit;
+  }
   if (p.gemv) {
-    p.ksplit = gs.ksplit;
+    // (no tiles)
   } else if (mc <= 64) {
     p.mt = (int)((mc + 15) / 16);
     // one launch, whole K per workgroup and eight wavefronts to a column, where
@@ -411,7 +417,7 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   // where the product's tiles sum the slices again for every strip
   int64_t sl = (p.sorted ? 2 : 4) * cus / (frags * p.slots), most = (K / 32 + kWaves - 1) / kWaves;
   if (sl > most) sl = most;
-  if (sl > 16) sl = 16;
+  if (sl > kMaxSlices) sl = kMaxSlices;
   p.slices = (int)(sl > 1 ? sl : 1);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -434,6 +440,34 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   else p.parts = -1;
   p.bytes = at;
   return p;
+}
+
+// Fewer rows can need more: their K slices are more.  The buffers of lora_plan
+// at their largest over 1 .. M rows, in closed form; each is at least what any
+// of those plans takes.
+int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int L, int R) {
+  const LoraPlan p = lora_plan(M, N, K, L, R);
+  const int64_t cus = device_cus(), m = p.rows, nt = (N + kTileCols - 1) / kTileCols;
+  if (m < 1) return 0;
+  // rows of float sums: ksplit times rows.  Up to 64 rows the K split changes
+  // at 1, 16 and 64; past them a split product has at most cus / 2 tiles, and
+  // ksplit times its tiles is at most cus.
+  int64_t sums = 0;
+  for (int64_t few : {(int64_t)1, (int64_t)16, (int64_t)64}) {
+    const LoraPlan q = few < m ? lora_plan(few, N, K, L, R) : p;
+    if (q.parts >= 0) sums = std::max(sums, q.ksplit * q.rows);
+    if (few >= m) break;
+  }
+  if (m > 64 && 2 * nt <= cus) {
+    const int64_t ks = std::max<int64_t>(1, std::min(cus / nt, K / kGroup / 4));
+    sums = std::max(sums, std::min(ks * m, kTileRows * cus / nt));
+  }
+  // slices of x A^T: at most kMaxSlices, and 4 cus over all 16-row fragments
+  // where there is more than one
+  const int64_t hx = std::max(m, std::min(kMaxSlices * m, 16 * 4 * cus));
+  int64_t bytes = up256(m * K) + up256(m * 4) + up256(hx * R * 4) + up256(sums * N * 4);
+  if (p.sorted) bytes += up256(m * 4) + 2 * up256(m * R * 2);
+  return bytes;
 }
 
 hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {

@@ -192,7 +192,7 @@ int w4a8_moe_mlp(const void* x, int32_t x_dtype, const void* up, size_t up_bytes
 
 size_t w4a8_lora_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t R) {
   if (check_lora(M, N, K, L, R)) return 0;
-  return (size_t)lora_plan(M, N, K, L, R).bytes;
+  return (size_t)lora_workspace(M, N, K, L, R);
 }
 
 int w4a8_lora_linear(const void* x, int32_t x_dtype, const void* packed, size_t packed_bytes_,

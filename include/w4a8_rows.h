@@ -66,7 +66,8 @@ int w4a8_moe_route(const void* logits, int32_t dtype, const float* bias, int64_t
  *   weights  device float [M][k]
  *   y        device bfloat16 bits [M][K]
  *   workspace  device scratch of w4a8_moe_mlp_workspace_bytes(M, k, E, I, K)
- *            bytes; contents on entry are ignored
+ *            bytes; contents on entry are ignored.  The size for M tokens
+ *            serves every smaller number of them
  * The result of a token does not depend on the other tokens of the call
  * except through the kernel that their number selects.  The experts' rows are
  * counted on the device: the call never synchronises and can be captured.
@@ -92,7 +93,10 @@ int w4a8_moe_mlp(const void* x, int32_t x_dtype, const void* up, size_t up_bytes
  *   scale   device float [L]
  *   ids     device int32 [M]; a row whose id lies outside [0, L) has no adapter
  *   y       device bfloat16 bits [M][N]
- *   workspace  device scratch of w4a8_lora_linear_workspace_bytes(M, N, K, L, R)
+ *   workspace  device scratch of w4a8_lora_linear_workspace_bytes(M, N, K, L, R) bytes;
+ *           contents on entry are ignored.  The size for M rows serves every
+ *           smaller number of them (few rows are split further along K and
+ *           can take more room than many)
  * Requirements: as w4a8_linear; R % 8 == 0, 8 <= R <= 128, 1 <= L <= 65536,
  * N * K / 2 below 2^31 bytes.
  */
