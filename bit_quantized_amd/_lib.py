@@ -36,8 +36,27 @@ PATH_PREFILL_N256 = 5      # w4a8_gemm_debug only: prefill with 256 x 256 tiles 
 
 GROUP = 128
 
-# Every symbol the headers declare, with its ctypes signature.
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+
+# Kernels of the products whose weight depends on the row (w4a8_rows.h).
+ROWS_TOKEN = 1
+ROWS_STREAM = 2
+ROWS_RUN = 3
+ROWS_TILE = 4
+
+
+class MoeMlpPlan(ctypes.Structure):
+    """How an expert MLP of these sizes runs (w4a8_moe_mlp_plan_t)."""
+    _fields_ = [("tokens", _i64), ("tile_rows", _i32), ("up_path", _i32), ("down_path", _i32),
+                ("down_columns", _i32)]
+
+
+class LoraLinearPlan(ctypes.Structure):
+    """How an adapter linear of these sizes runs (w4a8_lora_linear_plan_t)."""
+    _fields_ = [("rows", _i64), ("path", _i32), ("ksplit", _i32), ("in_epilogue", _i32), ("sorted", _i32)]
+
+
+# Every symbol the headers declare, with its ctypes signature.
 SIGNATURES = {
     "w4a8_abi_version": (ctypes.c_int, []),
     "w4a8_layout_version": (ctypes.c_int, []),
@@ -81,6 +100,8 @@ SIGNATURES = {
     # include/w4a8_rows.h
     "w4a8_moe_route": (ctypes.c_int, [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
                                       _i32, ctypes.c_float, _vp, _vp, _vp]),
+    "w4a8_moe_mlp_plan": (ctypes.c_int, [_i64, _i32, _i32, _i64, _i64, ctypes.POINTER(MoeMlpPlan)]),
+    "w4a8_lora_linear_plan": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(LoraLinearPlan)]),
     "w4a8_moe_mlp_workspace_bytes": (_sz, [_i64, _i32, _i32, _i64, _i64]),
     "w4a8_moe_mlp": (ctypes.c_int, [_vp, _i32, _vp, _sz, _vp, _sz, _vp, _vp, _i64, _i32, _i32, _i64,
                                     _i64, _vp, _vp, _sz, _vp]),
@@ -626,6 +647,12 @@ def pack_experts(q: torch.Tensor, z: torch.Tensor | None, s: torch.Tensor, n_exp
                          q.shape[0] // n_experts)
 
 
+def moe_mlp_plan(M: int, k: int, n_experts: int, intermediate: int, hidden: int) -> MoeMlpPlan:
+    plan = MoeMlpPlan()
+    _check(load().w4a8_moe_mlp_plan(M, k, n_experts, intermediate, hidden, ctypes.byref(plan)))
+    return plan
+
+
 def moe_mlp_workspace_bytes(M: int, k: int, n_experts: int, intermediate: int, hidden: int) -> int:
     """Bytes of a workspace for M tokens or any smaller number of them."""
     return int(load().w4a8_moe_mlp_workspace_bytes(M, k, n_experts, intermediate, hidden))
@@ -688,6 +715,12 @@ class LoraAdapters:
         L, R, _ = self.A.shape
         if self.B.shape[0] != L or self.B.shape[2] != R or tuple(self.scale.shape) != (L,):
             raise ValueError("A [L][R][K], B [L][N][R] and scale [L] do not fit together")
+
+
+def lora_linear_plan(M: int, N: int, K: int, L: int, R: int) -> LoraLinearPlan:
+    plan = LoraLinearPlan()
+    _check(load().w4a8_lora_linear_plan(M, N, K, L, R, ctypes.byref(plan)))
+    return plan
 
 
 def lora_linear_workspace_bytes(M: int, N: int, K: int, L: int, R: int) -> int:

@@ -388,6 +388,12 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
   const int64_t P = mc * k;
   p.direct = direct(M * k, I, K);
   p.bm = tile_rows(P, E, I, K);
+  const int64_t G = K / kGroup, GI = I / kGroup;
+  const int staged = p.bm < kTileRows ? staged_groups(p.bm / 16) : 0;
+  p.raw = !p.direct && p.bm == 16 && GI <= 32;  // (few rows share a tile)
+  p.up = p.direct ? kTokenPath : p.bm == kTileRows ? kTilePath : G <= staged ? kStreamPath : kRunPath;
+  p.down = p.direct ? kTokenPath : p.bm == kTileRows ? kTilePath : p.raw || GI <= staged ? kStreamPath : kRunPath;
+  if (p.direct) p.bm = 1;
   // (room for tiles of the least height, so that the workspace of a batch
   // serves every smaller one, whatever height that takes)
   const int64_t max_tiles = P / 16 + (E < P ? E : P);
@@ -412,6 +418,17 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
   }
   p.bytes = at;
   return p;
+}
+
+// Runs of about 24 units per wavefront, but columns shared out while the
+// tiles that can be expected leave compute units without a workgroup (644
+// tokens of 7, 15 experts, 128 -> 384: 35 us against 61).
+int down_columns(const MoePlan& p, int64_t P, int E, int64_t I, int64_t K) {
+  const int64_t GI = I / kGroup, cols = K / 16;
+  const int64_t tiles = P / p.bm + (E < P ? E : P) / 2 + 1;
+  const int64_t most = cols * tiles / (8 * (int64_t)device_cus());
+  const int64_t n = (24 + GI - 1) / GI;
+  return (int)(n <= most ? n : most > 1 ? most : 1);
 }
 
 static hipError_t moe_direct(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
@@ -479,7 +496,6 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
-  const bool big = p.bm == kTileRows;
   const int mt = p.bm / 16;
   RowsArgs a{};
   a.qa = qa;
@@ -499,24 +515,21 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
   a.div = m.k;
   a.cols = (int)(m.I / 16);
   a.h = h;
-  const int G = (int)(m.K / kGroup), GI = (int)(m.I / kGroup);
-  if (big) {
+  if (p.up == kTilePath) {
     a.strips = a.cols / 8;
     e = launch_rows_tile(a, kSwiglu, max_tiles * a.strips, 1, st);
   } else {
     a.kw = 0;
     a.ncol = 1;
     a.strips = (a.cols + 7) / 8;
-    a.sg = G;
-    e = G <= staged_groups(mt)
+    a.sg = (int)(m.K / kGroup);
+    e = p.up == kStreamPath
             ? launch_rows_stream(a, mt, false, kCodes, kSwiglu, max_tiles * a.strips, 1, st)
             : launch_rows_run(a, mt, kSwiglu, max_tiles * a.strips, 1, st);
   }
   if (e != hipSuccess) return e;
 
-  // the down product quantises its rows itself where few rows share a tile
-  const bool raw = p.bm == 16 && GI <= 32;
-  if (!raw) {
+  if (!p.raw) {
     if (m.I <= 64 * 8 * kRowHeld) {
       hipLaunchKernelGGL(quant_pairs_kernel, dim3((unsigned)((P + kWaves - 1) / kWaves)), dim3(kThreads), 0, st,
                          h, m.ids, P, m.E, (int)m.I, hq, hs);
@@ -541,23 +554,17 @@ hipError_t launch_moe(const MoeArgs& m, const MoePlan& p, hipStream_t st) {
   d.pw = m.weights;
   d.h = nullptr;
   d.parts = parts;
-  if (big) {
+  if (p.down == kTilePath) {
     d.strips = (d.nbe + 15) / 16;
     e = launch_rows_tile(d, kParts, max_tiles * d.strips, 1, st);
   } else {
-    d.sg = GI;
+    d.sg = (int)(m.I / kGroup);
     d.kw = 0;
-    // runs of about 24 units per wavefront, but columns shared out while the
-    // tiles that can be expected leave compute units without a workgroup (644
-    // tokens of 7, 15 experts, 128 -> 384: 35 us against 61)
-    const int64_t tiles = P / p.bm + (m.E < P ? m.E : P) / 2 + 1;
-    const int64_t most = d.cols * tiles / (8 * (int64_t)device_cus());
-    d.ncol = (24 + GI - 1) / GI;
-    if (d.ncol > most) d.ncol = most > 1 ? (int)most : 1;
+    d.ncol = down_columns(p, P, m.E, m.I, m.K);
     const int per = 8 * d.ncol;
     d.strips = (d.cols + per - 1) / per;
-    e = raw || GI <= staged_groups(mt)
-            ? launch_rows_stream(d, mt, false, raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st)
+    e = p.down == kStreamPath
+            ? launch_rows_stream(d, mt, false, p.raw ? kRawBf16 : kCodes, kParts, max_tiles * d.strips, 1, st)
             : launch_rows_run(d, mt, kParts, max_tiles * d.strips, 1, st);
   }
   if (e != hipSuccess) return e;

@@ -21,7 +21,8 @@ struct LoraArgs {
 // How a pass of at most `rows` rows runs, and its buffers in the workspace.
 struct LoraPlan {
   int64_t rows = 0;
-  bool gemv = false;  // one row: the M = 1 GEMV
+  int path = 0;       // RowPath of the shared product (one row: the M = 1 GEMV)
+  bool gemv = false;
   int mt = 0;      // 16-row tiles of the streaming kernel; 0: the 256-row tile kernel
   int kw = 0;      // streaming kernel: log2 wavefronts per column
   int ksplit = 1;  // K slices across workgroups (float sums, then a reduction)

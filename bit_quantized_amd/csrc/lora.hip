@@ -435,6 +435,10 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   }
   // (the streaming kernels go through the sums unless a column is whole, few
   // tiles so that the adapters' part runs on more compute units than they)
+  p.path = p.gemv ? kTokenPath
+           : !p.mt ? kTilePath
+           : p.kw == 0 && (G + p.ksplit - 1) / p.ksplit > staged_groups(p.mt) ? kRunPath
+                                                                              : kStreamPath;
   const bool sums = p.ksplit > 1 || (p.mt && p.kw == 0) || few;
   if (sums) p.parts = take((int64_t)p.ksplit * mc * N * 4);
   else p.parts = -1;
@@ -534,7 +538,7 @@ hipError_t launch_lora(const LoraArgs& l, const LoraPlan& p, hipStream_t st) {
     a.ncol = 1;
     const int cw = 8 >> p.kw, per = (G + p.ksplit - 1) / p.ksplit;
     a.strips = (a.cols + cw - 1) / cw;
-    if (parts && per > staged_groups(p.mt)) {
+    if (p.path == kRunPath) {
       e = launch_rows_run(a, p.mt, kSplit, a.strips, p.ksplit, st);
     } else {
       a.sg = per;

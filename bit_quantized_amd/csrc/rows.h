@@ -34,6 +34,13 @@ enum RowOut {
   kSplit = 2,   // unscaled float sums of one K slice
   kAdapt = 3,   // bf16 with the row's adapter product added
 };
+// The kernels that a product runs on; values of the plan queries (w4a8_rows.h).
+enum RowPath {
+  kTokenPath = 1,   // a single token's pairs, a single row
+  kStreamPath = 2,  // rows_stream_kernel
+  kRunPath = 3,     // rows_run_kernel
+  kTilePath = 4,    // rows_tile_kernel
+};
 enum RowAct { kCodes = 0, kRawBf16 = 1, kRawF32 = 2 };
 
 // A tile of grouped rows: pairs list[first .. first + rows) of `expert`; it is

@@ -190,9 +190,33 @@ int w4a8_moe_mlp(const void* x, int32_t x_dtype, const void* up, size_t up_bytes
   return finish(e, "expert MLP launch");
 }
 
+int w4a8_moe_mlp_plan(int64_t M, int32_t k, int32_t E, int64_t I, int64_t K, w4a8_moe_mlp_plan_t* plan) {
+  if (!plan) return fail(W4A8_ERR_INVALID_ARG, "null plan");
+  if (int rc = check_moe(M, k, E, I, K)) return rc;
+  const MoePlan p = moe_plan(M, k, E, I, K);
+  plan->tokens = p.tokens;
+  plan->tile_rows = p.bm;
+  plan->up_path = p.up;
+  plan->down_path = p.down;
+  plan->down_columns = p.down == kStreamPath || p.down == kRunPath ? down_columns(p, p.tokens * k, E, I, K) : 1;
+  return report_error(W4A8_OK, "");
+}
+
 size_t w4a8_lora_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t R) {
   if (check_lora(M, N, K, L, R)) return 0;
   return (size_t)lora_workspace(M, N, K, L, R);
+}
+
+int w4a8_lora_linear_plan(int64_t M, int64_t N, int64_t K, int32_t L, int32_t R, w4a8_lora_linear_plan_t* plan) {
+  if (!plan) return fail(W4A8_ERR_INVALID_ARG, "null plan");
+  if (int rc = check_lora(M, N, K, L, R)) return rc;
+  const LoraPlan p = lora_plan(M, N, K, L, R);
+  plan->rows = p.rows;
+  plan->path = p.path;
+  plan->ksplit = p.ksplit;
+  plan->in_epilogue = p.parts < 0;
+  plan->sorted = p.sorted;
+  return report_error(W4A8_OK, "");
 }
 
 int w4a8_lora_linear(const void* x, int32_t x_dtype, const void* packed, size_t packed_bytes_,

@@ -14,6 +14,30 @@
 extern "C" {
 #endif
 
+/*
+ * How a call runs, chosen from its sizes and the device's compute units (256
+ * on MI355X): host only, for tests and tuning; nothing is enqueued.  Kernels:
+ */
+#define W4A8_ROWS_TOKEN 1  /* a single token's experts, a single adapted row */
+#define W4A8_ROWS_STREAM 2 /* weights streamed past activations staged at once */
+#define W4A8_ROWS_RUN 3    /* weights streamed, activations in slices */
+#define W4A8_ROWS_TILE 4   /* 256 rows x 256 channels on the matrix cores */
+typedef struct {
+  int64_t tokens;       /* of a pass; more of them run in several */
+  int32_t tile_rows;    /* (token, slot) pairs that a tile of one expert holds */
+  int32_t up_path;      /* W4A8_ROWS_* of the up and the down product */
+  int32_t down_path;
+  int32_t down_columns; /* 16-channel columns that a wavefront of the down product
+                           takes one after another (STREAM, RUN) */
+} w4a8_moe_mlp_plan_t;
+typedef struct {
+  int64_t rows;         /* of a pass */
+  int32_t path;         /* W4A8_ROWS_* of the shared product */
+  int32_t ksplit;       /* its slices of the inputs */
+  int32_t in_epilogue;  /* the product's kernel adds the adapters, else a reduction does */
+  int32_t sorted;       /* rows taken in the order of their adapters */
+} w4a8_lora_linear_plan_t;
+
 /* score functions of w4a8_moe_route */
 #define W4A8_SCORE_SOFTMAX 0
 #define W4A8_SCORE_SIGMOID 1
@@ -74,6 +98,7 @@ int w4a8_moe_route(const void* logits, int32_t dtype, const float* bias, int64_t
  * Requirements: 1 <= M <= 2^24, 1 <= k <= 64, 1 <= E <= 1024, I % 128 == 0,
  * K % 128 == 0, one expert's 2 I K / 2 code bytes below 2^31.
  */
+int w4a8_moe_mlp_plan(int64_t M, int32_t k, int32_t E, int64_t I, int64_t K, w4a8_moe_mlp_plan_t* plan);
 size_t w4a8_moe_mlp_workspace_bytes(int64_t M, int32_t k, int32_t E, int64_t I, int64_t K);
 int w4a8_moe_mlp(const void* x, int32_t x_dtype, const void* up, size_t up_bytes, const void* down,
                  size_t down_bytes, const int32_t* ids, const float* weights, int64_t M, int32_t k,
@@ -100,6 +125,7 @@ int w4a8_moe_mlp(const void* x, int32_t x_dtype, const void* up, size_t up_bytes
  * Requirements: as w4a8_linear; R % 8 == 0, 8 <= R <= 128, 1 <= L <= 65536,
  * N * K / 2 below 2^31 bytes.
  */
+int w4a8_lora_linear_plan(int64_t M, int64_t N, int64_t K, int32_t L, int32_t R, w4a8_lora_linear_plan_t* plan);
 size_t w4a8_lora_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t R);
 int w4a8_lora_linear(const void* x, int32_t x_dtype, const void* packed, size_t packed_bytes,
                      const uint16_t* A, const uint16_t* B, const float* scale, const int32_t* ids,

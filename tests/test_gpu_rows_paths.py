@@ -1,0 +1,65 @@
+"""GPU: the kernels of the expert MLP and the adapter linear that only larger
+batches take, each case with the kernel that it has to reach (the plan queries
+of include/w4a8_rows.h), so that a change of the rules that choose cannot
+leave one of them without a test.
+
+Definitions, checks and tolerances are those of test_gpu_rows.py.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_rows import (acts, check_lora, check_moe, gen, lora_case, moe_case, moe_ref, pack, randn, w4,  # noqa: E402, F401
+                           weight)
+
+STREAM, RUN, TILE = 2, 3, 4
+
+# 256-row tiles, at least three groups of inputs (odd and even numbers), several strips of channels,
+# a last strip of half a tile: M, k, E, I, K
+MOE_TILE = [(4500, 3, 5, 384, 640), (1700, 6, 6, 640, 1152), (3001, 3, 3, 640, 1280), (12000, 1, 7, 512, 640)]
+
+
+@pytest.mark.parametrize("M,k,E,I,K", MOE_TILE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("skew", [False, True], ids=["even", "skewed"])
+def test_moe_tiles(w4, M, k, E, I, K, dtype, skew):  # noqa: F811
+    p = w4.moe_mlp_plan(M, k, E, I, K)
+    assert (p.tile_rows, p.up_path, p.down_path) == (256, TILE, TILE)
+    x, up, down, ids, wt = moe_case(M + K, M, k, E, I, K, dtype, drop=0.3 if skew else 0.0, skew=skew)
+    y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
+    check_moe(y, *moe_ref(x, up, down, ids, wt, E))
+
+
+# rows of each expert: whole tiles, last tiles of up to 64, 128 and more rows, and an expert without any
+ENDS = [2048, 1, 2 * 256 + 63, 3 * 256 + 64, 256 + 65, 0, 5 * 256 + 127, 4 * 256 + 128, 1024 + 129, 6 * 256 + 200, 3 * 256 + 255]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_moe_tile_ends(w4, dtype):  # noqa: F811
+    """Every kind of last tile, slots of other experts between them, repeated
+    calls with the same bits, and nothing written outside."""
+    k, E, I, K = 3, len(ENDS), 384, 896
+    g = gen(99)
+    flat = torch.cat([torch.full((n,), e, dtype=torch.int32) for e, n in enumerate(ENDS)] +
+                     [torch.full((998,), -1, dtype=torch.int32), torch.full((500,), E, dtype=torch.int32)])
+    flat = flat[: flat.numel() // k * k]
+    ids = flat[torch.randperm(flat.numel(), generator=torch.Generator().manual_seed(5))].view(-1, k).cuda().contiguous()
+    M = ids.shape[0]
+    p = w4.moe_mlp_plan(M, k, E, I, K)
+    assert (p.tile_rows, p.up_path, p.down_path) == (256, TILE, TILE)
+    x = acts(g, M, K, dtype)
+    up, down = weight(g, E * 2 * I, K), weight(g, E * K, I)
+    wt = torch.softmax(randn(g, M, k), dim=1).contiguous()
+    ups = pack(w4, up, down, E)
+    y = w4.moe_mlp(x, *ups, ids, wt)
+    check_moe(y, *moe_ref(x, up, down, ids, wt, E))
+    need = w4.moe_mlp_workspace_bytes(M, k, E, I, K)
+    buf = torch.randint(0, 256, (need + 8192,), generator=g, device="cuda", dtype=torch.uint8)
+    guard = buf.clone()
+    band = torch.full((M * K + 4096,), 7.0, device="cuda", dtype=torch.bfloat16)
+    for _ in range(3):
+        out = w4.moe_mlp(x, *ups, ids, wt, out=band[2048: 2048 + M * K].view(M, K), workspace=buf[4096: 4096 + need])
+        assert torch.equal(out, y)
+    assert torch.equal(buf[:4096], guard[:4096]) and torch.equal(buf[4096 + need:], guard[4096 + need:])
+    assert (band[:2048] == 7).all() and (band[2048 + M * K:] == 7).all()

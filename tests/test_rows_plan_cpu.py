@@ -1,0 +1,47 @@
+"""CPU: the plan queries of include/w4a8_rows.h, and that every kernel the expert
+MLP and the adapter linear can take is taken by some GPU test's sizes."""
+import ctypes
+
+import pytest
+
+pytest.importorskip("torch")
+
+import bit_quantized_amd as w4
+import test_gpu_rows
+import test_gpu_rows_long
+import test_gpu_rows_paths as paths
+from bit_quantized_amd import _lib
+
+TOKEN, STREAM, RUN, TILE = w4.ROWS_TOKEN, w4.ROWS_STREAM, w4.ROWS_RUN, w4.ROWS_TILE
+
+
+def moe_plans():
+    cases = [c[:5] for c in test_gpu_rows.MOE + test_gpu_rows_long.MOE + paths.MOE_TILE]
+    return [(c, w4.moe_mlp_plan(*c)) for c in cases]
+
+
+def test_gpu_tests_reach_every_expert_kernel():
+    plans = moe_plans()
+    up = {(p.tile_rows, p.up_path) for _, p in plans}
+    assert up == {(1, TOKEN), (16, STREAM), (16, RUN), (32, STREAM), (32, RUN), (64, STREAM), (64, RUN), (256, TILE)}
+    assert {(p.tile_rows, p.down_path) for _, p in plans} == up
+    # 256-row tiles: the groups' two buffers change places, several strips, a last strip of half a tile
+    tiles = [c for c, p in plans if p.up_path == TILE]
+    assert {c[4] // 128 % 2 for c in tiles} == {0, 1} and {c[3] // 128 % 2 for c in tiles} == {0, 1}
+    assert all(min(c[3], c[4]) // 128 >= 3 for c in tiles) and any(c[4] // 16 % 16 for c in tiles)
+
+
+def test_plan_queries_refuse():
+    lib = _lib.load()
+    moe, lora = _lib.MoeMlpPlan(), _lib.LoraLinearPlan()
+    assert lib.w4a8_moe_mlp_plan(4, 2, 8, 256, 384, None) == -1
+    assert lib.w4a8_lora_linear_plan(4, 256, 384, 3, 16, None) == -1
+    for args, status in (((0, 2, 8, 256, 384), -1), ((4, 0, 8, 256, 384), -1), ((4, 2, 8, 200, 384), -2)):
+        assert lib.w4a8_moe_mlp_plan(*args, ctypes.byref(moe)) == status
+    for args, status in (((0, 256, 384, 3, 16), -1), ((4, 256, 384, 3, 7), -2), ((4, 256, 200, 3, 16), -2)):
+        assert lib.w4a8_lora_linear_plan(*args, ctypes.byref(lora)) == status
+    with pytest.raises(w4._lib.W4A8Error):
+        w4.moe_mlp_plan(4, 2, 8, 200, 384)
+    with pytest.raises(w4._lib.W4A8Error):
+        w4.lora_linear_plan(4, 256, 384, 3, 7)
+    assert w4.moe_mlp_plan(1 << 20, 8, 8, 256, 4096).tokens < 1 << 20  # several passes
