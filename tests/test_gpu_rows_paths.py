@@ -63,3 +63,22 @@ def test_moe_tile_ends(w4, dtype):  # noqa: F811
         assert torch.equal(out, y)
     assert torch.equal(buf[:4096], guard[:4096]) and torch.equal(buf[4096 + need:], guard[4096 + need:])
     assert (band[:2048] == 7).all() and (band[2048 + M * K:] == 7).all()
+
+
+# several columns to a wavefront of the down product, with columns that end inside a strip and inside
+# a wavefront's share: M, k, E, I, K, tile rows, kernel, columns
+MOE_COLUMNS = [
+    (60, 3, 40, 128, 4224, 16, STREAM, 4), (40, 4, 32, 256, 4096, 16, STREAM, 3), (100, 4, 32, 128, 4096, 32, STREAM, 3),
+    (300, 5, 32, 128, 4224, 64, STREAM, 5), (300, 6, 24, 512, 4096, 64, STREAM, 5), (120, 4, 32, 2176, 2432, 32, RUN, 2),
+    (300, 5, 24, 1152, 4096, 64, RUN, 3), (300, 5, 24, 2176, 2176, 64, RUN, 2),
+]
+
+
+@pytest.mark.parametrize("M,k,E,I,K,rows,path,columns", MOE_COLUMNS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_moe_columns(w4, M, k, E, I, K, rows, path, columns, dtype):  # noqa: F811
+    p = w4.moe_mlp_plan(M, k, E, I, K)
+    assert (p.tile_rows, p.down_path, p.down_columns) == (rows, path, columns)
+    x, up, down, ids, wt = moe_case(M + K, M, k, E, I, K, dtype, drop=0.2, skew=E % 3 == 0)
+    y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
+    check_moe(y, *moe_ref(x, up, down, ids, wt, E))

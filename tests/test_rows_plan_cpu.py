@@ -16,7 +16,7 @@ TOKEN, STREAM, RUN, TILE = w4.ROWS_TOKEN, w4.ROWS_STREAM, w4.ROWS_RUN, w4.ROWS_T
 
 
 def moe_plans():
-    cases = [c[:5] for c in test_gpu_rows.MOE + test_gpu_rows_long.MOE + paths.MOE_TILE]
+    cases = [c[:5] for c in test_gpu_rows.MOE + test_gpu_rows_long.MOE + paths.MOE_TILE + paths.MOE_COLUMNS]
     return [(c, w4.moe_mlp_plan(*c)) for c in cases]
 
 
@@ -24,7 +24,10 @@ def test_gpu_tests_reach_every_expert_kernel():
     plans = moe_plans()
     up = {(p.tile_rows, p.up_path) for _, p in plans}
     assert up == {(1, TOKEN), (16, STREAM), (16, RUN), (32, STREAM), (32, RUN), (64, STREAM), (64, RUN), (256, TILE)}
-    assert {(p.tile_rows, p.down_path) for _, p in plans} == up
+    down = {(p.tile_rows, p.down_path, p.down_columns > 1) for _, p in plans}
+    one = {(r, s, False) for r, s in up}
+    # (16 rows: past 32 groups a column is a run of its own)
+    assert down == one | {(16, STREAM, True), (32, STREAM, True), (64, STREAM, True), (32, RUN, True), (64, RUN, True)}
     # 256-row tiles: the groups' two buffers change places, several strips, a last strip of half a tile
     tiles = [c for c, p in plans if p.up_path == TILE]
     assert {c[4] // 128 % 2 for c in tiles} == {0, 1} and {c[3] // 128 % 2 for c in tiles} == {0, 1}
