@@ -82,3 +82,22 @@ def test_moe_columns(w4, M, k, E, I, K, rows, path, columns, dtype):  # noqa: F8
     x, up, down, ids, wt = moe_case(M + K, M, k, E, I, K, dtype, drop=0.2, skew=E % 3 == 0)
     y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
     check_moe(y, *moe_ref(x, up, down, ids, wt, E))
+
+
+# the adapters added by the 256-row tiles, ranks in one and in several steps of 32, whole and half tiles,
+# and a few rows over many channels and groups: M, K, N, L, R, seg, kernel, in the epilogue
+LORA_PATHS = [
+    (300, 384, 33040, 3, 72, 1, TILE, 1), (300, 384, 33040, 3, 128, 7, TILE, 1), (1030, 256, 17424, 6, 96, 5, TILE, 1),
+    (1000, 384, 17424, 6, 128, 1, TILE, 1), (1000, 256, 25504, 5, 104, 300, TILE, 1), (257, 256, 33040, 200, 64, 1, TILE, 1),
+    (10, 4224, 32784, 3, 16, 1, RUN, 0), (16, 4608, 32784, 20, 104, 1, RUN, 0),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,R,seg,path,epilogue", LORA_PATHS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_lora_paths(w4, M, K, N, L, R, seg, path, epilogue, dtype):  # noqa: F811
+    p = w4.lora_linear_plan(M, N, K, L, R)
+    assert (p.path, p.in_epilogue) == (path, epilogue)
+    x, w, A, B, sc, ids = lora_case(M + N, M, K, N, L, R, dtype, seg)
+    y = w4.lora_linear(x, w4.pack_weights(*w), w4.LoraAdapters(A, B, sc), ids)
+    check_lora(y, x, w, A, B, sc, ids)

@@ -34,6 +34,17 @@ def test_gpu_tests_reach_every_expert_kernel():
     assert all(min(c[3], c[4]) // 128 >= 3 for c in tiles) and any(c[4] // 16 % 16 for c in tiles)
 
 
+def test_gpu_tests_reach_every_adapter_kernel():
+    cases = [c[:5] for c in test_gpu_rows.LORA + test_gpu_rows_long.LORA + paths.LORA_PATHS]
+    plans = [(c, w4.lora_linear_plan(c[0], c[2], c[1], c[3], c[4])) for c in cases]
+    reached = {(p.path, (c[0] + 15) // 16 if p.path in (STREAM, RUN) else 0, p.in_epilogue) for c, p in plans}
+    want = {(TOKEN, 0, 1), (TOKEN, 0, 0), (STREAM, 1, 1), (TILE, 0, 0), (TILE, 0, 1)}
+    assert reached == want | {(s, n, 0) for s in (STREAM, RUN) for n in (1, 2, 3, 4)}
+    assert {-(-c[4] // 32) for c, p in plans if p.path == TILE and p.in_epilogue} == {1, 2, 3, 4}  # steps of 32 ranks
+    assert {p.sorted for c, p in plans if c[0] <= 64} == {0, 1}
+    assert any(p.ksplit > 1 for c, p in plans if p.path == TILE)
+
+
 def test_plan_queries_refuse():
     lib = _lib.load()
     moe, lora = _lib.MoeMlpPlan(), _lib.LoraLinearPlan()
