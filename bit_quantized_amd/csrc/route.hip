@@ -23,29 +23,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTokens = kThreads / 64;
 
-template <int CTRL>
-__device__ __forceinline__ double dpp_max_step(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xF, 0xF, true);
-  return fmax(v, __builtin_bit_cast(double, (uint64_t)hi << 32 | lo));
-}
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-// Maximum over the wavefront, as wave_max64 for floats.
-__device__ __forceinline__ double wave_top(double v) {
-  v = dpp_max_step<0xB1>(v);
-  v = dpp_max_step<0x4E>(v);
-  v = dpp_max_step<0x141>(v);
-  v = dpp_max_step<0x140>(v);
-  return fmax(fmax(lane_value(v, 0), lane_value(v, 16)), fmax(lane_value(v, 32), lane_value(v, 48)));
-}
-__device__ __forceinline__ float wave_top(float v) { return wave_max64(v); }
-
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
@@ -53,7 +30,12 @@ __device__ __forceinline__ T wave_sum(T v) {
   return v;
 }
 
-__device__ __forceinline__ double lane_of(double v, int lane) { return lane_value(v, lane); }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ float lane_of(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
@@ -138,7 +120,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, S (&sel)[VPL], int fi
     }
     const bool keep = mine < a.n_groups && rank < a.topk_groups;
     if constexpr (CHECKED) {
-      const S most = wave_top(keep ? kNone : value);  // of the groups left out
+      static_assert(sizeof(S) == 4, "rounded scores are floats");
+      const S most = wave_max64(keep ? kNone : value);  // of the groups left out
       if (__ballot(keep && !(value - most > 2 * tol))) return false;
     }
     if (!keep) {
