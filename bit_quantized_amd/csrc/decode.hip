@@ -461,8 +461,7 @@ skinny_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scale
       if (c < nx) {
         float v[8];
         XChunk<T>::widen(xr[c], v);
-        // a zero row gives codes 0 (its quotients would be 0/0)
-        const uint2 codes = amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+        const uint2 codes = quant8_codes(v, scale, inv);
         *reinterpret_cast<uint2*>(qrow + c * 8 * kRowThreads) = codes;
       }
     }

@@ -188,7 +188,7 @@ quant_pairs_kernel(const uint16_t* __restrict__ h, const int* __restrict__ ids, 
       float v[8];
       RawRow<kRawBf16>::widen(raw[i], v);
       *reinterpret_cast<uint2*>(hq + p * I + 8 * (lane + 64 * i)) =
-          amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+          quant8_codes(v, scale, inv);
     }
 }
 
@@ -264,7 +264,7 @@ down_token_kernel(RowsArgs a, int k) {
         float t[8];
         RawRow<kRawBf16>::widen(raw, t);
         *reinterpret_cast<uint2*>(q + 8 * ch) =
-            amax != 0.0f ? quant8_codes(t, scale, inv) : make_uint2(0u, 0u);
+            quant8_codes(t, scale, inv);
       };
 #pragma unroll
       for (int i = 0; i < kRowHeld; ++i)

@@ -378,7 +378,7 @@ gemv_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
       scale = __uint_as_float(
           __hip_atomic_load(&s_sync[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) / 127.0f;
     }
-    const float inv = scale != 0.0f ? 1.0f / scale : 0.0f;  // correctly rounded
+    const float inv = 1.0f / scale;  // correctly rounded
     for (int b = nbatch - 1; b >= 0; --b) {
       if (b != nbatch - 1) {
 #pragma unroll
@@ -402,9 +402,8 @@ gemv_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
             pk = make_uint2(xr[i][0].x, xr[i][0].y);
           } else {
             // the rule of w4a8_quant_act (or w4a8_quant_act_hadamard), bit
-            // for bit (quant8_codes); an all-zero token has scale 0 and
-            // all-zero codes
-            pk = scale != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+            // for bit; an all-zero token has scale 0 and all-zero codes
+            pk = quant8_codes(v, scale, inv);
           }
           *reinterpret_cast<uint2*>(qs + 8 * ch) = pk;
           // chunk ch covers elements 8(ch%16)..+7 of group ch/16: quarter

@@ -42,9 +42,9 @@ struct Chunk8<float> {
 
 __device__ __forceinline__ float wave_max(float v) { return wave_max64(v); }
 
-// Codes of eight activations under one row scale (a zero row: codes 0).
-__device__ __forceinline__ uint2 quant8(const float* v, float amax, float scale) {
-  return amax != 0.0f ? quant8_codes(v, scale, 1.0f / scale) : make_uint2(0u, 0u);
+// Codes of eight activations under one row scale.
+__device__ __forceinline__ uint2 quant8(const float* v, float scale) {
+  return quant8_codes(v, scale, 1.0f / scale);
 }
 
 
@@ -89,7 +89,7 @@ quant_act_kernel(const T* __restrict__ x, int64_t K, int8_t* __restrict__ qa,
     float v[8];
     Chunk8<T>::load(row + ch * 8, v);
     if (HAD) hadamard_chunk(v);
-    *reinterpret_cast<uint2*>(out + ch * 8) = quant8(v, amax, scale);
+    *reinterpret_cast<uint2*>(out + ch * 8) = quant8(v, scale);
   }
 }
 
@@ -178,7 +178,7 @@ quant_row_kernel(const T* __restrict__ x, int64_t K, int8_t* __restrict__ qa,
   for (int c = 0; c < NPT; ++c) {
     const int ch = threadIdx.x + c * kRowThreads;
     if (ch < chunks)
-      *reinterpret_cast<uint2*>(qa + code_offset<TILED>(m, K, ch)) = quant8(v[c], amax, scale);
+      *reinterpret_cast<uint2*>(qa + code_offset<TILED>(m, K, ch)) = quant8(v[c], scale);
   }
 }
 

@@ -232,7 +232,7 @@ __device__ __forceinline__ void quantise_row(const uint8_t* xr, int K, int8_t* o
     float v[8];
     RR::widen(r, v);
     *reinterpret_cast<uint2*>(out + 8 * (int64_t)ch) =
-        amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+        quant8_codes(v, scale, inv);
   };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)

@@ -264,7 +264,7 @@ rows_stream_kernel(RowsArgs a) {
         auto put = [&](int ch, const v4u_rows* r) __attribute__((always_inline)) {
           float v[8];
           RR::widen(r, v);
-          const uint2 codes = amax != 0.0f ? quant8_codes(v, scale, inv) : make_uint2(0u, 0u);
+          const uint2 codes = quant8_codes(v, scale, inv);
           const int g = ch >> 4, h = (ch >> 3) & 1, jj = (ch >> 1) & 3;
           const int at = ONE ? ((g * 2 + h) * 4 + jj) * 16
                              : (((row >> 4) * sgn + g) * 2 + h) * 1024 + (16 * jj + (row & 15)) * 16;

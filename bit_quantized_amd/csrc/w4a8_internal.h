@@ -94,20 +94,21 @@ __device__ __forceinline__ float wave_max64(float v) {
   return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
-// Codes of eight finite activations under a row scale s > 0 with inv the
-// correctly rounded 1 / s: rint(x / s) (IEEE quotient, ties to even) clamped
-// to [-127, 127], as bytes.  The quotient is taken as x * inv, which differs
-// from the IEEE x / s by less than 2.3e-5 for |x / s| <= 127.5 (each is
-// within 2 ulp-of-1 relative rounding of the real quotient); the two can
-// round to different integers only when the product lies within that
-// distance of a boundary n + 1/2, so such elements (|t - rint(t)| > 1/2 -
-// 2^-14) are redone with the IEEE quotient.  Adding 1.5 * 2^23 rounds a
-// float of magnitude <= 127 to an integer (round to nearest even) whose
-// low byte is then the two's-complement code.
+// Codes of eight finite activations under a row scale s with inv the correctly
+// rounded 1 / s: rint(x / s) (IEEE quotient, ties to even; 0 for x = 0)
+// clamped to [-127, 127], as bytes.  The quotient is taken as x * inv, which
+// differs from the IEEE x / s by less than 2.3e-5 for |x / s| <= 127.5 (each
+// is within 2 ulp-of-1 relative rounding of the real quotient); the two can
+// round to different integers only when the product lies within that distance
+// of a boundary n + 1/2, so such elements (|t - rint(t)| > 1/2 - 2^-14) are
+// redone with the IEEE quotient, and so are all where 1 / s overflows (s up to
+// 2^-128, an all-zero row's 0 among them).  Adding 1.5 * 2^23 rounds a float of
+// magnitude <= 127 to an integer (round to nearest even) whose low byte is
+// then the two's-complement code.
 __device__ __forceinline__ uint2 quant8_codes(const float* v, float s, float inv) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
   uint32_t b[8];
-  bool near = false;
+  bool near = !(s > 0x1p-128f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = __builtin_amdgcn_fmed3f(v[i] * inv, -127.0f, 127.0f);
@@ -118,7 +119,7 @@ __device__ __forceinline__ uint2 quant8_codes(const float* v, float s, float inv
   if (near) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float r = fminf(fmaxf(rintf(v[i] / s), -127.0f), 127.0f);
+      const float r = fminf(fmaxf(rintf(v[i] != 0.0f ? v[i] / s : 0.0f), -127.0f), 127.0f);
       b[i] = static_cast<uint32_t>(static_cast<int32_t>(r));
     }
   }

@@ -7,7 +7,8 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_rows import check_lora, lora_case, w4  # noqa: E402, F401
+from test_gpu_rows import (check_lora, check_moe, codes, gen, lora_case, moe_case, moe_ref, pack, randn,  # noqa: E402
+                           w4)  # noqa: F401
 
 # between bfloat16's largest value and float32's: rounded to bfloat16 it would be an infinity
 TOP = 3.4e38
@@ -60,3 +61,38 @@ def test_lora_in_a_workspace_of_more_rows_and_in_the_least(w4, M):  # noqa: F811
     guard = buf.clone()
     assert torch.equal(w4.lora_linear(x, W, ad, ids, workspace=buf[4096: 4096 + need]), y0)
     assert torch.equal(buf[:4096], guard[:4096]) and torch.equal(buf[4096 + need:], guard[4096 + need:])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("top", [1e-30, 5e-37, 3.6e-37, 1e-37, 1e-38])
+@pytest.mark.parametrize("M,K", [(1, 256), (4, 3584), (40, 1152), (3, 40960)])
+def test_codes_of_tiny_rows(w4, M, K, top, dtype):  # noqa: F811
+    """Rows so small that 1 / (absmax / 127) overflows float32 have the codes of the rule all the same."""
+    g = gen(M + K)
+    x = (randn(g, M, K).double() * (top / 8)).clamp(-top, top).to(dtype)
+    x[:, 7], x[:, 9] = 0.0, top
+    qa, sa = w4.quant_act(x)
+    c, s = codes(x)
+    assert torch.equal(sa.double(), s)
+    assert torch.equal(qa.double(), c)
+
+
+@pytest.mark.parametrize("M,k,E", [(1, 4, 6), (40, 2, 8), (60, 4, 3), (3000, 3, 3)])
+def test_moe_of_tiny_intermediate_rows(w4, M, k, E):  # noqa: F811
+    """silu(gate) * up of about 1e-37, brought back to the normal range by the down weight."""
+    k = min(k, E)
+    x, up, down, ids, wt = moe_case(M, M, k, E, 640, 1280, torch.bfloat16)
+    up, down = (up[0], up[1], up[2] * 2.0 ** -63), (down[0], down[1], down[2] * 2.0 ** 40)
+    y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
+    ref, slack = moe_ref(x, up, down, ids, wt, E)
+    assert 0 < float(ref.abs().max()) < 1e-20
+    check_moe(y.double() * 2.0 ** 80, ref * 2.0 ** 80, slack * 2.0 ** 80)
+
+
+@pytest.mark.parametrize("M", [1, 8, 40, 300])
+def test_lora_of_tiny_rows(w4, M):  # noqa: F811
+    """The shared product of such rows, beside which the adapters' is nothing."""
+    x, w, A, B, sc, ids = lora_case(M, M, 1152, 528, 3, 16, torch.float32)
+    x = x * 2.0 ** -130
+    w = (w[0], w[1], w[2] * 2.0 ** 40)
+    check_lora(w4.lora_linear(x, w4.pack_weights(*w), w4.LoraAdapters(A, B, sc), ids), x, w, A, B, sc, ids)
