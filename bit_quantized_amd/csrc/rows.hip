@@ -653,9 +653,7 @@ __device__ __forceinline__ void row_tile(const RowsArgs& a, const Where& w, int 
   uint32_t sz[2];
   float ss;
   auto dma = [&](uint8_t* buf, int g) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_to_lds(rqa, buf + (4 * wave + i) * 1024, oa[i], g * kGroup);
+    load4_to_lds(rqa, buf + 4 * wave * 1024, oa, g * kGroup);
   };
   auto fetch = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
