@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) place_kernel(GroupArgs g) {
 //
 // One wavefront per pair, its row of at most 64 * 8 * kRowHeld values in
 // registers (w4a8_quant_act's rule); slots of experts held elsewhere are
-// skipped.  24576 rows of 1280: 20 us, against 36 with a workgroup per row.
+// skipped.  24576 rows of 1280: 18 us, against 36 with a workgroup per row.
 constexpr int kRowHeld = 4;
 __global__ void __launch_bounds__(kThreads)
 quant_pairs_kernel(const uint16_t* __restrict__ h, const int* __restrict__ ids, int64_t P, int E, int I,
@@ -356,7 +356,7 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // 64 and 256 past that the one that takes less time by what they measured a
 // group of inputs: a round of 256-row tiles 3.0 us, 64-row ones 1.3 us where
 // they lie one to a compute unit and that much more for every further one
-// (768 tokens, 5 experts, 3200 -> 2 x 256: 66 us against 92 on 256 rows;
+// (768 tokens of 4, 5 experts, 3200 -> 2 x 256: 65 us against 92 on 256 rows;
 // 4096 tokens, 64 experts, 3584 -> 2 x 1280 stay on 256).
 static int tile_rows(int64_t P, int E, int64_t I, int64_t K) {
   const double share = (double)P / E;
@@ -422,7 +422,7 @@ MoePlan moe_plan(int64_t M, int k, int E, int64_t I, int64_t K) {
 
 // Runs of about 24 units per wavefront, but columns shared out while the
 // tiles that can be expected leave compute units without a workgroup (644
-// tokens of 7, 15 experts, 128 -> 384: 35 us against 61).
+// tokens of 7, 15 experts, 128 -> 384: 36 us against 61).
 int down_columns(const MoePlan& p, int64_t P, int E, int64_t I, int64_t K) {
   const int64_t GI = I / kGroup, cols = K / 16;
   const int64_t tiles = P / p.bm + (E < P ? E : P) / 2 + 1;

@@ -185,7 +185,8 @@ __device__ __forceinline__ void wait_flag(uint32_t* s_sync) {
 // ADAPT: y also gets the token's adapter product (GemmArgs::ad).  The scaled
 // x A^T is summed by the last wavefront while it would wait for the flag, the
 // product with B taken in the epilogue (M = 1, K = 3584 -> N = 18944, rank
-// 16: 9.0 us against 8.0 without it, and 13.8 on the row-tile kernel).
+// 16: 9.0 us against 8.1 without it, 9.5 where neither A, B nor the weight was
+// read just before; 13.8 on the row-tile kernel).
 template <int XT, bool DEBUG, bool KSPLIT, int kQChunks, bool W8 = false, bool HAD = false,
           bool EARLY = false, int DR = D, bool ADAPT = false>
 __global__ void __launch_bounds__(kThreads)

@@ -6,7 +6,7 @@
 // the reduction that adds the second half where the shared product was split
 // over K.  Past 64 rows everything takes the rows in the order of their
 // adapters, so that 16 neighbours share one or two of them: 1024 rows of 16
-// adapters of rank 128, mixed, 3584 -> 18944: 221 us, against 1005 in the
+// adapters of rank 128, mixed, 3584 -> 18944: 194 us, against 1005 in the
 // order of the call.
 #include "lora.h"
 
@@ -87,7 +87,7 @@ constexpr int down_steps(int R) { return R > 64 ? 2 : 4; }
 // memory traffic, which is what bounds this step.  bf16 activations are exact
 // operands; float ones go in as two bf16 parts (16 significant bits, below
 // the bf16 weights' own 8).  33 rows with 20 adapters of rank 64, 18944
-// inputs: 16.5 us for 67 MB.
+// inputs: 17.6 us for 67 MB.
 template <int ACT, int RT>
 __global__ void __launch_bounds__(kThreads)
 adapter_down_kernel(LoraArgs a, int8_t* __restrict__ qa, float* __restrict__ sa,
@@ -268,7 +268,7 @@ adapter_parts_kernel(AdaptArgs ad, int64_t M, uint16_t* __restrict__ hi, uint16_
 // c: rows 4 j .. + 3, channel c).  Per adapter among the rows the product of
 // its rows' two parts with B is added to those rows only, so an adapter's B
 // is read once per 16 rows (200 rows of rank 32, three slices of 18944
-// channels: 13.5 us, 60 MB).
+// channels: 14.6 us, 60 MB).
 __global__ void __launch_bounds__(256)
 adapt_reduce_sorted_kernel(const float* __restrict__ parts, int ksplit, const float* __restrict__ sa,
                            const int* __restrict__ order, int64_t M, int N, AdaptArgs ad,
@@ -409,7 +409,8 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int L, int R) {
   }
   const int64_t frags = (mc + 15) / 16;
   // (few rows: sorted where reading B once per row would cost more than the
-  // two small launches; 64 rows of rank 64, 3584 -> 18944: 54 us against 65)
+  // two small launches; 64 rows of rank 64, 3584 -> 18944: 52 us against 63
+  // with 16 adapters, but 83 against 74 with 64)
   p.sorted = mc > 64 || (mc > 16 && mc * N * R * 2 > kSortBytes);
   p.slots = (int)(p.sorted ? 1 : mc < 16 ? mc : 16);  // (sorted: few adapters to a fragment)
   if (p.slots > L) p.slots = L;
