@@ -96,3 +96,48 @@ def test_lora_of_tiny_rows(w4, M):  # noqa: F811
     x = x * 2.0 ** -130
     w = (w[0], w[1], w[2] * 2.0 ** 40)
     check_lora(w4.lora_linear(x, w4.pack_weights(*w), w4.LoraAdapters(A, B, sc), ids), x, w, A, B, sc, ids)
+
+
+@pytest.mark.parametrize("M,K,N,L,R", [((1 << 20) + 300, 128, 32, 3, 8), (113152 + 300, 18944, 32, 4, 16)])
+def test_lora_passes(w4, M, K, N, L, R):  # noqa: F811
+    """More rows than one pass takes, by their number and by the 2^31 bytes of
+    their codes: rows before, at and after the border against the definition."""
+    p = w4.lora_linear_plan(M, N, K, L, R)
+    assert p.rows == M - 300
+    g = gen(M)
+    block = randn(g, 4099, K)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, M, 4099):
+        x[lo: lo + 4099] = block[: min(4099, M - lo)]
+    _, w, A, B, sc, _ = lora_case(7, 1, K, N, L, R, torch.bfloat16)
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    y = w4.lora_linear(x, w4.pack_weights(*w), w4.LoraAdapters(A, B, sc), ids)
+    for lo in (0, M - 400, M - 200):
+        r = slice(lo, lo + 200)
+        check_lora(y[r], x[r], w, A, B, sc, ids[r])
+
+
+def test_moe_passes_by_bytes(w4):  # noqa: F811
+    """A pass ends where a token's codes would pass 2^31 bytes."""
+    k, E, I, K = 1, 4, 128, 18944
+    M = (2 ** 31 - 1) // K + 150
+    assert w4.moe_mlp_plan(M, k, E, I, K).tokens == M - 150
+    x, up, down, _, _ = moe_case(5, 2, k, E, I, K, torch.bfloat16)
+    g = gen(6)
+    block = randn(g, 4099, K)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, M, 4099):
+        x[lo: lo + 4099] = block[: min(4099, M - lo)]
+    ids = torch.randint(-1, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    wt = torch.rand(M, k, generator=g, device="cuda")
+    y = w4.moe_mlp(x, *pack(w4, up, down, E), ids, wt)
+    for lo in (0, M - 250, M - 100):
+        r = slice(lo, lo + 100)
+        check_moe(y[r], *moe_ref(x[r], up, down, ids[r], wt[r], E))
+
+
+@pytest.mark.parametrize("M", [1, 20, 70])
+def test_moe_most_experts_and_slots(w4, M):  # noqa: F811
+    x, up, down, ids, wt = moe_case(M, M, 64, 1024, 128, 128, torch.float32, drop=0.1)
+    y = w4.moe_mlp(x, *pack(w4, up, down, 1024), ids, wt)
+    check_moe(y, *moe_ref(x, up, down, ids, wt, 1024))
