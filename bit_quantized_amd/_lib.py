@@ -1,4 +1,5 @@
-"""ctypes binding of libw4a8.so (include/w4a8.h, include/w4a8_rows.h).
+"""ctypes binding of libw4a8.so (include/w4a8.h, include/w4a8_rows.h,
+include/w4a8_mx.h).
 
 Argument marshalling only: torch supplies device memory and the current
 stream; every step of the layer runs in the library's HIP kernels.  If the
@@ -56,6 +57,20 @@ class LoraLinearPlan(ctypes.Structure):
     _fields_ = [("rows", _i64), ("path", _i32), ("ksplit", _i32), ("in_epilogue", _i32), ("sorted", _i32)]
 
 
+# Microscaled products (w4a8_mx.h): formats, scale rules and kernels.
+MX_FORMATS = {"fp4": 0, "fp8": 1}
+MX_RULES = {"floor": 0, "ceil": 1}
+MX_BLOCK = 32
+MX_TOKEN = 1
+MX_STREAM = 2
+MX_TILE = 3
+
+
+class MxPlan(ctypes.Structure):
+    """How a microscaled product of these sizes runs (w4a8_mx_plan_t)."""
+    _fields_ = [("path", _i32), ("tile_rows", _i32), ("tile_cols", _i32), ("ksplit", _i32)]
+
+
 # Every symbol the headers declare, with its ctypes signature.
 SIGNATURES = {
     "w4a8_abi_version": (ctypes.c_int, []),
@@ -108,6 +123,21 @@ SIGNATURES = {
     "w4a8_lora_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "w4a8_lora_linear": (ctypes.c_int, [_vp, _i32, _vp, _sz, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                                         _i32, _i32, _vp, _vp, _sz, _vp]),
+    # include/w4a8_mx.h
+    "w4a8_mx_quant": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "w4a8_mx_dequant": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp]),
+    "w4a8_mx_weight_bytes": (_sz, [_i64, _i64]),
+    "w4a8_mx_pack_weights": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "w4a8_mx_unpack_weights": (ctypes.c_int, [_vp, _sz, _i64, _i64, _vp, _vp, _vp]),
+    "w4a8_mx_linear_plan": (ctypes.c_int, [_i64, _i64, _i64, _i32, ctypes.POINTER(MxPlan)]),
+    "w4a8_mx_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "w4a8_mx_linear": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _sz, _i64, _i64, _i64, _vp, _vp, _sz,
+                                      _vp]),
+    "w4a8_mx_grouped_linear_plan": (ctypes.c_int, [_i64, _i64, _i32, _i64, _i64, _i32,
+                                                   ctypes.POINTER(MxPlan)]),
+    "w4a8_mx_grouped_linear_workspace_bytes": (_sz, [_i64, _i64, _i32, _i64, _i64, _i32]),
+    "w4a8_mx_grouped_linear": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _sz, _vp, _vp, _i64, _i64, _i32,
+                                              _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     # include/w4a8_peaks.h
     "w4a8_peak_stream_read": (ctypes.c_int, [_vp, _sz, _vp, _i32, _vp]),
     "w4a8_peak_mfma_i8": (ctypes.c_int, [_i32, _vp, _vp, _i32, _vp]),
@@ -751,6 +781,208 @@ def lora_linear(x: torch.Tensor, w: PackedWeight, adapters: LoraAdapters, ids: t
     _check(lib.w4a8_lora_linear(_p(x), dt, _p(w.buf), w.buf.numel(), _p(adapters.A), _p(adapters.B),
                                 _p(adapters.scale), _p(ids), M, w.N, K, L, R, _p(out), _p(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(x.device)))
+    return out
+
+
+# ------------------------------------------- microscaled floating point
+
+def _mx(table, name: str, what: str) -> int:
+    if name not in table:
+        raise ValueError(f"unknown {what} {name!r}")
+    return table[name]
+
+
+@dataclass
+class MxTensor:
+    """Rows in a microscaled format: codes uint8 [M][K / 2] ("fp4", the even
+    value in the low bits) or [M][K] ("fp8"), scales uint8 [M][K / 32] (2^(b -
+    127), 255 is NaN)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    format: str
+
+    @property
+    def shape(self):
+        M, per = self.scales.shape
+        return M, per * MX_BLOCK
+
+    def check(self):
+        _mx(MX_FORMATS, self.format, "element format")
+        if self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
+            raise TypeError("codes and scales must be uint8")
+        M, K = self.shape
+        if tuple(self.codes.shape) != (M, K // 2 if self.format == "fp4" else K):
+            raise ValueError(f"codes {tuple(self.codes.shape)} and scales {tuple(self.scales.shape)} do "
+                             f"not fit together")
+
+
+def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
+             codes: torch.Tensor | None = None, scales: torch.Tensor | None = None) -> MxTensor:
+    """x bfloat16 or float32 [M][K] -> MxTensor: blocks of 32 values share a
+    power of two.  rule "floor": the largest value falls into the format's
+    last binade and may be clipped; "ceil": nothing is clipped."""
+    lib = load()
+    fmt, ru = _mx(MX_FORMATS, format, "element format"), _mx(MX_RULES, rule, "scale rule")
+    _need_on(x.get_device(), x, codes, scales)
+    M, K = x.shape
+    dt = _act_dtype(x)
+    width = K // 2 if fmt == 0 else K
+    if codes is None:
+        codes = x.new_empty((M, width), dtype=torch.uint8)
+    elif codes.dtype != torch.uint8 or codes.shape != (M, width):
+        raise TypeError(f"codes must be uint8 [{M}][{width}]")
+    if scales is None:
+        scales = x.new_empty((M, K // MX_BLOCK), dtype=torch.uint8)
+    elif scales.dtype != torch.uint8 or scales.shape != (M, K // MX_BLOCK):
+        raise TypeError(f"scales must be uint8 [{M}][{K // MX_BLOCK}]")
+    _check(lib.w4a8_mx_quant(_p(x), dt, M, K, fmt, ru, _p(codes), _p(scales), _stream(x.device)))
+    return MxTensor(codes, scales, format)
+
+
+def mx_dequant(t: MxTensor, dtype: torch.dtype = torch.bfloat16,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that codes and scales stand for, bfloat16 or float32 [M][K]."""
+    lib = load()
+    t.check()
+    _need_on(t.codes.get_device(), t.codes, t.scales, out)
+    M, K = t.shape
+    if out is None:
+        out = t.codes.new_empty((M, K), dtype=dtype)
+    elif out.dtype != dtype or out.shape != (M, K):
+        raise TypeError(f"out must be {dtype} [{M}][{K}]")
+    _check(lib.w4a8_mx_dequant(_p(t.codes), _p(t.scales), MX_FORMATS[t.format], M, K, _p(out),
+                               _act_dtype(out), _stream(out.device)))
+    return out
+
+
+@dataclass
+class MxWeight:
+    """A packed 4-bit microscaled weight: n_experts weights of N channels and
+    K inputs, stacked along the channels."""
+    buf: torch.Tensor          # uint8, mx_weight_bytes(n_experts * N, K)
+    n_experts: int
+    N: int
+    K: int
+
+
+def mx_weight_bytes(N: int, K: int) -> int:
+    return int(load().w4a8_mx_weight_bytes(N, K))
+
+
+def mx_pack_weights(codes: torch.Tensor, scales: torch.Tensor, n_experts: int = 1,
+                    out: torch.Tensor | None = None) -> MxWeight:
+    """codes uint8 [n_experts * N][K / 2] and scales uint8 [n_experts * N][K /
+    32], as mx_quant(w, "fp4") and checkpoints hold them -> packed weight."""
+    lib = load()
+    MxTensor(codes, scales, "fp4").check()
+    _need_on(codes.get_device(), codes, scales, out)
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    if n_experts < 1 or rows % n_experts:
+        raise ValueError(f"{rows} channels are not those of {n_experts} experts")
+    nbytes = lib.w4a8_mx_weight_bytes(rows, K)
+    if nbytes == 0:
+        _check(lib.w4a8_mx_pack_weights(None, None, rows, K, None, 0, None))
+    if out is None:
+        out = codes.new_empty(nbytes)
+    _check(lib.w4a8_mx_pack_weights(_p(codes), _p(scales), rows, K, _p(out),
+                                    out.numel() * out.element_size(), _stream(codes.device)))
+    return MxWeight(out, n_experts, rows // n_experts, K)
+
+
+def mx_unpack_weights(w: MxWeight) -> MxTensor:
+    """The inverse of mx_pack_weights."""
+    lib = load()
+    _need_on(w.buf.get_device(), w.buf)
+    rows = w.n_experts * w.N
+    codes = w.buf.new_empty((rows, w.K // 2), dtype=torch.uint8)
+    scales = w.buf.new_empty((rows, w.K // MX_BLOCK), dtype=torch.uint8)
+    _check(lib.w4a8_mx_unpack_weights(_p(w.buf), w.buf.numel() * w.buf.element_size(), rows, w.K, _p(codes),
+                                      _p(scales), _stream(w.buf.device)))
+    return MxTensor(codes, scales, "fp4")
+
+
+def mx_linear_plan(M: int, N: int, K: int, act: str = "fp4") -> MxPlan:
+    plan = MxPlan()
+    _check(load().w4a8_mx_linear_plan(M, N, K, _mx(MX_FORMATS, act, "element format"), ctypes.byref(plan)))
+    return plan
+
+
+def mx_linear_workspace_bytes(M: int, N: int, K: int, act: str = "fp4") -> int:
+    """Bytes of a workspace for M rows or any smaller number of them."""
+    return int(load().w4a8_mx_linear_workspace_bytes(M, N, K, _mx(MX_FORMATS, act, "element format")))
+
+
+def mx_linear(x: torch.Tensor, w: MxWeight, act: str = "fp4", rule: str = "floor",
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 y [M][N]: rows of x (bf16/f32 [M][K]) quantised to `act` times a
+    4-bit microscaled weight."""
+    lib = load()
+    fmt, ru = _mx(MX_FORMATS, act, "element format"), _mx(MX_RULES, rule, "scale rule")
+    _need_on(x.get_device(), x, w.buf, out, workspace)
+    M, K = x.shape
+    dt = _act_dtype(x)
+    N = w.n_experts * w.N
+    if K != w.K:
+        raise ValueError(f"activations have K={K}, weight has K={w.K}")
+    out = _out(out, x, M, N)
+    if workspace is None:
+        workspace = x.new_empty(max(mx_linear_workspace_bytes(M, N, K, act), 16), dtype=torch.uint8)
+    _check(lib.w4a8_mx_linear(_p(x), dt, fmt, ru, _p(w.buf), w.buf.numel() * w.buf.element_size(), M, N, K,
+                              _p(out), _p(workspace), workspace.numel() * workspace.element_size(),
+                              _stream(x.device)))
+    return out
+
+
+def mx_grouped_linear_plan(M: int, P: int, n_experts: int, N: int, K: int, act: str = "fp4") -> MxPlan:
+    plan = MxPlan()
+    _check(load().w4a8_mx_grouped_linear_plan(M, P, n_experts, N, K,
+                                              _mx(MX_FORMATS, act, "element format"), ctypes.byref(plan)))
+    return plan
+
+
+def mx_grouped_linear_workspace_bytes(M: int, P: int, n_experts: int, N: int, K: int,
+                                      act: str = "fp4") -> int:
+    """Bytes of a workspace for M rows of x and P product rows or any smaller
+    numbers of them."""
+    return int(load().w4a8_mx_grouped_linear_workspace_bytes(M, P, n_experts, N, K,
+                                                             _mx(MX_FORMATS, act, "element format")))
+
+
+def mx_grouped_linear(x: torch.Tensor, w: MxWeight, offsets: torch.Tensor,
+                      rows: torch.Tensor | None = None, gated: bool = False, act: str = "fp4",
+                      rule: str = "floor", out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Ragged products by expert: product rows [offsets[e], offsets[e + 1])
+    (int32 [n_experts + 1], on the device) are rows of x (row p itself, or
+    x[rows[p]] with rows int32 [P]; an index outside x gives zeros) times
+    expert e's weight, bf16 [P][N]; gated: the first N / 2 channels are gates,
+    the others values, and y = silu(gate) * value, [P][N / 2].  Product rows
+    outside [offsets[0], offsets[-1]) stay as they were."""
+    lib = load()
+    fmt, ru = _mx(MX_FORMATS, act, "element format"), _mx(MX_RULES, rule, "scale rule")
+    _need_on(x.get_device(), x, w.buf, offsets, rows, out, workspace)
+    M, K = x.shape
+    dt = _act_dtype(x)
+    E, N = w.n_experts, w.N
+    if K != w.K:
+        raise ValueError(f"activations have K={K}, weight has K={w.K}")
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,):
+        raise TypeError(f"offsets must be int32 [{E + 1}]")
+    P = M
+    if rows is not None:
+        if rows.dtype != torch.int32 or rows.dim() != 1:
+            raise TypeError("rows must be int32 [P]")
+        P = rows.shape[0]
+    if gated and N % 2:
+        raise ValueError(f"{N} channels are not gates and values")
+    out = _out(out, x, P, N // 2 if gated else N)
+    if workspace is None:
+        workspace = x.new_empty(max(mx_grouped_linear_workspace_bytes(M, P, E, N, K, act), 16),
+                                dtype=torch.uint8)
+    _check(lib.w4a8_mx_grouped_linear(_p(x), dt, fmt, ru, _p(w.buf),
+                                      w.buf.numel() * w.buf.element_size(), _p(offsets), _p(rows), M, P, E,
+                                      N, K, int(gated), _p(out), _p(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(x.device)))
     return out
 
 

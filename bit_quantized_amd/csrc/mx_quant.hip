@@ -1,0 +1,321 @@
+// Rows to microscaled codes and scales and back, and the weight layout of the
+// products.  All of it streams: bound by memory.
+#include "mx.h"
+
+#include <type_traits>
+
+namespace w4a8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Chunk t (eight values) of a matrix of `per` chunks a row; four neighbouring
+// lanes hold one block, so its largest magnitude takes two quad permutations.
+// 16 bytes a lane in (bfloat16), 4 or 8 out.
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(kThreads)
+quant_kernel(const uint8_t* __restrict__ x, int64_t total, int rule, uint8_t* __restrict__ codes,
+             uint8_t* __restrict__ scales) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= total) return;  // total % 4 == 0: whole blocks leave together
+  MxRaw<F32> r;
+  r.load(x, t * 8);
+  const int b = mx_scale_byte<FMT>(dpp_umax_quad(r.top()), rule);
+  const uint2 c = mx_codes8<FMT, F32>(r, b);
+  if constexpr (FMT == kFp4)
+    reinterpret_cast<uint32_t*>(codes)[t] = c.x;
+  else
+    reinterpret_cast<uint2*>(codes)[t] = c;
+  if ((t & 3) == 0) scales[t >> 2] = (uint8_t)b;
+}
+
+// Eight values a lane out: 16 or 32 bytes.
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(kThreads)
+dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total,
+               uint8_t* __restrict__ y) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= total) return;
+  const int b = scales[t >> 2];
+  const float s = mx_scale_float(b);
+  uint32_t c[2] = {0u, 0u};
+  if constexpr (FMT == kFp4) {
+    c[0] = reinterpret_cast<const uint32_t*>(codes)[t];
+  } else {
+    const uint2 v = reinterpret_cast<const uint2*>(codes)[t];
+    c[0] = v.x;
+    c[1] = v.y;
+  }
+  v2f_mx v[4];
+  if constexpr (FMT == kFp4) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], s, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], s, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], s, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], s, 3);
+  } else {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[0], s, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[0], s, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[1], s, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[1], s, true);
+  }
+  if (b == 255) {
+    const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = v2f_mx{nan, nan};
+  }
+  if constexpr (F32) {
+    float4* out = reinterpret_cast<float4*>(y) + 2 * t;
+    out[0] = float4{v[0][0], v[0][1], v[1][0], v[1][1]};
+    out[1] = float4{v[2][0], v[2][1], v[3][0], v[3][1]};
+  } else {
+    const uint2 lo = mx_bf16x4(v4f_mx{v[0][0], v[0][1], v[1][0], v[1][1]});
+    const uint2 hi = mx_bf16x4(v4f_mx{v[2][0], v[2][1], v[3][0], v[3][1]});
+    reinterpret_cast<uint4*>(y)[t] = uint4{lo.x, lo.y, hi.x, hi.y};
+  }
+}
+
+// ------------------------------------------------- rows for the products
+
+struct GroupTiles {
+  const int* offsets;
+  int E, bm, slots;
+  int64_t P;
+  int* ntiles;
+  MxTile* tiles;
+};
+
+// The tiles of every group, by one workgroup: prefix sums of the groups' tile
+// counts (four groups a thread), then a thread a tile.
+__device__ __forceinline__ void list_tiles(const GroupTiles& g, int (&s_head)[kMxMaxGroups + 1], int* s_wave) {
+  constexpr int kPer = kMxMaxGroups / kThreads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int n[kPer], own = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    n[i] = 0;
+    if (e < g.E) {
+      int lo, hi;
+      mx_run(g.offsets, e, g.P, lo, hi);
+      n[i] = (hi - lo + g.bm - 1) / g.bm;
+    }
+    own += n[i];
+  }
+  int sum = own;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  if (lane == 63) s_wave[wave] = sum;
+  __syncthreads();
+  int base = sum - own;
+  for (int w = 0; w < wave; ++w) base += s_wave[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (tid * kPer + i <= g.E) s_head[tid * kPer + i] = base;
+    base += n[i];
+  }
+  if (tid == kThreads - 1 && g.E == kMxMaxGroups) s_head[kMxMaxGroups] = base;
+  __syncthreads();
+  // (offsets that do not ascend can name more tiles than there are slots)
+  const int total = min(s_head[g.E], g.slots);
+  if (tid == 0) g.ntiles[0] = total;
+  for (int t = tid; t < total; t += kThreads) {
+    int a = 0, b = g.E;  // the last group whose first tile is at most t
+    while (b - a > 1) {
+      const int m = (a + b) / 2;
+      if (s_head[m] <= t) a = m; else b = m;
+    }
+    int lo, hi;
+    mx_run(g.offsets, a, g.P, lo, hi);
+    const int at = t - s_head[a], first = lo + at * g.bm;
+    g.tiles[t] = MxTile{a, first, min(g.bm, hi - first), s_head[a], s_head[a + 1] - s_head[a], {0, 0, 0}};
+  }
+}
+
+// Workgroup (i, m): chunks of row m, past K the zeros that the layout asks
+// for.  The first workgroup lists the tiles as well.
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(kThreads)
+rows_kernel(const uint8_t* __restrict__ x, int K, int rule, int ldx, int lds, uint8_t* __restrict__ codes,
+            uint8_t* __restrict__ scales, int wide, GroupTiles g) {
+  __shared__ int s_head[kMxMaxGroups + 1], s_wave[kThreads / 64];
+  unsigned item = blockIdx.x;
+  if (g.offsets) {
+    if (item == 0) {
+      list_tiles(g, s_head, s_wave);
+      return;
+    }
+    --item;
+  }
+  const int64_t m = item / (unsigned)wide;
+  const int ch = (int)(item % (unsigned)wide) * kThreads + threadIdx.x;
+  if (ch >= lds * 4) return;  // lds * 4 chunks of a row: whole supers of 512 inputs
+  MxRaw<F32> r;
+  r.clear();
+  if (ch * 8 < K) r.load(x + m * K * (F32 ? 4 : 2), ch * 8);
+  const uint32_t top = dpp_umax_quad(r.top());
+  const int b = mx_scale_byte<FMT>(top, rule);
+  const uint2 c = mx_codes8<FMT, F32>(r, b);
+  const int at = ch * (FMT == kFp4 ? 4 : 8);
+  if (at < ldx) {
+    if constexpr (FMT == kFp4)
+      *reinterpret_cast<uint32_t*>(codes + m * ldx + at) = c.x;
+    else
+      *reinterpret_cast<uint2*>(codes + m * ldx + at) = c;
+  }
+  if ((ch & 3) == 0) {  // block 16 q + 4 s + j at byte 16 q + 4 j + s
+    const int blk = ch >> 2;
+    scales[m * lds + (blk & ~15) + 4 * (blk & 3) + ((blk >> 2) & 3)] = (uint8_t)b;
+  }
+}
+
+// ------------------------------------------------------------ weight layout
+
+// Thread: 16 bytes of a codes block (lane L of block (nb, g)).
+__global__ void __launch_bounds__(kThreads)
+pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t units, int K, int G, uint8_t* __restrict__ packed) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= units) return;
+  const int L = (int)(t & 63), j = L >> 4, c = L & 15;
+  const int64_t blk = t >> 6, nb = blk / G;
+  const int g = (int)(blk % G), k = g * kMxStep + j * kMxBlock;
+  v4u_rows v = {0, 0, 0, 0};
+  if (k < K) v = *reinterpret_cast<const v4u_rows*>(codes + ((nb * 16 + c) * K + k) / 2);
+  reinterpret_cast<v4u_rows*>(packed)[t] = v;
+}
+// Thread: the four scale bytes of lane L of super (nb, q); the last 256
+// threads clear the 1024 bytes behind the planes.
+__global__ void __launch_bounds__(kThreads)
+pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t units, int K, int Q, uint8_t* __restrict__ plane) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= units + 256) return;
+  uint32_t v = 0;
+  if (t < units) {
+    const int L = (int)(t & 63), j = L >> 4, c = L & 15;
+    const int64_t sup = t >> 6, nb = sup / Q;
+    const int q = (int)(sup % Q), per = K / kMxBlock;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int b = (4 * q + s) * 4 + j;
+      if (b < per) v |= (uint32_t)scales[(nb * 16 + c) * per + b] << (8 * s);
+    }
+  }
+  reinterpret_cast<uint32_t*>(plane)[t] = v;
+}
+__global__ void __launch_bounds__(kThreads)
+unpack_codes_kernel(const uint8_t* __restrict__ packed, int64_t units, int K, int G, uint8_t* __restrict__ codes) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= units) return;
+  const int L = (int)(t & 63), j = L >> 4, c = L & 15;
+  const int64_t blk = t >> 6, nb = blk / G;
+  const int k = (int)(blk % G) * kMxStep + j * kMxBlock;
+  if (k < K)
+    *reinterpret_cast<v4u_rows*>(codes + ((nb * 16 + c) * K + k) / 2) = reinterpret_cast<const v4u_rows*>(packed)[t];
+}
+__global__ void __launch_bounds__(kThreads)
+unpack_scales_kernel(const uint8_t* __restrict__ plane, int64_t units, int K, int Q, uint8_t* __restrict__ scales) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= units) return;
+  const int L = (int)(t & 63), j = L >> 4, c = L & 15;
+  const int64_t sup = t >> 6, nb = sup / Q;
+  const int q = (int)(sup % Q), per = K / kMxBlock;
+  const uint32_t v = reinterpret_cast<const uint32_t*>(plane)[t];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int b = (4 * q + s) * 4 + j;
+    if (b < per) scales[(nb * 16 + c) * per + b] = (uint8_t)(v >> (8 * s));
+  }
+}
+
+unsigned blocks_of(int64_t items) { return (unsigned)((items + kThreads - 1) / kThreads); }
+
+// f(format, float) as template arguments.
+template <typename F>
+void typed(int fmt, int f32, F&& f) {
+  using std::integral_constant;
+  if (fmt == kFp4) {
+    if (f32) f(integral_constant<int, kFp4>{}, integral_constant<bool, true>{});
+    else f(integral_constant<int, kFp4>{}, integral_constant<bool, false>{});
+  } else {
+    if (f32) f(integral_constant<int, kFp8>{}, integral_constant<bool, true>{});
+    else f(integral_constant<int, kFp8>{}, integral_constant<bool, false>{});
+  }
+}
+
+// Chunks of one launch: the grid stays below 2^31 / 256 workgroups.
+constexpr int64_t kMostChunks = (int64_t)1 << 30;
+
+}  // namespace
+
+hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t st) {
+  const int64_t total = a.M * a.K / 8;
+  for (int64_t t = 0; t < total; t += kMostChunks) {
+    const int64_t n = total - t < kMostChunks ? total - t : kMostChunks;
+    typed(a.fmt, a.f32, [&](auto fmt, auto f32) {
+      hipLaunchKernelGGL((quant_kernel<decltype(fmt)::value, decltype(f32)::value>), dim3(blocks_of(n)),
+                         dim3(kThreads), 0, st,
+                         static_cast<const uint8_t*>(a.x) + t * 8 * (a.f32 ? 4 : 2), n, a.rule,
+                         a.codes + t * (a.fmt == kFp4 ? 4 : 8), a.scales + t / 4);
+    });
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t M, int64_t K,
+                             void* y, int f32, hipStream_t st) {
+  const int64_t total = M * K / 8;
+  for (int64_t t = 0; t < total; t += kMostChunks) {
+    const int64_t n = total - t < kMostChunks ? total - t : kMostChunks;
+    typed(fmt, f32, [&](auto fm, auto fl) {
+      hipLaunchKernelGGL((dequant_kernel<decltype(fm)::value, decltype(fl)::value>), dim3(blocks_of(n)),
+                         dim3(kThreads), 0, st, codes + t * (fmt == kFp4 ? 4 : 8), scales + t / 4, n,
+                         static_cast<uint8_t*>(y) + t * 8 * (f32 ? 4 : 2));
+    });
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_rows(const MxQuantArgs& a, const int* offsets, int E, int64_t P, int bm, int* ntiles,
+                          MxTile* tiles, hipStream_t st) {
+  const int ldx = (int)mx_row_bytes(a.K, a.fmt), lds = (int)mx_row_scale_bytes(a.K);
+  const int wide = (lds * 4 + kThreads - 1) / kThreads;
+  const GroupTiles list{offsets, E, bm, offsets ? (int)mx_tile_slots(P, E, bm) : 0, P, ntiles, tiles};
+  constexpr int64_t kMostItems = (int64_t)1 << 23;  // workgroups of one launch
+  const int64_t pass = kMostItems / wide;
+  for (int64_t m = 0; m < a.M; m += pass) {
+    const int64_t n = a.M - m < pass ? a.M - m : pass;
+    GroupTiles g = list;
+    if (m) g.offsets = nullptr;  // listed by the first launch
+    typed(a.fmt, a.f32, [&](auto fmt, auto f32) {
+      hipLaunchKernelGGL((rows_kernel<decltype(fmt)::value, decltype(f32)::value>),
+                         dim3((unsigned)(n * wide + (g.offsets ? 1 : 0))), dim3(kThreads), 0, st,
+                         static_cast<const uint8_t*>(a.x) + m * a.K * (a.f32 ? 4 : 2), (int)a.K, a.rule, ldx, lds,
+                         a.codes + m * ldx, a.scales + m * lds, wide, g);
+    });
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K, uint8_t* packed,
+                          hipStream_t st) {
+  const int G = (int)mx_steps(K), Q = (int)mx_supers(K);
+  const int64_t uc = N / 16 * G * 64, us = N / 16 * Q * 64;
+  hipLaunchKernelGGL(pack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, codes, uc, (int)K, G, packed);
+  hipLaunchKernelGGL(pack_scales_kernel, dim3(blocks_of(us + 256)), dim3(kThreads), 0, st, scales, us, (int)K, Q,
+                     packed + mx_scales_offset(N, K));
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_unpack(const uint8_t* packed, int64_t N, int64_t K, uint8_t* codes, uint8_t* scales,
+                            hipStream_t st) {
+  const int G = (int)mx_steps(K), Q = (int)mx_supers(K);
+  const int64_t uc = N / 16 * G * 64, us = N / 16 * Q * 64;
+  hipLaunchKernelGGL(unpack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, packed, uc, (int)K, G, codes);
+  hipLaunchKernelGGL(unpack_scales_kernel, dim3(blocks_of(us)), dim3(kThreads), 0, st,
+                     packed + mx_scales_offset(N, K), us, (int)K, Q, scales);
+  return hipGetLastError();
+}
+
+}  // namespace w4a8

@@ -1,0 +1,156 @@
+/*
+ * w4a8_mx.h — C ABI of the products on microscaled floating point: blocks of
+ * 32 values along the inputs that share a power of two.  Weights have 4-bit
+ * elements; activations are quantised per call to 4-bit or 8-bit ones and
+ * multiplied on the block-scaled matrix cores of gfx950.  Status codes,
+ * activation dtypes, alignment, stream, ownership and determinism are as
+ * stated in w4a8.h.
+ *
+ * The formats:
+ *   W4A8_MX_FP4  e2m1: sign, 2 exponent bits, 1 mantissa bit; magnitudes
+ *                0, 0.5, 1, 1.5, 2, 3, 4, 6 in the order of the codes; no
+ *                infinity, no NaN
+ *   W4A8_MX_FP8  e4m3: bias 7, largest magnitude 448, no infinity; codes
+ *                0x7F and 0xFF are NaN
+ *   scale        one byte b per block: 2^(b - 127); b = 255 is NaN
+ * A value is its element times its block's scale.  In memory a row of K
+ * values is K / 2 bytes of 4-bit codes (the even value in the low bits) or K
+ * bytes of 8-bit ones, and K / 32 scale bytes.
+ *
+ * Quantisation of a block with largest magnitude a (bfloat16 and float
+ * inputs alike; subnormal values count as they are):
+ *   W4A8_MX_FLOOR  b = floor(log2 a) - e + 127, e = 2 (FP4) or 8 (FP8): the
+ *                  largest value falls into the format's last binade and is
+ *                  clipped where it lies above the format's largest magnitude
+ *   W4A8_MX_CEIL   the least b at which nothing is clipped
+ * and b at least 0; elements are rounded to nearest, ties to even, and keep
+ * their sign.  A block that holds an infinity or a NaN has b = 255 and codes
+ * 0: every sum that it enters is NaN.
+ */
+#ifndef W4A8_MX_H
+#define W4A8_MX_H
+
+#include "w4a8.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* element formats */
+#define W4A8_MX_FP4 0
+#define W4A8_MX_FP8 1
+/* scale rules */
+#define W4A8_MX_FLOOR 0
+#define W4A8_MX_CEIL 1
+
+/*
+ * w4a8_mx_quant — rows to codes and scales.
+ *   x       device [M][K], bfloat16 (W4A8_BF16) or float (W4A8_F32)
+ *   codes   device uint8 [M][K / 2] (FP4) or [M][K] (FP8)
+ *   scales  device uint8 [M][K / 32]
+ * w4a8_mx_dequant — codes and scales to the values they stand for.
+ *   y       device [M][K], bfloat16 or float; exact, except that a bfloat16 y
+ *           rounds FP8 values below 2^-130, and that values past the type's
+ *           largest become infinities
+ * Requirements: 1 <= M <= 2^24, K % 32 == 0, 32 <= K <= 2^22.
+ */
+int w4a8_mx_quant(const void* x, int32_t x_dtype, int64_t M, int64_t K, int32_t format, int32_t rule,
+                  uint8_t* codes, uint8_t* scales, void* stream);
+int w4a8_mx_dequant(const uint8_t* codes, const uint8_t* scales, int32_t format, int64_t M, int64_t K,
+                    void* y, int32_t y_dtype, void* stream);
+
+/*
+ * w4a8_mx_pack_weights — load-time conversion of a 4-bit weight into the
+ * layout that the products read (layout version 1).
+ *   codes   device uint8 [N][K / 2], scales device uint8 [N][K / 32]: as
+ *           w4a8_mx_quant writes them and checkpoints hold them
+ *   packed  device buffer of w4a8_mx_weight_bytes(N, K) bytes
+ * Format (G = K / 128 rounded up, NB = N / 16, Q = G / 4 rounded up):
+ *   codes,  1024 NB G bytes at offset 0: block (nb, g) at (nb G + g) 1024;
+ *     lane L = 16 j + c (j = 0..3, c = 0..15) owns bytes [16 L, 16 L + 16):
+ *     the codes of channel 16 nb + c, inputs [128 g + 32 j, 128 g + 32 j + 32);
+ *   scales, 256 NB Q bytes at 1024 NB G: block (nb, q) at (nb Q + q) 256; byte
+ *     s of lane L's 4 is the scale of channel 16 nb + c, inputs
+ *     [128 (4 q + s) + 32 j, ... + 32);
+ *   1024 bytes that are zero.
+ * Inputs past K have code 0 and scale 0.  Several weights of N channels each
+ * stacked along the channels (the experts of a layer) are one weight of all
+ * their channels.  w4a8_mx_unpack_weights is the exact inverse.
+ * Requirements: N % 16 == 0, K % 32 == 0, 32 <= K <= 2^22, N <= 2^31.
+ */
+size_t w4a8_mx_weight_bytes(int64_t N, int64_t K);
+int w4a8_mx_pack_weights(const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K, void* packed,
+                         size_t packed_bytes, void* stream);
+int w4a8_mx_unpack_weights(const void* packed, size_t packed_bytes, int64_t N, int64_t K, uint8_t* codes,
+                           uint8_t* scales, void* stream);
+
+/*
+ * How a call runs, chosen from its sizes and the device's compute units (256
+ * on MI355X): host only, for tests and tuning; nothing is enqueued.  Kernels:
+ */
+#define W4A8_MX_TOKEN 1  /* weights streamed, rows quantised by the same kernel */
+#define W4A8_MX_STREAM 2 /* weights streamed past a few quantised rows */
+#define W4A8_MX_TILE 3   /* tiles of rows and channels through LDS */
+typedef struct {
+  int32_t path;      /* W4A8_MX_* */
+  int32_t tile_rows; /* rows of a tile, of one group */
+  int32_t tile_cols; /* its channels */
+  int32_t ksplit;    /* slices of the inputs that a reduction sums (linear only) */
+} w4a8_mx_plan_t;
+
+/*
+ * w4a8_mx_linear — y[m][n] = bf16( sum over the inputs of x'[m][k] w[n][k] ),
+ * x' the values of row m quantised to `act` by `rule`, w the packed weight's
+ * values.  Sums are float32.
+ *   x       device [M][K], bfloat16 or float
+ *   act     W4A8_MX_FP4 or W4A8_MX_FP8: the format of the rows
+ *   y       device bfloat16 bits [M][N]
+ *   workspace  device scratch of w4a8_mx_linear_workspace_bytes(M, N, K, act)
+ *           bytes; contents on entry are ignored.  The size for M rows serves
+ *           every smaller number of them
+ * Requirements: 1 <= M <= 2^24, N % 16 == 0, K % 32 == 0, 32 <= K <= 2^22,
+ * N times K rounded up to 128 below 2^32.
+ */
+int w4a8_mx_linear_plan(int64_t M, int64_t N, int64_t K, int32_t act, w4a8_mx_plan_t* plan);
+size_t w4a8_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t act);
+int w4a8_mx_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, const void* packed,
+                   size_t packed_bytes, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * w4a8_mx_grouped_linear — the product of ragged runs of rows, each with a
+ * weight of its own (the experts of a layer).
+ *   x        device [M][K], bfloat16 or float
+ *   packed   packed weight of E * N channels: group e has channels
+ *            [N e, N (e + 1))
+ *   offsets  device int32 [E + 1], ascending: product rows
+ *            [offsets[e], offsets[e + 1]) belong to group e.  Product rows
+ *            outside [offsets[0], offsets[E]) belong to none and their y stays
+ *            as it was.  Read on the device, bounded to [0, P]
+ *   rows     device int32 [P]: product row p reads x[rows[p]]; a row whose
+ *            index lies outside [0, M) gives zeros.  NULL: row p reads x[p]
+ *            (then M == P)
+ *   gated    0: y[p] = bf16( sums ), [P][N].  Else the first N / 2 channels of
+ *            a group are gates, the others values, and y[p] = bf16(
+ *            silu(gate) * value ), [P][N / 2]
+ *   workspace  device scratch of w4a8_mx_grouped_linear_workspace_bytes(M, P, E,
+ *            N, K, act) bytes; contents on entry are ignored
+ * A row's result does not depend on the other rows except through the kernel
+ * that the sizes select.  The call never synchronises and can be captured.
+ * Requirements: as w4a8_mx_linear, 1 <= M, P <= 2^24, 1 <= E <= 1024, gated:
+ * N % 32 == 0; with rows the quantised rows of x below 2^32 bytes.
+ */
+int w4a8_mx_grouped_linear_plan(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act,
+                                w4a8_mx_plan_t* plan);
+size_t w4a8_mx_grouped_linear_workspace_bytes(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K,
+                                              int32_t act);
+int w4a8_mx_grouped_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, const void* packed,
+                           size_t packed_bytes, const int32_t* offsets, const int32_t* rows, int64_t M,
+                           int64_t P, int32_t E, int64_t N, int64_t K, int32_t gated, uint16_t* y,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* W4A8_MX_H */
