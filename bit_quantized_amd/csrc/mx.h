@@ -2,14 +2,17 @@
 // interface between the kernels (mx_quant.hip, mx_stream.hip, mx_tile.hip) and
 // the entry points (mx_abi.hip).
 //
-// The matrix core product is v_mfma_scale_f32_16x16x128: 16 channels x 16 rows
-// x 128 inputs.  Lane L = 16 j + c holds
-//   4-bit operand: 32 values, inputs 32 j .. 32 j + 31 of row (channel) c;
-//   8-bit operand: inputs 16 j .. 16 j + 15, then 64 + 16 j .. 64 + 16 j + 15;
+// The matrix core product is v_mfma_scale_f32_16x16x128 (a few rows) or
+// 32x32x64 (tiles; in 4 bits it reaches 9.5 PFLOP/s where the other, bound by
+// issue, reaches 6.9, and both 5.0 with 8-bit rows): c channels x c rows x 2048
+// / c inputs.  Lane L = c j + i holds
+//   4-bit operand: 32 values, inputs 32 j .. 32 j + 31 of row (channel) i;
+//   8-bit operand: inputs 16 j .. 16 j + 15, then those 1024 / c later;
 //   scale: a byte, chosen among the four of a register, for inputs 32 j ..
 //   32 j + 31 of its row in both formats;
-//   result: row (of the second operand) c, channels 4 j .. 4 j + 3.
-// Weights are the first operand, so that a lane's four sums are neighbours in
+//   result: row (of the second operand) i, of each 4 * 64 / c channels the
+//   four from 4 j.
+// Weights are the first operand, so that four sums of a lane are neighbours in
 // the output.
 #pragma once
 
@@ -44,6 +47,7 @@ inline int64_t mx_row_scale_bytes(int64_t K) { return mx_supers(K) * kMxRowScale
 
 typedef int v8i_mx __attribute__((ext_vector_type(8)));
 typedef float v4f_mx __attribute__((ext_vector_type(4)));
+typedef float v16f_mx __attribute__((ext_vector_type(16)));
 typedef short v2s_mx __attribute__((ext_vector_type(2)));
 typedef __bf16 v2bf_mx __attribute__((ext_vector_type(2)));
 typedef float v2f_mx __attribute__((ext_vector_type(2)));
@@ -203,6 +207,11 @@ __device__ __forceinline__ v8i_mx mx_wide(v4i a, v4i b) {
 template <int FMT, int S>
 __device__ __forceinline__ v4f_mx mx_mfma(v8i_mx w, v8i_mx x, v4f_mx acc, int sw, int sx) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, FMT == kFp4 ? 4 : 0, S, sw, S, sx);
+}
+
+template <int FMT, int S>
+__device__ __forceinline__ v16f_mx mx_mfma32(v8i_mx w, v8i_mx x, v16f_mx acc, int sw, int sx) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, FMT == kFp4 ? 4 : 0, S, sw, S, sx);
 }
 
 __device__ __forceinline__ uint2 mx_bf16x4(v4f_mx v) {

@@ -185,7 +185,7 @@ int check_product(int64_t M, int64_t N, int64_t K, int32_t act) {
 // A launch has fewer than 2^32 threads.
 int check_launch(const MxPlan& p, int64_t P, int32_t E, int64_t N) {
   const int64_t tiles = E ? mx_tile_slots(P, E, p.bm) : ceil_div(P, p.bm);
-  const int64_t threads = p.path == kMxTile ? 256 : 64 * p.waves;
+  const int64_t threads = p.path == kMxTile ? (p.bm == 256 ? 512 : 256) : 64 * p.waves;
   if (tiles * ceil_div(N, p.bn) * threads >= (int64_t)1 << 32)
     return fail(W4A8_ERR_UNSUPPORTED_SHAPE, "%lld x %lld outputs in one call", (long long)P, (long long)N);
   return W4A8_OK;

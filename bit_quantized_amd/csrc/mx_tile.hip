@@ -4,16 +4,15 @@
 // Both operands pass through LDS, two buffers of one stage each: 128 bytes of
 // every row (256 inputs in 4 bits, 128 in 8) and the weight's code blocks of
 // the same inputs, all by loads that go straight to LDS.  Code blocks are
-// operands as they lie; of a row, 16-byte chunk i is kept at chunk i ^ (row %
-// 8), so that the 16 rows of an operand read spread over the banks.  Scales
-// come once per 512 inputs: a register of a lane then serves four products,
-// which choose its byte.
+// operands as they lie; of a row, 16-byte chunk i is kept at chunk i ^ (row /
+// 2 % 8), so that the 16 rows of a quarter of an operand read take 256 bytes
+// of different banks.  Scales come once per 512 inputs.
 //
-// A wavefront holds the operands of one step of 128 inputs in registers and
-// reads the next step's while it multiplies.  Before the last step of a stage
-// every wavefront has all of that stage in registers: one barrier there frees
-// its buffer for the stage after the next, whose loads then have a whole stage
-// of products to arrive in.
+// A wavefront multiplies half steps of 64 inputs, with the operands of one in
+// registers while it reads those of the next.  At the last half step of a
+// stage all of the stage is in registers: one barrier there, behind the first
+// products, frees its buffer for the stage after the next, whose loads then
+// have a whole stage of products to arrive in.
 #include "mx.h"
 
 #include <type_traits>
@@ -59,6 +58,14 @@ __device__ __forceinline__ int source_row(const MxArgs& a, int p) {
   return r >= 0 && r < a.M ? r : -1;
 }
 
+// As load_to_lds (rows.h), to LDS address `at`.
+__device__ __forceinline__ void load_at(const LdsSource& src, int at, uint32_t offset, int base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(uniform(at)), "v"(offset), "s"(src.words), "s"(uniform(base))
+               : "memory");
+}
+
 // Every load and LDS read of this wavefront has arrived; then all wavefronts.
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
@@ -67,13 +74,20 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// WM x WN wavefronts of 16 FM rows and 16 FN channels each.
+// LDS writes of this wavefront's lanes before, reads of its other lanes after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// WM x WN wavefronts of 32 FM rows and 32 FN channels each.
 template <int FMT, int WM, int WN, int FM, int FN>
 struct Shape {
   static constexpr int kWaves = WM * WN;
-  static constexpr int kRows = 16 * WM * FM, kBlocks = WN * FN;  // of the tile
-  static constexpr int kSteps = FMT == kFp4 ? 2 : 1;             // steps of a stage
-  static constexpr int kStages = 4 / kSteps;                     // stages of a super
+  static constexpr int kRows = 32 * WM * FM, kBlocks = 2 * WN * FN;  // of the tile
+  static constexpr int kSteps = FMT == kFp4 ? 2 : 1;                 // steps of 128 inputs of a stage
+  static constexpr int kStages = 4 / kSteps;                         // stages of a super
   static constexpr int kRowKiB = kRows / 8, kCodeKiB = kBlocks * kSteps;
   static constexpr int kStageBytes = (kRowKiB + kCodeKiB) * 1024;
   static constexpr int kScaleKiB = (kRows + 16 * kBlocks) / 64;
@@ -90,16 +104,16 @@ mx_tile_kernel(const MxArgs a) {
   if (!locate(a, sp)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int c = lane & 15, j = lane >> 4;
+  const int c = lane & 31, j = lane >> 5;
   const int Q0 = SPLIT ? (int)((int64_t)a.Q * blockIdx.y / gridDim.y) : 0;
   const int Q1 = SPLIT ? (int)((int64_t)a.Q * (blockIdx.y + 1) / gridDim.y) : a.Q;
 
   // Block i of the tile: plain: consecutive ones; gated: each wavefront has
-  // FN / 2 gate blocks, then the value blocks beside them.
+  // FN gate blocks, then the value blocks beside them.
   auto block_of = [&](int i) __attribute__((always_inline)) {
     if constexpr (GATED) {
-      const int f = i % FN, half = f / (FN / 2);
-      const int at = (sp.strip * WN + i / FN) * (FN / 2) + f % (FN / 2);
+      const int f = i % (2 * FN), half = f / FN;
+      const int at = (sp.strip * WN + i / (2 * FN)) * FN + f % FN;
       return half * (a.nb / 2) + min(at, a.nb / 2 - 1);
     } else {
       return min(sp.strip * S::kBlocks + i, a.nb - 1);  // past the end: never stored
@@ -113,209 +127,207 @@ mx_tile_kernel(const MxArgs a) {
   const int64_t code_bytes = (int64_t)a.nb * a.G * kBlockBytes + 1024;
   LdsSource rx = lds_source(a.qx + base * a.ldx, left * a.ldx);
   LdsSource rw = lds_source(a.codes + (int64_t)sp.group * a.nb * a.G * kBlockBytes, code_bytes);
-  const LdsSource rs = lds_source(a.qs + base * a.lds, left * a.lds);
-  const LdsSource rv = lds_source(a.scales + (int64_t)sp.group * a.nb * a.Q * kMxScaleBytes,
-                                  (int64_t)a.nb * a.Q * kMxScaleBytes);
   auto source = [&](int r) __attribute__((always_inline)) {  // of row r of the tile, from base
     const int i = min(r, sp.rows - 1);
     return a.rows ? max(source_row(a, sp.first + i), 0) : i;
   };
   constexpr int kRowLoads = S::kRowKiB / S::kWaves;
   constexpr int kCodeLoads = S::kCodeKiB / S::kWaves;
-  constexpr int kScaleLoads = (S::kScaleKiB + S::kWaves - 1) / S::kWaves;
   static_assert(S::kRowKiB % S::kWaves == 0 && S::kCodeKiB % S::kWaves == 0, "whole loads");
-  uint32_t ox[kRowLoads], ow[kCodeLoads], os[kScaleLoads];
+  static_assert(S::kScaleKiB <= S::kWaves, "one load of scales");
+  uint32_t ox[kRowLoads], ow[kCodeLoads];
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
     const int r = (wave * kRowLoads + i) * 8 + (lane >> 3);
-    ox[i] = (uint32_t)source(r) * a.ldx + 16 * ((lane & 7) ^ (r & 7));
+    ox[i] = (uint32_t)source(r) * a.ldx + 16 * ((lane & 7) ^ (r >> 1 & 7));
   }
 #pragma unroll
   for (int i = 0; i < kCodeLoads; ++i) {
     const int k = wave * kCodeLoads + i;
     ow[i] = ((uint32_t)block_of(k / S::kSteps) * a.G + k % S::kSteps) * kBlockBytes + lane * 16;
   }
-#pragma unroll
-  for (int i = 0; i < kScaleLoads; ++i) {
-    const int k = i * S::kWaves + wave;
-    os[i] = k < S::kRows / 64
-                ? (uint32_t)source(k * 64 + lane) * a.lds
-                : (uint32_t)block_of(min((k - S::kRows / 64) * 4 + (lane >> 4), S::kBlocks - 1)) * a.Q * kMxScaleBytes +
-                      (lane & 15) * 16;
-  }
-  // Load i of the kLoads that fill a stage.
+  // One KiB of scales each, of rows or of blocks (wavefronts past the last KiB
+  // load it as well).
+  const int scale_kib = min(wave, S::kScaleKiB - 1);
+  const bool row_scales = scale_kib < S::kRows / 64;
+  const LdsSource rs = lds_source(row_scales ? a.qs + base * a.lds : a.scales + (int64_t)sp.group * a.nb * a.Q * kMxScaleBytes,
+                                  row_scales ? left * a.lds : (int64_t)a.nb * a.Q * kMxScaleBytes);
+  const int scale_step = row_scales ? kMxRowScale : kMxScaleBytes;
+  const uint32_t os = row_scales ? (uint32_t)source(scale_kib * 64 + lane) * a.lds
+                                 : (uint32_t)block_of((scale_kib - S::kRows / 64) * 4 + (lane >> 4)) * a.Q * kMxScaleBytes +
+                                       (lane & 15) * 16;
+  const int lds0 = uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
+  // Load i of the kLoads that fill the stage buffer at byte `at`.
   constexpr int kLoads = kRowLoads + kCodeLoads;
-  auto fill_one = [&](int i, uint8_t* at, int t) __attribute__((always_inline)) {
+  auto fill_one = [&](int i, int at, int t) __attribute__((always_inline)) {
     if (i < kRowLoads)
-      load_to_lds(rx, at + (wave * kRowLoads + i) * 1024, (int)ox[i], t * 128);
+      load_at(rx, lds0 + at + (wave * kRowLoads + i) * 1024, ox[i], t * 128);
     else
-      load_to_lds(rw, at + (S::kRowKiB + wave * kCodeLoads + i - kRowLoads) * 1024, (int)ow[i - kRowLoads],
-                  t * S::kSteps * kBlockBytes);
+      load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i - kRowLoads) * 1024, ow[i - kRowLoads],
+              t * S::kSteps * kBlockBytes);
   };
   auto scales_at = [&](int buf) __attribute__((always_inline)) {
-    return lds + 2 * S::kStageBytes + buf * S::kScaleKiB * 1024;
+    return 2 * S::kStageBytes + buf * S::kScaleKiB * 1024;
   };
   auto fill_scales = [&](int buf, int q) __attribute__((always_inline)) {
-    uint8_t* at = scales_at(buf);
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-      const int k = i * S::kWaves + wave;
-      if (k < S::kRows / 64)
-        load_to_lds(rs, at + k * 1024, (int)os[i], q * kMxRowScale);
-      else if (k < S::kScaleKiB)
-        load_to_lds(rv, at + k * 1024, (int)os[i], q * kMxScaleBytes);
-    }
+    load_at(rs, lds0 + scales_at(buf) + scale_kib * 1024, os, q * scale_step);
   };
 
-  // ---- operands: rows in place, as soon as their products are issued; the
-  // weight's in two sets
-  v4i w[2][FN], x[FM][kUnits];
-  int sw[FN], sw1[FN], sx[FM];
-  auto read_row = [&](int m, const uint8_t* at, int step) __attribute__((always_inline)) {
+  // ---- operands of a half step, in two sets; scales, by half of a step
+  v4i w[2][FN], x[2][FM][kUnits];
+  int sw[2][FN], sx[2][FM];
+  int x_at[4];  // this lane's row of the first 32, chunks 2 i and 2 i + 1 of it
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int chunk = (FMT == kFp4 ? 4 * (step % S::kSteps) : 4 * u) + j;
-      x[m][u] = *reinterpret_cast<const v4i*>(at + ((wm * FM + m) * 16 + c) * 128 + 16 * (chunk ^ (c & 7)));
-    }
+  for (int i = 0; i < 4; ++i) x_at[i] = (wm * FM * 32 + c) * 128 + 16 * ((2 * i + j) ^ (c >> 1 & 7));
+  const int w_at = S::kRowKiB * 1024 + (wn * FN * 2 + (c >> 4)) * S::kSteps * 1024 + j * 256 + (c & 15) * 16;
+  const int sx_at = (wm * FM * 32 + c) * 16 + 4 * j;
+  const int sw_at = S::kRows * 16 + (wn * FN * 2 + (c >> 4)) * 256 + j * 64 + (c & 15) * 4;
+  // half step hs of an iteration, from the stage buffer at byte `at`
+  auto read_row = [&](int m, int at, int hs) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+      x[hs & 1][m][u] =
+          *reinterpret_cast<const v4i*>(lds + at + x_at[FMT == kFp4 ? hs & 3 : (hs & 1) * 2 + u] + m * 4096);
   };
-  auto read_block = [&](int n, int set, const uint8_t* at, int step) __attribute__((always_inline)) {
-    w[set][n] = *reinterpret_cast<const v4i*>(at + S::kRowKiB * 1024 +
-                                              ((wn * FN + n) * S::kSteps + step % S::kSteps) * 1024 + lane * 16);
+  auto read_blocks = [&](int n, int at, int hs) __attribute__((always_inline)) {
+    w[hs & 1][n] = *reinterpret_cast<const v4i*>(lds + at + w_at + n * 2 * S::kSteps * 1024 +
+                                                 (hs >> 1) % S::kSteps * 1024 + (hs & 1) * 512);
   };
-  // (half: the steps of 256 inputs, in the upper or lower half of a register)
-  auto row_scale = [&](int m, const uint8_t* at, int half) __attribute__((always_inline)) {
-    return (int)(*reinterpret_cast<const uint32_t*>(at + ((wm * FM + m) * 16 + c) * 16 + 4 * j) >> (16 * half));
-  };
-  auto block_scale = [&](int n, const uint8_t* at, int half) __attribute__((always_inline)) {
-    return (int)(*reinterpret_cast<const uint32_t*>(at + S::kRows * 16 + (wn * FN + n) * 256 + lane * 4) >>
-                 (16 * half));
+  // (an iteration's two steps have the upper or the lower two of four bytes)
+  auto read_scales = [&](int h, int at, int upper) __attribute__((always_inline)) {
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+      sx[h][m] = *reinterpret_cast<const uint16_t*>(lds + at + sx_at + 2 * upper + m * 512 + h * 8);
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      sw[h][n] = *reinterpret_cast<const uint16_t*>(lds + at + sw_at + 2 * upper + n * 512 + h * 128);
   };
 
-  v4f_mx acc[FM][FN];
+  v16f_mx acc[FM][FN];
 #pragma unroll
   for (int m = 0; m < FM; ++m)
 #pragma unroll
-    for (int n = 0; n < FN; ++n) acc[m][n] = v4f_mx{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
 
-  // Iterations of 256 inputs (two steps); the last may end in a step past the
-  // inputs, whose rows have code 0.
+  // Iterations of 256 inputs (four half steps); the last may end past the
+  // inputs, where rows have code 0.
   const int I0 = Q0 * 2, I1 = min(Q1 * 2, (a.G + 1) / 2);
   constexpr int kPer = 2 / S::kSteps;  // stages of an iteration
   const int T1 = I1 * kPer;
   if (I0 < I1) {
     fill_scales(0, Q0);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) fill_one(i, lds, I0 * kPer);
+    for (int i = 0; i < kLoads; ++i) fill_one(i, 0, I0 * kPer);
     if (I0 * kPer + 1 < T1) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) fill_one(i, lds + S::kStageBytes, I0 * kPer + 1);
+      for (int i = 0; i < kLoads; ++i) fill_one(i, S::kStageBytes, I0 * kPer + 1);
     }
     stage_barrier();
+    read_scales(0, scales_at(0), 0);
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      read_row(m, lds, 0);
-      sx[m] = row_scale(m, scales_at(0), 0);
-    }
+    for (int m = 0; m < FM; ++m) read_row(m, 0, 0);
 #pragma unroll
-    for (int n = 0; n < FN; ++n) {
-      read_block(n, 0, lds, 0);
-      sw[n] = block_scale(n, scales_at(0), 0);
-    }
+    for (int n = 0; n < FN; ++n) read_blocks(n, 0, 0);
   }
   for (int it = I0; it < I1; ++it) {
-    // the next iteration's scales: their super's buffer and half
-    const uint8_t* next_scales = scales_at((((it + 1) >> 1) - Q0) & 1);
-    const int next_half = (it + 1) & 1;
-    auto step = [&](auto sc) __attribute__((always_inline)) {
-      constexpr int s = decltype(sc)::value;
-      constexpr bool last = s % S::kSteps == S::kSteps - 1;
-      // groups of products before the barrier, which by then waits for no read
-      constexpr int kBefore = last ? (FM >= 8 ? 2 : 1) : 0;
+    auto half_step = [&](auto hc) __attribute__((always_inline)) {
+      constexpr int hs = decltype(hc)::value, s = hs >> 1, h = hs & 1;
+      constexpr bool last = h == 1 && s % S::kSteps == S::kSteps - 1;
       const int t = it * kPer + (kPer == 2 ? s : 0);
-      uint8_t* own = lds + (kPer == 2 ? s : (it - I0) & 1) * S::kStageBytes;
-      uint8_t* other = lds + (kPer == 2 ? 1 - s : 1 - ((it - I0) & 1)) * S::kStageBytes;
-      uint8_t* from = last ? other : own;
+      const int own = (kPer == 2 ? s : (it - I0) & 1) * S::kStageBytes;
+      const int from = last ? S::kStageBytes - own : own;
       const bool more = t + 2 < T1;
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
-        if (last && m == kBefore) {
-          stage_barrier();
-          rx.words[2] = more ? (int)(uint32_t)(left * a.ldx) : 0;  // (else without requests)
-          rw.words[2] = more ? (int)(uint32_t)code_bytes : 0;
-          if (more && (t + 2) % S::kStages == 0) fill_scales((((t + 2) / S::kStages) - Q0) & 1, (t + 2) / S::kStages);
-        }
         v8i_mx xv;
-        if constexpr (FMT == kFp4) xv = mx_wide(x[m][0]);
-        else xv = mx_wide(x[m][0], x[m][kUnits - 1]);
+        if constexpr (FMT == kFp4) xv = mx_wide(x[h][m][0]);
+        else xv = mx_wide(x[h][m][0], x[h][m][kUnits - 1]);
 #pragma unroll
-        for (int n = 0; n < FN; ++n) acc[m][n] = mx_mfma<FMT, s>(mx_wide(w[s][n]), xv, acc[m][n], sw[n], sx[m]);
-        if (m >= kBefore) {
-          // a share of the next step's reads, of the stage's loads
-          constexpr int kGroups = FM - kBefore;
-          const int g = m - kBefore;
+        for (int n = 0; n < FN; ++n) acc[m][n] = mx_mfma32<FMT, s>(mx_wide(w[h][n]), xv, acc[m][n], sw[h][n], sx[h][m]);
+        if (m == 0) {
+          if constexpr (last) {
+            stage_barrier();
+            rx.words[2] = more ? (int)(uint32_t)(left * a.ldx) : 0;  // (else without requests)
+            rw.words[2] = more ? (int)(uint32_t)code_bytes : 0;
+          }
 #pragma unroll
-          for (int i = 0; i < FN; ++i)
-            if (i >= g * FN / kGroups && i < (g + 1) * FN / kGroups) {
-              read_block(i, s ^ 1, from, s + 1);
-              if (s == 1) sw1[i] = block_scale(i, next_scales, next_half);
+          for (int i = 0; i < FM; ++i) read_row(i, from, hs + 1);
+#pragma unroll
+          for (int i = 0; i < FN; ++i) read_blocks(i, from, hs + 1);
+          // scales of this iteration's odd halves, of the next one's even ones
+          if constexpr (hs == 0) read_scales(1, scales_at(((it >> 1) - Q0) & 1), it & 1);
+          if constexpr (hs == 3) read_scales(0, scales_at((((it + 1) >> 1) - Q0) & 1), (it + 1) & 1);
+          if constexpr (last) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) fill_one(i, own, t + 2);
+            // The scales of that stage's super, with each of its iterations: the
+            // second time the same bytes once more.  (A branch here would let
+            // the compiler move the products of the whole iteration behind it.)
+            if constexpr (kPer == 1 || s == 0) {
+              const int q = min(t + 2, T1 - 1) / S::kStages;
+              fill_scales((q - Q0) & 1, q);
             }
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-            if (i >= g * FM / kGroups && i < (g + 1) * FM / kGroups) {
-              read_row(i, from, s + 1);
-              if (s == 1) sx[i] = row_scale(i, next_scales, next_half);
-            }
-          if (last) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-              if (i >= g * kLoads / kGroups && i < (g + 1) * kLoads / kGroups) fill_one(i, own, t + 2);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-#pragma unroll
-    for (int n = 0; n < FN; ++n) sw[n] = sw1[n];
+    half_step(std::integral_constant<int, 0>{});
+    half_step(std::integral_constant<int, 1>{});
+    half_step(std::integral_constant<int, 2>{});
+    half_step(std::integral_constant<int, 3>{});
   }
   stage_barrier();  // (the last loads, none of them a request)
 
-  // ---- out: a lane has four channels of row c of each 16
+  // ---- out: a lane has row c of each 32, and of each 32 channels the four
+  // from 8 i + 4 j, i = 0..3.  Each wavefront turns 32 rows of 256 bytes (or
+  // what it has) around in LDS, so that stores write whole lines: written from
+  // the registers, 8 bytes a row, 4096 x 16384 outputs took 100 us of their
+  // own, four times as long.
+  constexpr int kOut = GATED ? FN / 2 : FN;        // fragments of 32 channels
+  constexpr int kSize = SPLIT ? 4 : 2;             // bytes of an output
+  constexpr int kOnce = kOut * 32 * kSize > 256 ? 256 / (32 * kSize) : kOut;
+  constexpr int kRowBytes = kOnce * 32 * kSize, kStride = kRowBytes + 16;
+  static_assert(S::kWaves * 32 * kStride <= S::kLds, "fits the stages' LDS");
+  constexpr int kLanes = kRowBytes / 16;           // lanes of a row
+  uint8_t* mine = lds + wave * 32 * kStride;
+  const int width = GATED ? a.nb * 8 : a.nb * 16;
+  const int lane_row = lane / kLanes, lane_at = lane % kLanes * 16;
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
-    const int at = (wm * FM + m) * 16 + c;
-    if (at >= sp.rows) continue;
-    const int p = sp.first + at;
-    const bool gone = a.rows && source_row(a, p) < 0;
-    if constexpr (SPLIT) {
-      float* out = a.parts + ((int64_t)blockIdx.y * a.P + p) * a.nb * 16;
 #pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const int b = sp.strip * S::kBlocks + wn * FN + n;
-        if (b < a.nb) *reinterpret_cast<v4f_mx*>(out + b * 16 + 4 * j) = acc[m][n];
+    for (int n0 = 0; n0 < kOut; n0 += kOnce) {
+#pragma unroll
+      for (int n = n0; n < n0 + kOnce; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v4f_mx v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = acc[m][n][4 * i + e];
+            if constexpr (GATED) v[e] = silu_mul(v[e], acc[m][n + FN / 2][4 * i + e]);
+          }
+          uint8_t* to = mine + c * kStride + ((n - n0) * 32 + 8 * i + 4 * j) * kSize;
+          if constexpr (SPLIT) *reinterpret_cast<v4f_mx*>(to) = v;
+          else *reinterpret_cast<uint2*>(to) = mx_bf16x4(v);
+        }
+      wave_sync();
+      const int ch = ((sp.strip * WN + wn) * kOut + n0) * 32 + lane_at / kSize;
+#pragma unroll
+      for (int k = 0; k < kLanes / 2; ++k) {
+        const int r = k * (64 / kLanes) + lane_row, at = (wm * FM + m) * 32 + r;
+        v4u_rows bits = *reinterpret_cast<const v4u_rows*>(mine + r * kStride + lane_at);
+        if (at < sp.rows && ch < width) {
+          const int p = sp.first + at;
+          if (a.rows && source_row(a, p) < 0) bits = v4u_rows{0, 0, 0, 0};
+          uint8_t* out = SPLIT ? reinterpret_cast<uint8_t*>(a.parts + (int64_t)blockIdx.y * a.P * width)
+                               : reinterpret_cast<uint8_t*>(a.y);
+          *reinterpret_cast<v4u_rows*>(out + ((int64_t)p * width + ch) * kSize) = bits;
+        }
       }
-    } else if constexpr (GATED) {
-      uint16_t* out = a.y + (int64_t)p * a.nb * 8;
-#pragma unroll
-      for (int n = 0; n < FN / 2; ++n) {
-        const int b = (sp.strip * WN + wn) * (FN / 2) + n;
-        v4f_mx v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = silu_mul(acc[m][n][i], acc[m][n + FN / 2][i]);
-        uint2 bits = mx_bf16x4(v);
-        if (gone) bits = uint2{0u, 0u};
-        if (b < a.nb / 2) *reinterpret_cast<uint2*>(out + b * 16 + 4 * j) = bits;
-      }
-    } else {
-      uint16_t* out = a.y + (int64_t)p * a.nb * 16;
-#pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const int b = sp.strip * S::kBlocks + wn * FN + n;
-        uint2 bits = mx_bf16x4(acc[m][n]);
-        if (gone) bits = uint2{0u, 0u};
-        if (b < a.nb) *reinterpret_cast<uint2*>(out + b * 16 + 4 * j) = bits;
-      }
+      wave_sync();
     }
   }
 }
@@ -348,9 +360,9 @@ hipError_t launch_shape(const MxArgs& a, const MxPlan& p, bool gated, unsigned b
 
 template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
-  if (p.bm == 256) return launch_shape<FMT, 2, 2, 8, 8>(a, p, gated, blocks, st);
-  if (p.bm == 128) return launch_shape<FMT, 2, 2, 4, 4>(a, p, gated, blocks, st);
-  return launch_shape<FMT, 1, 4, 4, 2>(a, p, gated, blocks, st);
+  if (p.bm == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
+  if (p.bm == 128) return launch_shape<FMT, 2, 2, 2, 2>(a, p, gated, blocks, st);
+  return launch_shape<FMT, 2, 2, 1, 2>(a, p, gated, blocks, st);
 }
 
 }  // namespace
@@ -358,7 +370,7 @@ hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blo
 hipError_t launch_mx_tile(const MxArgs& a, const MxPlan& p, int fmt, bool gated, hipStream_t st) {
   const int64_t tiles = a.offsets ? mx_tile_slots(a.P, a.E, a.bm) : (a.P + a.bm - 1) / a.bm;
   const int64_t blocks = tiles * a.strips;
-  if (blocks * 256 >= ((int64_t)1 << 32)) return hipErrorInvalidValue;
+  if (blocks * 512 >= ((int64_t)1 << 32)) return hipErrorInvalidValue;
   hipError_t e = fmt == kFp4 ? launch_fmt<kFp4>(a, p, gated, (unsigned)blocks, st)
                              : launch_fmt<kFp8>(a, p, gated, (unsigned)blocks, st);
   if (e != hipSuccess || p.ksplit == 1) return e;
