@@ -1,18 +1,19 @@
 // Products of many rows with a microscaled 4-bit weight: tiles of rows and
 // channels, bound by the matrix cores.
 //
-// Both operands pass through LDS, two buffers of one stage each: 128 bytes of
-// every row (256 inputs in 4 bits, 128 in 8) and the weight's code blocks of
-// the same inputs, all by loads that go straight to LDS.  Code blocks are
-// operands as they lie; of a row, 16-byte chunk i is kept at chunk i ^ (row /
-// 2 % 8), so that the 16 rows of a quarter of an operand read take 256 bytes
-// of different banks.  Scales come once per 512 inputs.
+// Both operands pass through LDS in stages of 128 inputs, all by loads that go
+// straight to LDS: of every row 64 bytes (4 bits) or 128 (8), and the weight's
+// code blocks, which are operands as they lie.  16-byte chunk i of a row is
+// kept at another place, i ^ (row / 4 % 4) or i ^ (row / 2 % 8), so that the
+// 16 rows of a quarter of an operand read take 256 bytes of different banks.
+// Scales come once per 256 inputs (a load has those of 512).
 //
 // A wavefront multiplies half steps of 64 inputs, with the operands of one in
 // registers while it reads those of the next.  At the last half step of a
 // stage all of the stage is in registers: one barrier there, behind the first
-// products, frees its buffer for the stage after the next, whose loads then
-// have a whole stage of products to arrive in.
+// products, frees its buffer for the stage after those in flight.  Four
+// buffers (three with 8-bit rows) keep loads on their way behind the one that
+// the barrier waits for.
 #include "mx.h"
 
 #include <type_traits>
@@ -66,10 +67,13 @@ __device__ __forceinline__ void load_at(const LdsSource& src, int at, uint32_t o
                : "memory");
 }
 
-// Every load and LDS read of this wavefront has arrived; then all wavefronts.
+// All but this wavefront's last N loads and every LDS read of it have arrived;
+// then all wavefronts.
+template <int N>
 __device__ __forceinline__ void stage_barrier() {
+  static_assert(N < 64, "six bits of count");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);  // lgkmcnt 0
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -86,12 +90,12 @@ template <int FMT, int WM, int WN, int FM, int FN>
 struct Shape {
   static constexpr int kWaves = WM * WN;
   static constexpr int kRows = 32 * WM * FM, kBlocks = 2 * WN * FN;  // of the tile
-  static constexpr int kSteps = FMT == kFp4 ? 2 : 1;                 // steps of 128 inputs of a stage
-  static constexpr int kStages = 4 / kSteps;                         // stages of a super
-  static constexpr int kRowKiB = kRows / 8, kCodeKiB = kBlocks * kSteps;
+  static constexpr int kRowBytes = FMT == kFp4 ? 64 : 128;           // of a stage
+  static constexpr int kRowKiB = kRows * kRowBytes / 1024, kCodeKiB = kBlocks;
+  static constexpr int kBuffers = FMT == kFp4 ? 4 : 3;
   static constexpr int kStageBytes = (kRowKiB + kCodeKiB) * 1024;
   static constexpr int kScaleKiB = (kRows + 16 * kBlocks) / 64;
-  static constexpr int kLds = 2 * (kStageBytes + kScaleKiB * 1024);
+  static constexpr int kLds = kBuffers * kStageBytes + 2 * kScaleKiB * 1024;
 };
 
 template <int FMT, int WM, int WN, int FM, int FN, bool GATED, bool SPLIT>
@@ -136,16 +140,16 @@ mx_tile_kernel(const MxArgs a) {
   static_assert(S::kRowKiB % S::kWaves == 0 && S::kCodeKiB % S::kWaves == 0, "whole loads");
   static_assert(S::kScaleKiB <= S::kWaves, "one load of scales");
   uint32_t ox[kRowLoads], ow[kCodeLoads];
+  constexpr int kChunks = S::kRowBytes / 16;
+  auto place = [&](int r) __attribute__((always_inline)) { return FMT == kFp4 ? r >> 2 & 3 : r >> 1 & 7; };
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
-    const int r = (wave * kRowLoads + i) * 8 + (lane >> 3);
-    ox[i] = (uint32_t)source(r) * a.ldx + 16 * ((lane & 7) ^ (r >> 1 & 7));
+    const int r = (wave * kRowLoads + i) * (64 / kChunks) + lane / kChunks;
+    ox[i] = (uint32_t)source(r) * a.ldx + 16 * (lane % kChunks ^ place(r));
   }
 #pragma unroll
-  for (int i = 0; i < kCodeLoads; ++i) {
-    const int k = wave * kCodeLoads + i;
-    ow[i] = ((uint32_t)block_of(k / S::kSteps) * a.G + k % S::kSteps) * kBlockBytes + lane * 16;
-  }
+  for (int i = 0; i < kCodeLoads; ++i)
+    ow[i] = (uint32_t)block_of(wave * kCodeLoads + i) * a.G * kBlockBytes + lane * 16;
   // One KiB of scales each, of rows or of blocks (wavefronts past the last KiB
   // load it as well).
   const int scale_kib = min(wave, S::kScaleKiB - 1);
@@ -157,50 +161,60 @@ mx_tile_kernel(const MxArgs a) {
                                  : (uint32_t)block_of((scale_kib - S::kRows / 64) * 4 + (lane >> 4)) * a.Q * kMxScaleBytes +
                                        (lane & 15) * 16;
   const int lds0 = uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
-  // Load i of the kLoads that fill the stage buffer at byte `at`.
-  constexpr int kLoads = kRowLoads + kCodeLoads;
-  auto fill_one = [&](int i, int at, int t) __attribute__((always_inline)) {
-    if (i < kRowLoads)
-      load_at(rx, lds0 + at + (wave * kRowLoads + i) * 1024, ox[i], t * 128);
-    else
-      load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i - kRowLoads) * 1024, ow[i - kRowLoads],
-              t * S::kSteps * kBlockBytes);
-  };
   auto scales_at = [&](int buf) __attribute__((always_inline)) {
-    return 2 * S::kStageBytes + buf * S::kScaleKiB * 1024;
+    return S::kBuffers * S::kStageBytes + buf * S::kScaleKiB * 1024;
   };
-  auto fill_scales = [&](int buf, int q) __attribute__((always_inline)) {
-    load_at(rs, lds0 + scales_at(buf) + scale_kib * 1024, os, q * scale_step);
+  // Stages of 128 inputs T0 .. T1 - 1, two to an iteration; the last one may
+  // lie past the inputs, where rows have code 0.
+  const int I0 = Q0 * 2, I1 = min(Q1 * 2, (a.G + 1) / 2), T0 = I0 * 2, T1 = I1 * 2;
+  // Loads of stage t to the buffer at byte `at`; past the last stage without a
+  // request.  Even stages bring the scales of their super, the second time the
+  // same bytes once more (a branch here would let the compiler move the
+  // products of the whole iteration behind it).
+  constexpr int kLoads = kRowLoads + kCodeLoads;
+  auto fill = [&](int at, int t, bool even) __attribute__((always_inline)) {
+    if (even) {
+      const int q = min(t, T1 - 1) >> 2;
+      load_at(rs, lds0 + scales_at((q - Q0) & 1) + scale_kib * 1024, os, q * scale_step);
+    }
+    rx.words[2] = t < T1 ? (int)(uint32_t)(left * a.ldx) : 0;
+    rw.words[2] = t < T1 ? (int)(uint32_t)code_bytes : 0;
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i)
+      load_at(rx, lds0 + at + (wave * kRowLoads + i) * 1024, ox[i], t * S::kRowBytes);
+#pragma unroll
+    for (int i = 0; i < kCodeLoads; ++i)
+      load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i) * 1024, ow[i], t * kBlockBytes);
   };
 
   // ---- operands of a half step, in two sets; scales, by half of a step
   v4i w[2][FN], x[2][FM][kUnits];
   int sw[2][FN], sx[2][FM];
-  int x_at[4];  // this lane's row of the first 32, chunks 2 i and 2 i + 1 of it
+  int x_at[kChunks / 2];  // this lane's row of the first 32, chunks 2 i and 2 i + 1 of it
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x_at[i] = (wm * FM * 32 + c) * 128 + 16 * ((2 * i + j) ^ (c >> 1 & 7));
-  const int w_at = S::kRowKiB * 1024 + (wn * FN * 2 + (c >> 4)) * S::kSteps * 1024 + j * 256 + (c & 15) * 16;
+  for (int i = 0; i < kChunks / 2; ++i)
+    x_at[i] = (wm * FM * 32 + c) * S::kRowBytes + 16 * ((2 * i + j) ^ place(c));
+  const int w_at = S::kRowKiB * 1024 + (wn * FN * 2 + (c >> 4)) * 1024 + j * 256 + (c & 15) * 16;
   const int sx_at = (wm * FM * 32 + c) * 16 + 4 * j;
   const int sw_at = S::kRows * 16 + (wn * FN * 2 + (c >> 4)) * 256 + j * 64 + (c & 15) * 4;
-  // half step hs of an iteration, from the stage buffer at byte `at`
-  auto read_row = [&](int m, int at, int hs) __attribute__((always_inline)) {
+  // half h of the stage in the buffer at byte `at`
+  auto read_row = [&](int m, int at, int h) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u)
-      x[hs & 1][m][u] =
-          *reinterpret_cast<const v4i*>(lds + at + x_at[FMT == kFp4 ? hs & 3 : (hs & 1) * 2 + u] + m * 4096);
+      x[h][m][u] = *reinterpret_cast<const v4i*>(lds + at + x_at[h * kUnits + u] + m * 32 * S::kRowBytes);
   };
-  auto read_blocks = [&](int n, int at, int hs) __attribute__((always_inline)) {
-    w[hs & 1][n] = *reinterpret_cast<const v4i*>(lds + at + w_at + n * 2 * S::kSteps * 1024 +
-                                                 (hs >> 1) % S::kSteps * 1024 + (hs & 1) * 512);
+  auto read_blocks = [&](int n, int at, int h) __attribute__((always_inline)) {
+    w[h][n] = *reinterpret_cast<const v4i*>(lds + at + w_at + n * 2048 + h * 512);
   };
   // (an iteration's two steps have the upper or the lower two of four bytes)
-  auto read_scales = [&](int h, int at, int upper) __attribute__((always_inline)) {
+  auto read_scales = [&](int h, int it) __attribute__((always_inline)) {
+    const int at = scales_at(((it >> 1) - Q0) & 1) + 2 * (it & 1);
 #pragma unroll
     for (int m = 0; m < FM; ++m)
-      sx[h][m] = *reinterpret_cast<const uint16_t*>(lds + at + sx_at + 2 * upper + m * 512 + h * 8);
+      sx[h][m] = *reinterpret_cast<const uint16_t*>(lds + at + sx_at + m * 512 + h * 8);
 #pragma unroll
     for (int n = 0; n < FN; ++n)
-      sw[h][n] = *reinterpret_cast<const uint16_t*>(lds + at + sw_at + 2 * upper + n * 512 + h * 128);
+      sw[h][n] = *reinterpret_cast<const uint16_t*>(lds + at + sw_at + n * 512 + h * 128);
   };
 
   v16f_mx acc[FM][FN];
@@ -211,34 +225,23 @@ mx_tile_kernel(const MxArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
 
-  // Iterations of 256 inputs (four half steps); the last may end past the
-  // inputs, where rows have code 0.
-  const int I0 = Q0 * 2, I1 = min(Q1 * 2, (a.G + 1) / 2);
-  constexpr int kPer = 2 / S::kSteps;  // stages of an iteration
-  const int T1 = I1 * kPer;
-  if (I0 < I1) {
-    fill_scales(0, Q0);
+  if (T0 < T1) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) fill_one(i, 0, I0 * kPer);
-    if (I0 * kPer + 1 < T1) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) fill_one(i, S::kStageBytes, I0 * kPer + 1);
-    }
-    stage_barrier();
-    read_scales(0, scales_at(0), 0);
+    for (int b = 0; b < S::kBuffers; ++b) fill(b * S::kStageBytes, T0 + b, b % 2 == 0);
+    stage_barrier<(S::kBuffers - 1) * kLoads + (S::kBuffers - 1) / 2>();
+    read_scales(0, I0);
 #pragma unroll
     for (int m = 0; m < FM; ++m) read_row(m, 0, 0);
 #pragma unroll
     for (int n = 0; n < FN; ++n) read_blocks(n, 0, 0);
   }
+  int own = 0;  // the buffer of the stage that is multiplied
   for (int it = I0; it < I1; ++it) {
-    auto half_step = [&](auto hc) __attribute__((always_inline)) {
-      constexpr int hs = decltype(hc)::value, s = hs >> 1, h = hs & 1;
-      constexpr bool last = h == 1 && s % S::kSteps == S::kSteps - 1;
-      const int t = it * kPer + (kPer == 2 ? s : 0);
-      const int own = (kPer == 2 ? s : (it - I0) & 1) * S::kStageBytes;
-      const int from = last ? S::kStageBytes - own : own;
-      const bool more = t + 2 < T1;
+    auto half_step = [&](auto sc, auto hc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, h = decltype(hc)::value;
+      constexpr bool last = h == 1;
+      const int next = own == (S::kBuffers - 1) * S::kStageBytes ? 0 : own + S::kStageBytes;
+      const int from = last ? next : own;
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
         v8i_mx xv;
@@ -247,39 +250,34 @@ mx_tile_kernel(const MxArgs a) {
 #pragma unroll
         for (int n = 0; n < FN; ++n) acc[m][n] = mx_mfma32<FMT, s>(mx_wide(w[h][n]), xv, acc[m][n], sw[h][n], sx[h][m]);
         if (m == 0) {
-          if constexpr (last) {
-            stage_barrier();
-            rx.words[2] = more ? (int)(uint32_t)(left * a.ldx) : 0;  // (else without requests)
-            rw.words[2] = more ? (int)(uint32_t)code_bytes : 0;
-          }
+          // behind the stage that is read next: kBuffers - 2 of them, every
+          // second one with a load of scales (even stages go to even steps
+          // when the buffers are even in number, to odd ones when not)
+          constexpr int kBehind = S::kBuffers - 2;
+          constexpr bool even_first = s == 0;  // stage t + 2 for step s of t
+          if constexpr (last) stage_barrier<kBehind * kLoads + (kBehind + (even_first ? 1 : 0)) / 2>();
 #pragma unroll
-          for (int i = 0; i < FM; ++i) read_row(i, from, hs + 1);
+          for (int i = 0; i < FM; ++i) read_row(i, from, 1 - h);
 #pragma unroll
-          for (int i = 0; i < FN; ++i) read_blocks(i, from, hs + 1);
+          for (int i = 0; i < FN; ++i) read_blocks(i, from, 1 - h);
           // scales of this iteration's odd halves, of the next one's even ones
-          if constexpr (hs == 0) read_scales(1, scales_at(((it >> 1) - Q0) & 1), it & 1);
-          if constexpr (hs == 3) read_scales(0, scales_at((((it + 1) >> 1) - Q0) & 1), (it + 1) & 1);
+          if constexpr (s == 0 && h == 0) read_scales(1, it);
+          if constexpr (s == 1 && h == 1) read_scales(0, it + 1);
           if constexpr (last) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) fill_one(i, own, t + 2);
-            // The scales of that stage's super, with each of its iterations: the
-            // second time the same bytes once more.  (A branch here would let
-            // the compiler move the products of the whole iteration behind it.)
-            if constexpr (kPer == 1 || s == 0) {
-              const int q = min(t + 2, T1 - 1) / S::kStages;
-              fill_scales((q - Q0) & 1, q);
-            }
+            const int t = 2 * it + s + S::kBuffers;
+            fill(own, t, (s + S::kBuffers) % 2 == 0);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (last) own = next;
     };
-    half_step(std::integral_constant<int, 0>{});
-    half_step(std::integral_constant<int, 1>{});
-    half_step(std::integral_constant<int, 2>{});
-    half_step(std::integral_constant<int, 3>{});
+    half_step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
+    half_step(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+    half_step(std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
+    half_step(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
   }
-  stage_barrier();  // (the last loads, none of them a request)
+  stage_barrier<0>();  // (the last loads, none of them a request)
 
   // ---- out: a lane has row c of each 32, and of each 32 channels the four
   // from 8 i + 4 j, i = 0..3.  Each wavefront turns 32 rows of 256 bytes (or
@@ -289,9 +287,9 @@ mx_tile_kernel(const MxArgs a) {
   constexpr int kOut = GATED ? FN / 2 : FN;        // fragments of 32 channels
   constexpr int kSize = SPLIT ? 4 : 2;             // bytes of an output
   constexpr int kOnce = kOut * 32 * kSize > 256 ? 256 / (32 * kSize) : kOut;
-  constexpr int kRowBytes = kOnce * 32 * kSize, kStride = kRowBytes + 16;
+  constexpr int kTurned = kOnce * 32 * kSize, kStride = kTurned + 16;
   static_assert(S::kWaves * 32 * kStride <= S::kLds, "fits the stages' LDS");
-  constexpr int kLanes = kRowBytes / 16;           // lanes of a row
+  constexpr int kLanes = kTurned / 16;             // lanes of a row
   uint8_t* mine = lds + wave * 32 * kStride;
   const int width = GATED ? a.nb * 8 : a.nb * 16;
   const int lane_row = lane / kLanes, lane_at = lane % kLanes * 16;
