@@ -32,18 +32,35 @@ constexpr int64_t kMxMaxK = (int64_t)1 << 22;
 
 inline int64_t mx_steps(int64_t K) { return (K + kMxStep - 1) / kMxStep; }
 inline int64_t mx_supers(int64_t K) { return (K + kMxSuper - 1) / kMxSuper; }
-inline int64_t mx_scales_offset(int64_t N, int64_t K) { return N / 16 * mx_steps(K) * kBlockBytes; }
+// Strides are odd numbers of what is loaded at once (1 KiB of codes, 128 bytes
+// of a row's), so that loads at the same inputs of neighbouring channels and
+// rows spread over the memory channels instead of meeting in a few.
+inline int64_t mx_code_stride(int64_t K) { return mx_steps(K) | 1; }
+inline int64_t mx_scale_stride(int64_t K) { return mx_supers(K) | 1; }
+inline int64_t mx_scales_offset(int64_t N, int64_t K) { return N / 16 * mx_code_stride(K) * kBlockBytes; }
 inline int64_t mx_weight_bytes(int64_t N, int64_t K) {
-  return mx_scales_offset(N, K) + N / 16 * mx_supers(K) * kMxScaleBytes + 1024;
+  return mx_scales_offset(N, K) + N / 16 * mx_scale_stride(K) * kMxScaleBytes + 1024;
 }
-// Quantised rows in a workspace: codes [rows][mx_row_bytes], inputs in whole
-// 256, so that no iteration of two steps leaves its row; scales
-// [rows][mx_supers * 16], byte 4 j + s of 16 for inputs 128 s + 32 j of 512.
-// Inputs past K have code 0 and scale 0.
+// Quantised rows in a workspace, in one of two layouts; in both, inputs past K
+// have code 0 and scale 0.
+// Rows (tiles, whose loads to LDS take whole pieces of a row): codes
+// [rows][mx_row_bytes], inputs in whole 256, so that no iteration of two steps
+// leaves its row; scales [rows][mx_row_scale_bytes], byte 4 j + s of 16 for
+// inputs 128 s + 32 j of 512.
+// Interleaved (the stream, whose lanes load operands): like the weight's
+// blocks.  Codes of rows 16 b + c, inputs 128 g and on, at (b G + g) blocks of 1
+// KiB (4 bits) or 2, 16-byte unit 16 j + c (and 64 + 16 j + c); scales at (b Q +
+// q) 256 + 4 (16 j + c).  The 16 rows of a load are at most two runs of
+// consecutive bytes per j wherever they start.  Read from the other layout,
+// every lane would meet a line of its own: 16 rows 18944 -> 3584 took 17.4 us.
 inline int64_t mx_row_bytes(int64_t K, int fmt) {
-  return (K + 255) / 256 * (fmt == kFp4 ? 128 : 256);
+  return ((K + 255) / 256 * (fmt == kFp4 ? 1 : 2) | 1) * 128;
 }
-inline int64_t mx_row_scale_bytes(int64_t K) { return mx_supers(K) * kMxRowScale; }
+inline int64_t mx_row_scale_bytes(int64_t K) { return mx_scale_stride(K) * kMxRowScale; }
+inline int64_t mx_block_bytes(int64_t K, int fmt) {  // of 16 interleaved rows
+  return mx_steps(K) * kBlockBytes * (fmt == kFp4 ? 1 : 2);
+}
+inline int64_t mx_block_scale_bytes(int64_t K) { return mx_supers(K) * kMxScaleBytes; }
 
 typedef int v8i_mx __attribute__((ext_vector_type(8)));
 typedef float v4f_mx __attribute__((ext_vector_type(4)));
@@ -176,6 +193,7 @@ struct MxArgs {
   int64_t M;              // source rows
   int64_t P;              // product rows
   int E, K, G, Q;         // groups, inputs, steps of 128, of 512
+  int gstride, qstride;            // strides of the planes, in blocks
   int ldx, lds;           // bytes of a quantised row and of its scales
   int nb;                 // 16-channel blocks of a group
   int strips;             // column strips of a tile
@@ -234,10 +252,19 @@ hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int64_t N
                           hipStream_t st);
 hipError_t launch_mx_unpack(const uint8_t* packed, int64_t N, int64_t K, uint8_t* codes, uint8_t* scales,
                             hipStream_t st);
-// Rows into the workspace layout (a.codes, a.scales), and, with offsets, the
-// tiles of bm rows of each group.
-hipError_t launch_mx_rows(const MxQuantArgs& a, const int* offsets, int E, int64_t P, int bm, int* ntiles,
-                          MxTile* tiles, hipStream_t st);
+// Rows into a workspace layout (a.codes, a.scales), and, with offsets, the
+// tiles of bm rows of each group.  Interleaved: the P product rows, with rows
+// those that it names (zeros where it names none); else the a.M rows of x.
+struct MxRowsArgs {
+  bool interleaved;
+  const int* rows;
+  const int* offsets;
+  int E, bm;
+  int64_t P;
+  int* ntiles;
+  MxTile* tiles;
+};
+hipError_t launch_mx_rows(const MxQuantArgs& a, const MxRowsArgs& r, hipStream_t st);
 
 enum MxPath { kMxToken = 1, kMxStream = 2, kMxTile = 3 };
 struct MxPlan {

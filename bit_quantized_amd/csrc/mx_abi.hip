@@ -13,68 +13,131 @@ namespace {
 constexpr int64_t kMostRows = (int64_t)1 << 24;
 constexpr int64_t kMostOffset = ((int64_t)1 << 32) - 1;  // bytes that 32 bits of offset reach
 
-struct TileShape {
-  int bm, bn;
-};
-constexpr TileShape kSmall{64, 128}, kMiddle{128, 128}, kLarge{256, 256};
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Wavefronts of a stream workgroup: those that share the supers most evenly,
-// the more the better.
-int stream_waves(int64_t Q) {
-  int best = 1;
-  int64_t best_cost = Q;
-  for (int w = 1; w <= 8 && w <= Q; ++w) {
-    const int64_t cost = ceil_div(Q, w);
-    if (cost < best_cost) {
-      best = w;
-      best_cost = cost;
+// Tiles of the tile kernel.  `one` and `two`: microseconds of a step of 128
+// inputs where a compute unit has one of them, and where it has as many as fit
+// (`fit`); 3584 and 18944 inputs, either format, 16 to 4096 rows, +- 20 %.
+struct TileShape {
+  int bm, bn, fit;
+  double one, two;
+};
+constexpr TileShape kShapes[] = {{64, 128, 2, 0.35, 0.55}, {128, 128, 2, 0.47, 0.82}, {128, 256, 1, 0.80, 0.80},
+                                 {256, 256, 1, 1.25, 1.25}};
+constexpr int kSplitMost = 16;
+
+// Microseconds of `tiles` tiles of `steps` steps each.
+double tile_cost(const TileShape& s, int64_t tiles, double steps) {
+  const int64_t cus = device_cus(), round = cus * s.fit;
+  const int64_t rest = tiles % round;
+  return steps * (double(tiles / round) * s.two + (rest == 0 ? 0.0 : rest <= cus ? s.one : s.two));
+}
+
+// The linear's tiles: the shape and split of least cost.  A split adds a
+// launch and its sums, written and read at 4 TB/s (33 rows 18944 -> 3584: 16.8
+// us of 8 slices, 17.6 of 9, 52 unsplit).
+double plan_tiles(MxPlan& p, int64_t M, int64_t N, int64_t Q) {
+  double best = 1e30;
+  for (const TileShape& s : kShapes) {
+    const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
+    for (int64_t k = 1; k == 1 || (k <= kSplitMost && k <= Q / 2 && tiles * k <= device_cus()); ++k) {
+      if (ceil_div(Q, ceil_div(Q, k)) != k) continue;  // as long with fewer
+      const double cost = tile_cost(s, tiles * k, 4.0 * ceil_div(Q, k)) + (k > 1 ? 3.0 + 8e-6 * k * M * N / 4.0 : 0.0);
+      if (cost < best) {
+        best = cost;
+        p.bm = s.bm;
+        p.bn = s.bn;
+        p.ksplit = (int)k;
+      }
     }
   }
   return best;
 }
 
-// Raw rows that a token workgroup quantises into LDS.
-constexpr int64_t kTokenLds = 48 * 1024;
+// Rows that the stream takes, all at once or of a group, and its 16-row
+// fragments a workgroup.
+constexpr int kStreamRows = 64;
 
-int split_of(int64_t tiles, int64_t Q) {
-  const int64_t room = device_cus() / tiles;
-  return (int)std::max<int64_t>(1, std::min(room, Q / 2));
+// Microseconds of the stream for M rows: the weight from memory, or the rows
+// through the L1 caches of the compute units, KiB at 45 a microsecond (33 rows
+// 18944 -> 3584 in 8 bits: 16 us; 64 rows 4096 -> 4096 in 4: 4).
+double stream_cost(int64_t M, int64_t N, int64_t K, int fmt) {
+  const double blocks = std::max(1.0, N / 16.0 / device_cus()), G = double(mx_steps(K));
+  const double kib = blocks * G * (ceil_div(M, 16) * (fmt == kFp4 ? 1 : 2) + 1);
+  return std::max(kib / 45.0, N * K * 0.53 / 6.5e6);
+}
+
+// Wavefronts of a stream workgroup: as many as shorten the longest share of
+// the supers.
+int stream_waves(int64_t Q, int most) {
+  int best = 1;
+  for (int w = 2; w <= most && w <= Q; ++w)
+    if (ceil_div(Q, w) < ceil_div(Q, best)) best = w;
+  return best;
+}
+
+// Raw rows: every workgroup quantises all of its tile's.  It saves a launch
+// (2.5 us) where there are one or two, or the rows that workgroups read again
+// are few bytes (8 rows 3584 -> 3584: 8.2 against 9.6 us; 4 rows 3584 ->
+// 18944, 34 MB: 12.3 against 11.5).
+constexpr int64_t kTokenLds = 48 * 1024, kTokenReads = 20 << 20;
+bool token_fits(int64_t rows, int64_t N, int64_t K, int fmt) {
+  return rows <= 16 && rows * (mx_row_bytes(K, fmt) + mx_row_scale_bytes(K)) <= kTokenLds &&
+         (rows <= 2 || N / 16 * rows * K * 2 <= kTokenReads);
 }
 
 }  // namespace
 
 MxPlan mx_plan(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
   MxPlan p;
-  const int64_t Q = mx_supers(K), cus = device_cus();
-  const int64_t row = mx_row_bytes(K, fmt) + mx_row_scale_bytes(K);
-  const int64_t per = E ? ceil_div(P, E) : P;  // rows of a group, evenly shared
-  const int64_t most = std::min<int64_t>(P, 16);
-  if (E ? P <= 16 : P <= 4) p.path = most * row <= kTokenLds ? kMxToken : kMxStream;
-  else if (per <= 16) p.path = kMxStream;
-  else p.path = kMxTile;
-  if (p.path != kMxTile) {
-    p.bm = 16;
-    p.bn = 16;
-    p.waves = stream_waves(Q);
+  const int64_t Q = mx_supers(K);
+  p.bm = p.bn = 16;
+  if (token_fits(P, N, K, fmt)) {
+    p.path = kMxToken;
+  } else if (!E) {
+    const double tiles = M > 16 ? plan_tiles(p, M, N, Q) : 1e30;
+    p.path = kMxTile;
+    if (M <= 16 || (M <= kStreamRows && stream_cost(M, N, K, fmt) < tiles)) {
+      p.path = kMxStream;
+      p.ksplit = 1;
+      p.bm = (int)ceil_div(M, 16) * 16;
+      p.bn = M > 16 && N / 32 >= device_cus() ? 32 : 16;  // (20 rows 3584 -> 18944: 14.4 against 16.1 us)
+    }
   } else {
-    auto work = [&](const TileShape& s) { return (E ? P / s.bm + E / 2 : ceil_div(P, s.bm)) * ceil_div(N, s.bn); };
-    TileShape s = kLarge;
-    if (per <= 64) s = kSmall;
-    else if (per <= 128 || work(kLarge) * 4 < cus * 3) s = kMiddle;
-    p.bm = s.bm;
-    p.bn = s.bn;
-    if (!E) p.ksplit = split_of(work(s), Q);
+    // By the rows of a group, evenly shared (the groups' own numbers are on
+    // the device): 64 tokens x 8 of 128 (4 rows a group) take 31 us streamed,
+    // 256 (16 rows) 47, and 37 in tiles of 64; 64 rows a group 51, and 57 in
+    // tiles of 128; 384 rows 220, against 224 (128 x 128), 228 (256 x 256) and
+    // 261 (64 x 128).
+    const double per = double(P) / E;
+    p.path = kMxTile;
+    if (per <= 8) {
+      p.path = kMxStream;
+      p.bn = 32;  // (of the plain product: 27.1 against 29.7 us at 4 rows a group)
+    } else if (per <= 80) {
+      p.bm = 64, p.bn = 128;
+    } else if (per <= 256 || N <= 256) {
+      p.bm = 128, p.bn = 128;
+    } else if (per <= 768) {
+      p.bm = 128, p.bn = 256;
+    } else {
+      p.bm = 256, p.bn = 256;
+    }
   }
+  if (p.path != kMxTile) p.waves = stream_waves(Q, p.bm > 16 ? 8 : 16);
   auto take = [&](int64_t bytes) {
     const int64_t at = p.bytes;
     p.bytes += round_up256(bytes);
     return at;
   };
   if (p.path != kMxToken) {
-    p.codes = take(M * mx_row_bytes(K, fmt));
-    p.scales = take(M * mx_row_scale_bytes(K));
+    if (p.path == kMxStream) {
+      p.codes = take(ceil_div(P, 16) * mx_block_bytes(K, fmt));
+      p.scales = take(ceil_div(P, 16) * mx_block_scale_bytes(K));
+    } else {
+      p.codes = take(M * mx_row_bytes(K, fmt));
+      p.scales = take(M * mx_row_scale_bytes(K));
+    }
     if (E) {
       p.ntiles = take(sizeof(int));
       p.tiles = take(mx_tile_slots(P, E, p.bm) * (int64_t)sizeof(MxTile));
@@ -89,16 +152,17 @@ namespace {
 
 // Bytes that serve M (P) rows and every smaller number of them.
 int64_t workspace_bound(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
-  int64_t n = round_up256(M * mx_row_bytes(K, fmt)) + round_up256(M * mx_row_scale_bytes(K));
+  // rows, or interleaved product rows of the stream
+  const int64_t Ps = std::min<int64_t>(P, E ? (int64_t)kStreamRows * E : kStreamRows);
+  const int64_t n = std::max(round_up256(M * mx_row_bytes(K, fmt)) + round_up256(M * mx_row_scale_bytes(K)),
+                             ceil_div(Ps, 16) * (mx_block_bytes(K, fmt) + mx_block_scale_bytes(K)));
   if (E) return n + 256 + round_up256(mx_tile_slots(P, E, 16) * (int64_t)sizeof(MxTile));
-  // ksplit times the tiles is at most the compute units, and at most half the supers a tile
+  // ksplit times the tiles is at most the compute units; no split of fewer than four supers
   int64_t parts = 0;
   const int64_t Q = mx_supers(K);
-  for (const TileShape& s : {kSmall, kMiddle, kLarge}) {
-    const int64_t strips = ceil_div(N, s.bn);
-    if (strips * 2 > device_cus() || Q < 4) continue;  // never split
-    parts = std::max(parts, std::min<int64_t>((int64_t)device_cus() * s.bm * s.bn, Q / 2 * M * N));
-  }
+  for (const TileShape& s : kShapes)
+    if (Q >= 4 && ceil_div(N, s.bn) * 2 <= device_cus())  // (else never split)
+      parts = std::max(parts, std::min((int64_t)device_cus() * s.bm * s.bn, std::min<int64_t>(kSplitMost, Q / 2) * M * N));
   return std::max<int64_t>(n + round_up256(parts * 4), 256);
 }
 
@@ -177,7 +241,7 @@ int check_product(int64_t M, int64_t N, int64_t K, int32_t act) {
   if (int rc = check_rows(M)) return rc;
   if (int rc = check_weight(N, K)) return rc;
   if (int rc = check_format(act)) return rc;
-  if (N * mx_steps(K) * kMxStep > kMostOffset)
+  if (N * mx_code_stride(K) * kMxStep > kMostOffset)
     return fail(W4A8_ERR_UNSUPPORTED_SHAPE, "the codes are addressed with 32-bit offsets (N=%lld K=%lld)",
                 (long long)N, (long long)K);
   return W4A8_OK;
@@ -185,21 +249,24 @@ int check_product(int64_t M, int64_t N, int64_t K, int32_t act) {
 // A launch has fewer than 2^32 threads.
 int check_launch(const MxPlan& p, int64_t P, int32_t E, int64_t N) {
   const int64_t tiles = E ? mx_tile_slots(P, E, p.bm) : ceil_div(P, p.bm);
-  const int64_t threads = p.path == kMxTile ? (p.bm == 256 ? 512 : 256) : 64 * p.waves;
+  const int64_t threads = p.path == kMxTile ? 512 : 64 * p.waves;
   if (tiles * ceil_div(N, p.bn) * threads >= (int64_t)1 << 32)
     return fail(W4A8_ERR_UNSUPPORTED_SHAPE, "%lld x %lld outputs in one call", (long long)P, (long long)N);
   return W4A8_OK;
 }
-int check_linear(int64_t M, int64_t N, int64_t K, int32_t act) {
+// The checks of the sizes, and the plan that they give.
+int plan_linear(int64_t M, int64_t N, int64_t K, int32_t act, MxPlan& p) {
   if (int rc = check_product(M, N, K, act)) return rc;
-  return check_launch(mx_plan(M, M, 0, N, K, act), M, 0, N);
+  p = mx_plan(M, M, 0, N, K, act);
+  return check_launch(p, M, 0, N);
 }
-int check_grouped(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act) {
+int plan_grouped(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act, MxPlan& p) {
   if (int rc = check_rows(M)) return rc;
   if (E < 1 || E > kMxMaxGroups) return fail(W4A8_ERR_INVALID_ARG, "E=%d out of [1, %d]", (int)E, kMxMaxGroups);
   if (int rc = check_product(P, N, K, act)) return rc;
   if (N * E > (int64_t)1 << 31) return fail(W4A8_ERR_INVALID_ARG, "N=%lld times E=%d out of range", (long long)N, (int)E);
-  return check_launch(mx_plan(M, P, E, N, K, act), P, E, N);
+  p = mx_plan(M, P, E, N, K, act);
+  return check_launch(p, P, E, N);
 }
 
 size_t value_bytes(int32_t d) { return d == W4A8_F32 ? 4 : 2; }
@@ -232,6 +299,8 @@ hipError_t run(const Call& c, const MxPlan& p, hipStream_t st) {
   a.K = (int)c.K;
   a.G = (int)mx_steps(c.K);
   a.Q = (int)mx_supers(c.K);
+  a.gstride = (int)mx_code_stride(c.K);
+  a.qstride = (int)mx_scale_stride(c.K);
   a.ldx = (int)mx_row_bytes(c.K, c.act);
   a.lds = (int)mx_row_scale_bytes(c.K);
   a.nb = (int)(c.N / 16);
@@ -250,15 +319,16 @@ hipError_t run(const Call& c, const MxPlan& p, hipStream_t st) {
     }
     a.parts = reinterpret_cast<float*>(c.ws + p.parts);
     const MxQuantArgs q{c.x, c.x_dtype == W4A8_F32, c.act, c.rule, c.M, c.K, c.ws + p.codes, c.ws + p.scales};
-    const hipError_t e = launch_mx_rows(q, c.offsets, c.E, c.P, p.bm, const_cast<int*>(a.ntiles),
-                                        const_cast<MxTile*>(a.tiles), st);
+    const MxRowsArgs r{p.path == kMxStream, c.rows, c.offsets, c.E, p.bm, c.P, const_cast<int*>(a.ntiles),
+                       const_cast<MxTile*>(a.tiles)};
+    const hipError_t e = launch_mx_rows(q, r, st);
     if (e != hipSuccess) return e;
   }
   if (p.path == kMxTile) {
     a.strips = (int)ceil_div(c.N, p.bn);
     return launch_mx_tile(a, p, c.act, c.gated, st);
   }
-  a.strips = a.nb / (c.gated ? 2 : 1);
+  a.strips = c.gated ? a.nb / 2 : (int)ceil_div(c.N, p.bn);
   return launch_mx_stream(a, p, c.act, c.gated, st);
 }
 
@@ -343,25 +413,27 @@ int w4a8_mx_unpack_weights(const void* packed, size_t packed_bytes, int64_t N, i
 
 int w4a8_mx_linear_plan(int64_t M, int64_t N, int64_t K, int32_t act, w4a8_mx_plan_t* plan) {
   if (!plan) return fail(W4A8_ERR_INVALID_ARG, "null plan");
-  if (int rc = check_linear(M, N, K, act)) return rc;
-  return fill_plan(mx_plan(M, M, 0, N, K, act), plan);
+  MxPlan p;
+  if (int rc = plan_linear(M, N, K, act, p)) return rc;
+  return fill_plan(p, plan);
 }
 
 size_t w4a8_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t act) {
-  if (check_linear(M, N, K, act)) return 0;
+  MxPlan p;
+  if (plan_linear(M, N, K, act, p)) return 0;
   return (size_t)workspace_bound(M, M, 0, N, K, act);
 }
 
 int w4a8_mx_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, const void* packed,
                    size_t packed_bytes, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
                    size_t workspace_bytes, void* stream) {
-  if (int rc = check_linear(M, N, K, act)) return rc;
+  MxPlan p;
+  if (int rc = plan_linear(M, N, K, act, p)) return rc;
   if (int rc = check_dtype(x_dtype)) return rc;
   if (int rc = check_rule(rule)) return rc;
   const size_t wb = (size_t)mx_weight_bytes(N, K);
   if (packed && packed_bytes < wb)
     return fail(W4A8_ERR_BUFFER_TOO_SMALL, "packed buffer %zu bytes, need %zu", packed_bytes, wb);
-  const MxPlan p = mx_plan(M, M, 0, N, K, act);
   if (!workspace || workspace_bytes < (size_t)p.bytes)
     return fail(W4A8_ERR_BUFFER_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes, (size_t)p.bytes);
   const Span in[] = {{x, (size_t)M * K * value_bytes(x_dtype)}, {packed, wb}};
@@ -376,12 +448,14 @@ int w4a8_mx_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, co
 int w4a8_mx_grouped_linear_plan(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act,
                                 w4a8_mx_plan_t* plan) {
   if (!plan) return fail(W4A8_ERR_INVALID_ARG, "null plan");
-  if (int rc = check_grouped(M, P, E, N, K, act)) return rc;
-  return fill_plan(mx_plan(M, P, E, N, K, act), plan);
+  MxPlan p;
+  if (int rc = plan_grouped(M, P, E, N, K, act, p)) return rc;
+  return fill_plan(p, plan);
 }
 
 size_t w4a8_mx_grouped_linear_workspace_bytes(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act) {
-  if (check_grouped(M, P, E, N, K, act)) return 0;
+  MxPlan p;
+  if (plan_grouped(M, P, E, N, K, act, p)) return 0;
   return (size_t)workspace_bound(M, P, E, N, K, act);
 }
 
@@ -389,7 +463,8 @@ int w4a8_mx_grouped_linear(const void* x, int32_t x_dtype, int32_t act, int32_t 
                            size_t packed_bytes, const int32_t* offsets, const int32_t* rows, int64_t M, int64_t P,
                            int32_t E, int64_t N, int64_t K, int32_t gated, uint16_t* y, void* workspace,
                            size_t workspace_bytes, void* stream) {
-  if (int rc = check_grouped(M, P, E, N, K, act)) return rc;
+  MxPlan p;
+  if (int rc = plan_grouped(M, P, E, N, K, act, p)) return rc;
   if (int rc = check_dtype(x_dtype)) return rc;
   if (int rc = check_rule(rule)) return rc;
   if (gated && N % 32)
@@ -402,7 +477,6 @@ int w4a8_mx_grouped_linear(const void* x, int32_t x_dtype, int32_t act, int32_t 
   const size_t wb = (size_t)mx_weight_bytes(E * N, K);
   if (packed && packed_bytes < wb)
     return fail(W4A8_ERR_BUFFER_TOO_SMALL, "packed buffer %zu bytes, need %zu", packed_bytes, wb);
-  const MxPlan p = mx_plan(M, P, E, N, K, act);
   if (!workspace || workspace_bytes < (size_t)p.bytes)
     return fail(W4A8_ERR_BUFFER_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes, (size_t)p.bytes);
   const Span in[] = {{x, (size_t)M * K * value_bytes(x_dtype)},

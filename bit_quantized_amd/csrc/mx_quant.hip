@@ -134,12 +134,21 @@ __device__ __forceinline__ void list_tiles(const GroupTiles& g, int (&s_head)[kM
   }
 }
 
-// Workgroup (i, m): chunks of row m, past K the zeros that the layout asks
+struct RowPlaces {
+  int ldx, lds;      // rows: strides in bytes
+  int G, Q;          // interleaved: steps and supers of a row
+  const int* rows;   // interleaved: source rows
+  int64_t M;         // of x
+  int64_t first;     // row of the launch's first
+  int chunks;        // of eight inputs that a row is written in
+};
+
+// Workgroup (m, i): chunks of row m, past K the zeros that the layout asks
 // for.  The first workgroup lists the tiles as well.
-template <int FMT, bool F32>
+template <int FMT, bool F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
-rows_kernel(const uint8_t* __restrict__ x, int K, int rule, int ldx, int lds, uint8_t* __restrict__ codes,
-            uint8_t* __restrict__ scales, int wide, GroupTiles g) {
+rows_kernel(const uint8_t* __restrict__ x, int K, int rule, uint8_t* __restrict__ codes,
+            uint8_t* __restrict__ scales, int wide, RowPlaces at, GroupTiles g) {
   __shared__ int s_head[kMxMaxGroups + 1], s_wave[kThreads / 64];
   unsigned item = blockIdx.x;
   if (g.offsets) {
@@ -149,38 +158,57 @@ rows_kernel(const uint8_t* __restrict__ x, int K, int rule, int ldx, int lds, ui
     }
     --item;
   }
-  const int64_t m = item / (unsigned)wide;
+  const int64_t m = at.first + item / (unsigned)wide;
   const int ch = (int)(item % (unsigned)wide) * kThreads + threadIdx.x;
-  if (ch >= lds * 4) return;  // lds * 4 chunks of a row: whole supers of 512 inputs
+  if (ch >= at.chunks) return;
+  int64_t from = m;
+  if (INTERLEAVED && at.rows) {
+    const int r = at.rows[m];
+    from = r >= 0 && r < at.M ? r : -1;
+  }
   MxRaw<F32> r;
   r.clear();
-  if (ch * 8 < K) r.load(x + m * K * (F32 ? 4 : 2), ch * 8);
-  const uint32_t top = dpp_umax_quad(r.top());
-  const int b = mx_scale_byte<FMT>(top, rule);
+  if (ch * 8 < K && from >= 0) r.load(x + from * K * (F32 ? 4 : 2), ch * 8);
+  const int b = mx_scale_byte<FMT>(dpp_umax_quad(r.top()), rule);
   const uint2 c = mx_codes8<FMT, F32>(r, b);
-  const int at = ch * (FMT == kFp4 ? 4 : 8);
-  if (at < ldx) {
+  // block blk of 32 inputs: step g = blk / 4, j = blk % 4
+  const int blk = ch >> 2, j = blk & 3, s = blk >> 2 & 3;
+  uint8_t *to, *scale;
+  if constexpr (INTERLEAVED) {
+    const int64_t b16 = m >> 4;
+    const int row = (int)(m & 15);
+    if (FMT == kFp4)
+      to = codes + (b16 * at.G + (blk >> 2)) * kBlockBytes + (j * 16 + row) * 16 + (ch & 3) * 4;
+    else  // 16-byte chunk ch / 2 of the step's eight
+      to = codes + ((b16 * at.G + (blk >> 2)) * 2 + (ch >> 3 & 1)) * kBlockBytes + ((ch >> 1 & 3) * 16 + row) * 16 +
+           (ch & 1) * 8;
+    if (blk >> 2 >= at.G) to = nullptr;
+    scale = scales + (b16 * at.Q + (blk >> 4)) * kMxScaleBytes + (j * 16 + row) * 4 + s;
+  } else {
+    const int byte = ch * (FMT == kFp4 ? 4 : 8);
+    to = byte < at.ldx ? codes + m * at.ldx + byte : nullptr;
+    scale = scales + m * at.lds + (blk & ~15) + 4 * j + s;
+  }
+  if (to) {
     if constexpr (FMT == kFp4)
-      *reinterpret_cast<uint32_t*>(codes + m * ldx + at) = c.x;
+      *reinterpret_cast<uint32_t*>(to) = c.x;
     else
-      *reinterpret_cast<uint2*>(codes + m * ldx + at) = c;
+      *reinterpret_cast<uint2*>(to) = c;
   }
-  if ((ch & 3) == 0) {  // block 16 q + 4 s + j at byte 16 q + 4 j + s
-    const int blk = ch >> 2;
-    scales[m * lds + (blk & ~15) + 4 * (blk & 3) + ((blk >> 2) & 3)] = (uint8_t)b;
-  }
+  if ((ch & 3) == 0) *scale = (uint8_t)b;
 }
 
 // ------------------------------------------------------------ weight layout
 
-// Thread: 16 bytes of a codes block (lane L of block (nb, g)).
+// Thread: 16 bytes of a codes block (lane L of block (nb, g)); blocks that only
+// fill the stride are zero.
 __global__ void __launch_bounds__(kThreads)
-pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t units, int K, int G, uint8_t* __restrict__ packed) {
+pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t units, int K, int stride, uint8_t* __restrict__ packed) {
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units) return;
   const int L = (int)(t & 63), j = L >> 4, c = L & 15;
-  const int64_t blk = t >> 6, nb = blk / G;
-  const int g = (int)(blk % G), k = g * kMxStep + j * kMxBlock;
+  const int64_t blk = t >> 6, nb = blk / stride;
+  const int g = (int)(blk % stride), k = g * kMxStep + j * kMxBlock;
   v4u_rows v = {0, 0, 0, 0};
   if (k < K) v = *reinterpret_cast<const v4u_rows*>(codes + ((nb * 16 + c) * K + k) / 2);
   reinterpret_cast<v4u_rows*>(packed)[t] = v;
@@ -188,14 +216,14 @@ pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t units, int K, int G
 // Thread: the four scale bytes of lane L of super (nb, q); the last 256
 // threads clear the 1024 bytes behind the planes.
 __global__ void __launch_bounds__(kThreads)
-pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t units, int K, int Q, uint8_t* __restrict__ plane) {
+pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t units, int K, int stride, uint8_t* __restrict__ plane) {
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units + 256) return;
   uint32_t v = 0;
   if (t < units) {
     const int L = (int)(t & 63), j = L >> 4, c = L & 15;
-    const int64_t sup = t >> 6, nb = sup / Q;
-    const int q = (int)(sup % Q), per = K / kMxBlock;
+    const int64_t sup = t >> 6, nb = sup / stride;
+    const int q = (int)(sup % stride), per = K / kMxBlock;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int b = (4 * q + s) * 4 + j;
@@ -205,22 +233,22 @@ pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t units, int K, int
   reinterpret_cast<uint32_t*>(plane)[t] = v;
 }
 __global__ void __launch_bounds__(kThreads)
-unpack_codes_kernel(const uint8_t* __restrict__ packed, int64_t units, int K, int G, uint8_t* __restrict__ codes) {
+unpack_codes_kernel(const uint8_t* __restrict__ packed, int64_t units, int K, int stride, uint8_t* __restrict__ codes) {
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units) return;
   const int L = (int)(t & 63), j = L >> 4, c = L & 15;
-  const int64_t blk = t >> 6, nb = blk / G;
-  const int k = (int)(blk % G) * kMxStep + j * kMxBlock;
+  const int64_t blk = t >> 6, nb = blk / stride;
+  const int k = (int)(blk % stride) * kMxStep + j * kMxBlock;
   if (k < K)
     *reinterpret_cast<v4u_rows*>(codes + ((nb * 16 + c) * K + k) / 2) = reinterpret_cast<const v4u_rows*>(packed)[t];
 }
 __global__ void __launch_bounds__(kThreads)
-unpack_scales_kernel(const uint8_t* __restrict__ plane, int64_t units, int K, int Q, uint8_t* __restrict__ scales) {
+unpack_scales_kernel(const uint8_t* __restrict__ plane, int64_t units, int K, int stride, uint8_t* __restrict__ scales) {
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units) return;
   const int L = (int)(t & 63), j = L >> 4, c = L & 15;
-  const int64_t sup = t >> 6, nb = sup / Q;
-  const int q = (int)(sup % Q), per = K / kMxBlock;
+  const int64_t sup = t >> 6, nb = sup / stride;
+  const int q = (int)(sup % stride), per = K / kMxBlock;
   const uint32_t v = reinterpret_cast<const uint32_t*>(plane)[t];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -277,22 +305,37 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int fm
   return hipGetLastError();
 }
 
-hipError_t launch_mx_rows(const MxQuantArgs& a, const int* offsets, int E, int64_t P, int bm, int* ntiles,
-                          MxTile* tiles, hipStream_t st) {
-  const int ldx = (int)mx_row_bytes(a.K, a.fmt), lds = (int)mx_row_scale_bytes(a.K);
-  const int wide = (lds * 4 + kThreads - 1) / kThreads;
-  const GroupTiles list{offsets, E, bm, offsets ? (int)mx_tile_slots(P, E, bm) : 0, P, ntiles, tiles};
+hipError_t launch_mx_rows(const MxQuantArgs& a, const MxRowsArgs& r, hipStream_t st) {
+  RowPlaces at{};
+  at.ldx = (int)mx_row_bytes(a.K, a.fmt);
+  at.lds = (int)mx_row_scale_bytes(a.K);
+  at.G = (int)mx_steps(a.K);
+  at.Q = (int)mx_supers(a.K);
+  at.rows = r.rows;
+  at.M = a.M;
+  // whole supers; of the other layout the stride of the scales, which the codes' lies in
+  at.chunks = r.interleaved ? at.Q * 64 : at.lds * 4;
+  const int64_t rows = r.interleaved ? r.P : a.M;
+  const int wide = (at.chunks + kThreads - 1) / kThreads;
+  const GroupTiles list{r.offsets, r.E, r.bm, r.offsets ? (int)mx_tile_slots(r.P, r.E, r.bm) : 0, r.P, r.ntiles,
+                        r.tiles};
   constexpr int64_t kMostItems = (int64_t)1 << 23;  // workgroups of one launch
   const int64_t pass = kMostItems / wide;
-  for (int64_t m = 0; m < a.M; m += pass) {
-    const int64_t n = a.M - m < pass ? a.M - m : pass;
+  for (int64_t m = 0; m < rows; m += pass) {
+    const int64_t n = rows - m < pass ? rows - m : pass;
     GroupTiles g = list;
     if (m) g.offsets = nullptr;  // listed by the first launch
+    at.first = m;
+    const dim3 grid((unsigned)(n * wide + (g.offsets ? 1 : 0)));
     typed(a.fmt, a.f32, [&](auto fmt, auto f32) {
-      hipLaunchKernelGGL((rows_kernel<decltype(fmt)::value, decltype(f32)::value>),
-                         dim3((unsigned)(n * wide + (g.offsets ? 1 : 0))), dim3(kThreads), 0, st,
-                         static_cast<const uint8_t*>(a.x) + m * a.K * (a.f32 ? 4 : 2), (int)a.K, a.rule, ldx, lds,
-                         a.codes + m * ldx, a.scales + m * lds, wide, g);
+      constexpr int F = decltype(fmt)::value;
+      constexpr bool W = decltype(f32)::value;
+      if (r.interleaved)
+        hipLaunchKernelGGL((rows_kernel<F, W, true>), grid, dim3(kThreads), 0, st,
+                           static_cast<const uint8_t*>(a.x), (int)a.K, a.rule, a.codes, a.scales, wide, at, g);
+      else
+        hipLaunchKernelGGL((rows_kernel<F, W, false>), grid, dim3(kThreads), 0, st,
+                           static_cast<const uint8_t*>(a.x), (int)a.K, a.rule, a.codes, a.scales, wide, at, g);
     });
   }
   return hipGetLastError();
@@ -300,21 +343,21 @@ hipError_t launch_mx_rows(const MxQuantArgs& a, const int* offsets, int E, int64
 
 hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K, uint8_t* packed,
                           hipStream_t st) {
-  const int G = (int)mx_steps(K), Q = (int)mx_supers(K);
-  const int64_t uc = N / 16 * G * 64, us = N / 16 * Q * 64;
-  hipLaunchKernelGGL(pack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, codes, uc, (int)K, G, packed);
-  hipLaunchKernelGGL(pack_scales_kernel, dim3(blocks_of(us + 256)), dim3(kThreads), 0, st, scales, us, (int)K, Q,
+  const int cs = (int)mx_code_stride(K), ss = (int)mx_scale_stride(K);
+  const int64_t uc = N / 16 * cs * 64, us = N / 16 * ss * 64;
+  hipLaunchKernelGGL(pack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, codes, uc, (int)K, cs, packed);
+  hipLaunchKernelGGL(pack_scales_kernel, dim3(blocks_of(us + 256)), dim3(kThreads), 0, st, scales, us, (int)K, ss,
                      packed + mx_scales_offset(N, K));
   return hipGetLastError();
 }
 
 hipError_t launch_mx_unpack(const uint8_t* packed, int64_t N, int64_t K, uint8_t* codes, uint8_t* scales,
                             hipStream_t st) {
-  const int G = (int)mx_steps(K), Q = (int)mx_supers(K);
-  const int64_t uc = N / 16 * G * 64, us = N / 16 * Q * 64;
-  hipLaunchKernelGGL(unpack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, packed, uc, (int)K, G, codes);
+  const int cs = (int)mx_code_stride(K), ss = (int)mx_scale_stride(K);
+  const int64_t uc = N / 16 * cs * 64, us = N / 16 * ss * 64;
+  hipLaunchKernelGGL(unpack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, packed, uc, (int)K, cs, codes);
   hipLaunchKernelGGL(unpack_scales_kernel, dim3(blocks_of(us)), dim3(kThreads), 0, st,
-                     packed + mx_scales_offset(N, K), us, (int)K, Q, scales);
+                     packed + mx_scales_offset(N, K), us, (int)K, ss, scales);
   return hipGetLastError();
 }
 

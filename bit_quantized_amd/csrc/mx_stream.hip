@@ -1,9 +1,9 @@
 // Products of a few rows with a microscaled 4-bit weight: one pass over the
 // weight, bound by its stream from memory.
 //
-// A workgroup has one 16-channel block of one group (two with the gated
-// activation: gates and values) and all of the inputs, dealt to its wavefronts
-// in supers of 512 inputs.  A wavefront's load of a code block is 1 KiB of
+// A workgroup has one or two 16-channel blocks of one group (with the gated
+// activation one of gates and one of values) and all of the inputs, dealt to
+// its wavefronts in supers of 512 inputs.  A wavefront's load of a code block is 1 KiB of
 // consecutive bytes and is the matrix core operand as it stands: nothing is
 // unpacked, and the scales of four steps are one register.  Code blocks are
 // loaded four steps ahead of their use.  The wavefronts' sums meet in LDS and
@@ -94,8 +94,8 @@ __device__ __forceinline__ int64_t source_row(const MxArgs& a, int p) {
   return r >= 0 && r < a.M ? r : -1;
 }
 
-template <int FMT, int MT, int RAW, int NC>
-__global__ void __launch_bounds__(64 * kMaxWaves)
+template <int FMT, int MT, int RAW, int NC, bool GATED>
+__global__ void __launch_bounds__(64 * (MT > 1 ? 8 : kMaxWaves))
 mx_stream_kernel(const MxArgs a) {
   constexpr int kUnits = FMT == kFp4 ? 1 : 2;  // 16-byte units of a lane's row operand
   constexpr int kStepBytes = FMT == kFp4 ? 64 : 128;
@@ -108,9 +108,9 @@ mx_stream_kernel(const MxArgs a) {
 
   int nb[NC];
 #pragma unroll
-  for (int n = 0; n < NC; ++n) nb[n] = sp.strip + n * (a.nb / NC);
-  const uint8_t* wc = a.codes + (int64_t)sp.group * a.nb * a.G * kBlockBytes + lane * 16;
-  const uint8_t* ws = a.scales + (int64_t)sp.group * a.nb * a.Q * kMxScaleBytes + lane * 4;
+  for (int n = 0; n < NC; ++n) nb[n] = GATED ? sp.strip + n * (a.nb / 2) : min(sp.strip * NC + n, a.nb - 1);
+  const uint8_t* wc = a.codes + (int64_t)sp.group * a.nb * a.gstride * kBlockBytes + lane * 16;
+  const uint8_t* ws = a.scales + (int64_t)sp.group * a.nb * a.qstride * kMxScaleBytes + lane * 4;
 
   // This lane's row of each 16: past the last, the last one again.
   const uint8_t* xc[MT];
@@ -118,9 +118,9 @@ mx_stream_kernel(const MxArgs a) {
   if constexpr (!RAW) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int64_t r = max(source_row(a, sp.first + min(m * 16 + c, sp.rows - 1)), (int64_t)0);
-      xc[m] = a.qx + r * a.ldx + j * 16;
-      xs[m] = a.qs + r * a.lds + j * 4;
+      const int r = sp.first + min(m * 16 + c, sp.rows - 1);
+      xc[m] = a.qx + (int64_t)(r >> 4) * a.G * kUnits * kBlockBytes + (j * 16 + (r & 15)) * 16;
+      xs[m] = a.qs + (int64_t)(r >> 4) * a.Q * kMxScaleBytes + (j * 16 + (r & 15)) * 4;
     }
   }
 
@@ -131,7 +131,7 @@ mx_stream_kernel(const MxArgs a) {
 #pragma unroll
     for (int n = 0; n < NC; ++n)
       w[s][n] = __builtin_nontemporal_load(
-          reinterpret_cast<const v4i*>(wc + ((int64_t)nb[n] * a.G + g) * kBlockBytes));
+          reinterpret_cast<const v4i*>(wc + ((int64_t)nb[n] * a.gstride + g) * kBlockBytes));
   };
   auto load_row = [&](int s, int q) __attribute__((always_inline)) {
     const int g = min(4 * q + s, a.G - 1);
@@ -143,14 +143,14 @@ mx_stream_kernel(const MxArgs a) {
           const int r = min(c, sp.rows - 1);  // (rows of a raw tile: at most 16)
           x[s][m][u] = *reinterpret_cast<const v4i*>(lds + r * a.ldx + g * kStepBytes + u * 64 + j * 16);
         } else {
-          x[s][m][u] = *reinterpret_cast<const v4i*>(xc[m] + (int64_t)g * kStepBytes + u * 64);
+          x[s][m][u] = *reinterpret_cast<const v4i*>(xc[m] + (int64_t)(g * kUnits + u) * kBlockBytes);
         }
       }
   };
   auto load_weight_scales = [&](int q, int (&d)[NC]) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < NC; ++n)
-      d[n] = *reinterpret_cast<const int*>(ws + ((int64_t)nb[n] * a.Q + q) * kMxScaleBytes);
+      d[n] = *reinterpret_cast<const int*>(ws + ((int64_t)nb[n] * a.qstride + q) * kMxScaleBytes);
   };
   auto load_row_scales = [&](int q, int (&d)[MT]) __attribute__((always_inline)) {
 #pragma unroll
@@ -159,7 +159,7 @@ mx_stream_kernel(const MxArgs a) {
         const int r = min(c, sp.rows - 1);
         d[m] = *reinterpret_cast<const int*>(lds + sp.rows * a.ldx + r * a.lds + q * kMxRowScale + j * 4);
       } else {
-        d[m] = *reinterpret_cast<const int*>(xs[m] + q * kMxRowScale);
+        d[m] = *reinterpret_cast<const int*>(xs[m] + (int64_t)q * kMxScaleBytes);
       }
     }
   };
@@ -274,52 +274,63 @@ mx_stream_kernel(const MxArgs a) {
       for (int n = 0; n < NC; ++n) red[(wave * kTiles + m * NC + n) * 64 + lane] = acc[m][n];
     __syncthreads();
   }
-  const int width = a.nb * 16 / NC;
-  for (int m = wave; m < MT; m += waves) {
-    v4f_mx v[NC];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
+  constexpr int kOut = GATED ? 1 : NC;
+  const int width = a.nb * (GATED ? 8 : 16);
+  for (int i = wave; i < MT * kOut; i += waves) {  // (only one wavefront: all of them)
+    const int m = i / kOut, n0 = i % kOut;
+    auto sum = [&](int n) __attribute__((always_inline)) {
+      v4f_mx v = {0.f, 0.f, 0.f, 0.f};
       if (waves > 1) {
-        v[n] = red[(m * NC + n) * 64 + lane];
-        for (int i = 1; i < waves; ++i) v[n] += red[(i * kTiles + m * NC + n) * 64 + lane];
+        v = red[(m * NC + n) * 64 + lane];
+        for (int k = 1; k < waves; ++k) v += red[(k * kTiles + m * NC + n) * 64 + lane];
       } else {
-        v[n] = acc[MT > 1 ? 0 : m][n];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          if (i == m) v[n] = acc[i][n];
+        for (int t = 0; t < kTiles; ++t)
+          if (t == m * NC + n) v = acc[t / NC][t % NC];
       }
-    }
-    const int at = m * 16 + c;
-    if (at >= sp.rows) continue;
-    const int p = sp.first + at;
-    v4f_mx out = v[0];
-    if constexpr (NC == 2) {
+      return v;
+    };
+    v4f_mx out = sum(n0);
+    if constexpr (GATED) {
+      const v4f_mx value = sum(1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) out[i] = silu_mul(v[0][i], v[1][i]);
+      for (int e = 0; e < 4; ++e) out[e] = silu_mul(out[e], value[e]);
     }
+    const int at = m * 16 + c, block = sp.strip * kOut + n0;
+    if (at >= sp.rows || block * 16 >= width) continue;
+    const int p = sp.first + at;
     uint2 bits = mx_bf16x4(out);
-    if (a.rows && source_row(a, p) < 0) bits = uint2{0u, 0u};
-    *reinterpret_cast<uint2*>(a.y + (int64_t)p * width + sp.strip * 16 + 4 * j) = bits;
+    if (RAW && a.rows && source_row(a, p) < 0) bits = uint2{0u, 0u};
+    *reinterpret_cast<uint2*>(a.y + (int64_t)p * width + block * 16 + 4 * j) = bits;
   }
 }
 
-template <int FMT, int MT, int RAW>
-hipError_t launch_one(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
-  const size_t sums = p.waves > 1 ? (size_t)p.waves * MT * (gated ? 2 : 1) * 1024 : 0;
+template <int FMT, int MT, int RAW, int NC, bool GATED>
+hipError_t launch_one(const MxArgs& a, const MxPlan& p, unsigned blocks, hipStream_t st) {
+  const size_t sums = p.waves > 1 ? (size_t)p.waves * MT * NC * 1024 : 0;
   const size_t rows = RAW ? (size_t)(a.P < a.bm ? a.P : a.bm) * (a.ldx + a.lds) : 0;
   const size_t lds = sums > rows ? sums : rows;
-  if (gated)
-    hipLaunchKernelGGL((mx_stream_kernel<FMT, MT, RAW, 2>), dim3(blocks), dim3(64 * p.waves), lds, st, a);
-  else
-    hipLaunchKernelGGL((mx_stream_kernel<FMT, MT, RAW, 1>), dim3(blocks), dim3(64 * p.waves), lds, st, a);
+  hipLaunchKernelGGL((mx_stream_kernel<FMT, MT, RAW, NC, GATED>), dim3(blocks), dim3(64 * p.waves), lds, st, a);
   return hipGetLastError();
+}
+
+template <int FMT, int MT, int RAW>
+hipError_t launch_cols(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
+  if (gated) return launch_one<FMT, MT, RAW, 2, true>(a, p, blocks, st);
+  if (p.bn == 32) return launch_one<FMT, MT, RAW, 2, false>(a, p, blocks, st);
+  return launch_one<FMT, MT, RAW, 1, false>(a, p, blocks, st);
 }
 
 template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
   if (p.path == kMxToken)
-    return a.f32 ? launch_one<FMT, 1, 2>(a, p, gated, blocks, st) : launch_one<FMT, 1, 1>(a, p, gated, blocks, st);
-  return launch_one<FMT, 1, 0>(a, p, gated, blocks, st);
+    return a.f32 ? launch_cols<FMT, 1, 2>(a, p, gated, blocks, st) : launch_cols<FMT, 1, 1>(a, p, gated, blocks, st);
+  switch (p.bm) {
+    case 16: return launch_cols<FMT, 1, 0>(a, p, gated, blocks, st);
+    case 32: return launch_cols<FMT, 2, 0>(a, p, gated, blocks, st);
+    case 48: return launch_cols<FMT, 3, 0>(a, p, gated, blocks, st);
+    default: return launch_cols<FMT, 4, 0>(a, p, gated, blocks, st);
+  }
 }
 
 }  // namespace

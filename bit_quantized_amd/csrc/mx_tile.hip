@@ -21,6 +21,8 @@
 namespace w4a8 {
 namespace {
 
+constexpr int kBand = 8;
+
 struct Spot {
   int group, first, rows, strip;
 };
@@ -30,10 +32,14 @@ struct Spot {
 __device__ __forceinline__ bool locate(const MxArgs& a, Spot& s) {
   const int b = blockIdx.x;
   if (!a.offsets) {
+    // bands of kBand row tiles, strip by strip: the 32 compute units of an XCD
+    // work on 8 x 4 tiles, whose rows and channels they share in its L2
     const int tiles = (int)((a.P + a.bm - 1) / a.bm);
     const int at = xcd_run(b, tiles * a.strips);
-    const int t = at % tiles;
-    s.strip = at / tiles;
+    const int band = at / (kBand * a.strips), first = band * kBand;
+    const int high = min(kBand, tiles - first), local = at - first * a.strips;
+    const int t = first + local % high;
+    s.strip = local / high;
     s.group = 0;
     s.first = t * a.bm;
     s.rows = (int)(a.P - s.first < a.bm ? a.P - s.first : a.bm);
@@ -128,9 +134,9 @@ mx_tile_kernel(const MxArgs a) {
   // code blocks and of scales
   const int64_t base = a.rows ? 0 : sp.first;
   const int64_t left = a.rows ? a.M : sp.rows;
-  const int64_t code_bytes = (int64_t)a.nb * a.G * kBlockBytes + 1024;
+  const int64_t code_bytes = (int64_t)a.nb * a.gstride * kBlockBytes + 1024;
   LdsSource rx = lds_source(a.qx + base * a.ldx, left * a.ldx);
-  LdsSource rw = lds_source(a.codes + (int64_t)sp.group * a.nb * a.G * kBlockBytes, code_bytes);
+  LdsSource rw = lds_source(a.codes + (int64_t)sp.group * a.nb * a.gstride * kBlockBytes, code_bytes);
   auto source = [&](int r) __attribute__((always_inline)) {  // of row r of the tile, from base
     const int i = min(r, sp.rows - 1);
     return a.rows ? max(source_row(a, sp.first + i), 0) : i;
@@ -149,16 +155,16 @@ mx_tile_kernel(const MxArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < kCodeLoads; ++i)
-    ow[i] = (uint32_t)block_of(wave * kCodeLoads + i) * a.G * kBlockBytes + lane * 16;
+    ow[i] = (uint32_t)block_of(wave * kCodeLoads + i) * a.gstride * kBlockBytes + lane * 16;
   // One KiB of scales each, of rows or of blocks (wavefronts past the last KiB
   // load it as well).
   const int scale_kib = min(wave, S::kScaleKiB - 1);
   const bool row_scales = scale_kib < S::kRows / 64;
-  const LdsSource rs = lds_source(row_scales ? a.qs + base * a.lds : a.scales + (int64_t)sp.group * a.nb * a.Q * kMxScaleBytes,
-                                  row_scales ? left * a.lds : (int64_t)a.nb * a.Q * kMxScaleBytes);
+  const LdsSource rs = lds_source(row_scales ? a.qs + base * a.lds : a.scales + (int64_t)sp.group * a.nb * a.qstride * kMxScaleBytes,
+                                  row_scales ? left * a.lds : (int64_t)a.nb * a.qstride * kMxScaleBytes);
   const int scale_step = row_scales ? kMxRowScale : kMxScaleBytes;
   const uint32_t os = row_scales ? (uint32_t)source(scale_kib * 64 + lane) * a.lds
-                                 : (uint32_t)block_of((scale_kib - S::kRows / 64) * 4 + (lane >> 4)) * a.Q * kMxScaleBytes +
+                                 : (uint32_t)block_of((scale_kib - S::kRows / 64) * 4 + (lane >> 4)) * a.qstride * kMxScaleBytes +
                                        (lane & 15) * 16;
   const int lds0 = uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
   auto scales_at = [&](int buf) __attribute__((always_inline)) {
@@ -358,9 +364,11 @@ hipError_t launch_shape(const MxArgs& a, const MxPlan& p, bool gated, unsigned b
 
 template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
-  if (p.bm == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
-  if (p.bm == 128) return launch_shape<FMT, 2, 2, 2, 2>(a, p, gated, blocks, st);
-  return launch_shape<FMT, 2, 2, 1, 2>(a, p, gated, blocks, st);
+  if (p.bm == 256 && p.bn == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
+  if (p.bm == 128 && p.bn == 256) return launch_shape<FMT, 2, 4, 2, 2>(a, p, gated, blocks, st);
+  if (p.bm == 128 && p.bn == 128) return launch_shape<FMT, 2, 2, 2, 2>(a, p, gated, blocks, st);
+  if (p.bm == 64 && p.bn == 128) return launch_shape<FMT, 2, 2, 1, 2>(a, p, gated, blocks, st);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace

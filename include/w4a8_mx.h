@@ -65,7 +65,8 @@ int w4a8_mx_dequant(const uint8_t* codes, const uint8_t* scales, int32_t format,
  *   codes   device uint8 [N][K / 2], scales device uint8 [N][K / 32]: as
  *           w4a8_mx_quant writes them and checkpoints hold them
  *   packed  device buffer of w4a8_mx_weight_bytes(N, K) bytes
- * Format (G = K / 128 rounded up, NB = N / 16, Q = G / 4 rounded up):
+ * Format (NB = N / 16; G = K / 128 rounded up and Q = G / 4 rounded up, each
+ * made odd by adding 1 if it is even):
  *   codes,  1024 NB G bytes at offset 0: block (nb, g) at (nb G + g) 1024;
  *     lane L = 16 j + c (j = 0..3, c = 0..15) owns bytes [16 L, 16 L + 16):
  *     the codes of channel 16 nb + c, inputs [128 g + 32 j, 128 g + 32 j + 32);

@@ -136,7 +136,7 @@ def test_pack_round_trip_and_layout(w4, N, K):
     back = w4.mx_unpack_weights(w)
     assert torch.equal(back.codes.cpu(), ref.pack4(q)) and torch.equal(back.scales.cpu(), s)
     buf = w.buf.cpu()
-    G, Q = -(-K // 128), -(-K // 512)
+    G, Q = -(-K // 128) | 1, -(-K // 512) | 1
     assert buf.numel() == N // 16 * (G * 1024 + Q * 256) + 1024
     full = torch.zeros(N, G * 128, dtype=torch.uint8)
     full[:, :K] = q
@@ -188,9 +188,28 @@ def test_linear_of_float_rows_and_ceil(w4, act, M, N, K):
 
 
 @pytest.mark.parametrize("act", FMTS)
-@pytest.mark.parametrize("M,N,K", [(2048, 8192, 1056), (1030, 16400, 288)])
-def test_linear_of_large_tiles(w4, act, M, N, K):
-    assert w4.mx_linear_plan(M, N, K, act).tile_rows == 256
+@pytest.mark.parametrize("M,N,K,tile", [
+    (2048, 8192, 1056, (256, 256)), (1030, 12816, 288, (256, 256)), (300, 18960, 416, (128, 256)),
+    (517, 4112, 672, (128, 128)), (200, 8208, 288, (128, 128)), (150, 4112, 288, (64, 128)), (65, 4112, 672, (64, 128))])
+def test_linear_of_each_tile(w4, act, M, N, K, tile):
+    p = w4.mx_linear_plan(M, N, K, act)
+    assert (p.path, p.tile_rows, p.tile_cols, p.ksplit) == (w4.MX_TILE, *tile, 1)
+    linear_case(w4, M, N, K, act, "floor", "bf16", True)
+
+
+@pytest.mark.parametrize("act", FMTS)
+@pytest.mark.parametrize("M,N,K", [(33, 256, 18944), (100, 144, 4128), (513, 528, 16416), (70, 2064, 9248)])
+def test_linear_in_slices(w4, act, M, N, K):
+    assert w4.mx_linear_plan(M, N, K, act).ksplit > 1
+    linear_case(w4, M, N, K, act, "floor", "bf16", True)
+
+
+@pytest.mark.parametrize("act", FMTS)
+@pytest.mark.parametrize("M,N,K,cols", [(16, 4112, 2912, 16), (17, 528, 1056, 16), (40, 4112, 544, 16),
+                                        (64, 4096, 1024, 16), (48, 8208, 160, 32), (60, 8208, 160, 32)])
+def test_linear_streamed(w4, act, M, N, K, cols):
+    p = w4.mx_linear_plan(M, N, K, act)
+    assert (p.path, p.tile_rows, p.tile_cols) == (w4.MX_STREAM, -(-M // 16) * 16, cols)
     linear_case(w4, M, N, K, act, "floor", "bf16", True)
 
 
