@@ -811,7 +811,7 @@ class MxTensor:
         if self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
             raise TypeError("codes and scales must be uint8")
         M, K = self.shape
-        if tuple(self.codes.shape) != (M, K // 2 if self.format == "fp4" else K):
+        if self.codes.shape != (M, K // 2 if self.format == "fp4" else K):
             raise ValueError(f"codes {tuple(self.codes.shape)} and scales {tuple(self.scales.shape)} do "
                              f"not fit together")
 
@@ -835,7 +835,8 @@ def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
         scales = x.new_empty((M, K // MX_BLOCK), dtype=torch.uint8)
     elif scales.dtype != torch.uint8 or scales.shape != (M, K // MX_BLOCK):
         raise TypeError(f"scales must be uint8 [{M}][{K // MX_BLOCK}]")
-    _check(lib.w4a8_mx_quant(_p(x), dt, M, K, fmt, ru, _p(codes), _p(scales), _stream(x.device)))
+    _check(lib.w4a8_mx_quant(x.data_ptr(), dt, M, K, fmt, ru, codes.data_ptr(), scales.data_ptr(),
+                             _stream(x.device)))
     return MxTensor(codes, scales, format)
 
 
@@ -844,13 +845,14 @@ def mx_dequant(t: MxTensor, dtype: torch.dtype = torch.bfloat16,
     """The values that codes and scales stand for, bfloat16 or float32 [M][K]."""
     lib = load()
     t.check()
-    _need_on(t.codes.get_device(), t.codes, t.scales, out)
+    codes, scales = t.codes, t.scales
+    _need_on(codes.get_device(), codes, scales, out)
     M, K = t.shape
     if out is None:
-        out = t.codes.new_empty((M, K), dtype=dtype)
+        out = codes.new_empty((M, K), dtype=dtype)
     elif out.dtype != dtype or out.shape != (M, K):
         raise TypeError(f"out must be {dtype} [{M}][{K}]")
-    _check(lib.w4a8_mx_dequant(_p(t.codes), _p(t.scales), MX_FORMATS[t.format], M, K, _p(out),
+    _check(lib.w4a8_mx_dequant(codes.data_ptr(), scales.data_ptr(), MX_FORMATS[t.format], M, K, out.data_ptr(),
                                _act_dtype(out), _stream(out.device)))
     return out
 

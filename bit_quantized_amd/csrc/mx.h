@@ -213,6 +213,21 @@ __device__ __forceinline__ void mx_run(const int* offsets, int e, int64_t P, int
   hi = max(min(max(offsets[e + 1], 0), (int)P), lo);
 }
 
+// Sum of v over this lane and those below it, by DPP moves: prefix sums of
+// each row of 16, then the rows' totals.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add_step(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_prefix_sum(int v) {
+  v = dpp_add_step<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v = dpp_add_step<0x112, 0xF>(v);
+  v = dpp_add_step<0x114, 0xF>(v);
+  v = dpp_add_step<0x118, 0xF>(v);
+  v = dpp_add_step<0x142, 0xA>(v);  // row_bcast 15: lane 15 of a row to the next row (1 and 3)
+  return dpp_add_step<0x143, 0xC>(v);  // row_bcast 31: lane 31 to rows 2 and 3
+}
+
 // Operand of a matrix core product from loaded registers.
 __device__ __forceinline__ v8i_mx mx_wide(v4i a) {
   return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);

@@ -86,51 +86,50 @@ struct GroupTiles {
 
 // The tiles of every group, by one workgroup: prefix sums of the groups' tile
 // counts (four groups a thread), then a thread a tile.
-__device__ __forceinline__ void list_tiles(const GroupTiles& g, int (&s_head)[kMxMaxGroups + 1], int* s_wave) {
+struct ListLds {
+  int head[kMxMaxGroups + 1], lo[kMxMaxGroups], hi[kMxMaxGroups], wave[kThreads / 64];
+};
+__device__ __forceinline__ void list_tiles(const GroupTiles& g, ListLds& s) {
   constexpr int kPer = kMxMaxGroups / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int n[kPer], own = 0;
+  int n[kPer], lo[kPer], hi[kPer], own = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    n[i] = 0;
-    if (e < g.E) {
-      int lo, hi;
-      mx_run(g.offsets, e, g.P, lo, hi);
-      n[i] = (hi - lo + g.bm - 1) / g.bm;
-    }
-    own += n[i];
+    lo[i] = hi[i] = 0;
+    if (tid * kPer + i < g.E) mx_run(g.offsets, tid * kPer + i, g.P, lo[i], hi[i]);
   }
-  int sum = own;
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
+  for (int i = 0; i < kPer; ++i) {
+    n[i] = (hi[i] - lo[i] + g.bm - 1) / g.bm;
+    own += n[i];
+    if (tid * kPer + i < g.E) {
+      s.lo[tid * kPer + i] = lo[i];
+      s.hi[tid * kPer + i] = hi[i];
+    }
   }
-  if (lane == 63) s_wave[wave] = sum;
+  const int sum = wave_prefix_sum(own);
+  if (lane == 63) s.wave[wave] = sum;
   __syncthreads();
   int base = sum - own;
-  for (int w = 0; w < wave; ++w) base += s_wave[w];
+  for (int w = 0; w < wave; ++w) base += s.wave[w];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (tid * kPer + i <= g.E) s_head[tid * kPer + i] = base;
+    if (tid * kPer + i <= g.E) s.head[tid * kPer + i] = base;
     base += n[i];
   }
-  if (tid == kThreads - 1 && g.E == kMxMaxGroups) s_head[kMxMaxGroups] = base;
+  if (tid == kThreads - 1 && g.E == kMxMaxGroups) s.head[kMxMaxGroups] = base;
   __syncthreads();
   // (offsets that do not ascend can name more tiles than there are slots)
-  const int total = min(s_head[g.E], g.slots);
+  const int total = min(s.head[g.E], g.slots);
   if (tid == 0) g.ntiles[0] = total;
   for (int t = tid; t < total; t += kThreads) {
     int a = 0, b = g.E;  // the last group whose first tile is at most t
     while (b - a > 1) {
       const int m = (a + b) / 2;
-      if (s_head[m] <= t) a = m; else b = m;
+      if (s.head[m] <= t) a = m; else b = m;
     }
-    int lo, hi;
-    mx_run(g.offsets, a, g.P, lo, hi);
-    const int at = t - s_head[a], first = lo + at * g.bm;
-    g.tiles[t] = MxTile{a, first, min(g.bm, hi - first), s_head[a], s_head[a + 1] - s_head[a], {0, 0, 0}};
+    const int first = s.lo[a] + (t - s.head[a]) * g.bm;
+    g.tiles[t] = MxTile{a, first, min(g.bm, s.hi[a] - first), s.head[a], s.head[a + 1] - s.head[a], {0, 0, 0}};
   }
 }
 
@@ -149,11 +148,11 @@ template <int FMT, bool F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
 rows_kernel(const uint8_t* __restrict__ x, int K, int rule, uint8_t* __restrict__ codes,
             uint8_t* __restrict__ scales, int wide, RowPlaces at, GroupTiles g) {
-  __shared__ int s_head[kMxMaxGroups + 1], s_wave[kThreads / 64];
+  __shared__ ListLds list;
   unsigned item = blockIdx.x;
   if (g.offsets) {
     if (item == 0) {
-      list_tiles(g, s_head, s_wave);
+      list_tiles(g, list);
       return;
     }
     --item;

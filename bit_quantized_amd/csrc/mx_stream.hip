@@ -27,31 +27,32 @@ struct Spot {
   int group, first, rows, strip;
 };
 
-// Tile t of bm rows, found from the offsets by every wavefront for itself.
+// Tile t of bm rows, found from the offsets by every wavefront for itself, 128
+// groups at a time.
 __device__ __forceinline__ bool find_tile(const MxArgs& a, int t, Spot& s) {
   const int lane = threadIdx.x & 63;
   int before = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 64) {
-    int lo = 0, hi = 0;
-    if (e0 + lane < a.E) mx_run(a.offsets, e0 + lane, a.P, lo, hi);
-    const int n = (hi - lo + a.bm - 1) / a.bm;
-    int sum = n;
+  for (int e0 = 0; e0 < a.E; e0 += 128) {
+    int lo[2] = {0, 0}, hi[2] = {0, 0};
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(sum, d);
-      if (lane >= d) sum += o;
+    for (int i = 0; i < 2; ++i)
+      if (e0 + 64 * i + lane < a.E) mx_run(a.offsets, e0 + 64 * i + lane, a.P, lo[i], hi[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = (hi[i] - lo[i] + a.bm - 1) / a.bm;
+      const int sum = wave_prefix_sum(n), head = before + sum - n;
+      const uint64_t hit = __ballot(t >= head && t < head + n);
+      if (hit) {
+        const int l = __ffsll((unsigned long long)hit) - 1;
+        const int first =
+            __builtin_amdgcn_readlane(lo[i], l) + (t - __builtin_amdgcn_readlane(head, l)) * a.bm;
+        s.group = e0 + 64 * i + l;
+        s.first = first;
+        s.rows = min(a.bm, __builtin_amdgcn_readlane(hi[i], l) - first);
+        return true;
+      }
+      before += __builtin_amdgcn_readlane(sum, 63);
     }
-    const int head = before + sum - n;
-    const uint64_t hit = __ballot(t >= head && t < head + n);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int first = __builtin_amdgcn_readlane(lo, l) + (t - __builtin_amdgcn_readlane(head, l)) * a.bm;
-      s.group = e0 + l;
-      s.first = first;
-      s.rows = min(a.bm, __builtin_amdgcn_readlane(hi, l) - first);
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(sum, 63);
   }
   return false;
 }

@@ -11,9 +11,9 @@
 // A wavefront multiplies half steps of 64 inputs, with the operands of one in
 // registers while it reads those of the next.  At the last half step of a
 // stage all of the stage is in registers: one barrier there, behind the first
-// products, frees its buffer for the stage after those in flight.  Four
-// buffers (three with 8-bit rows) keep loads on their way behind the one that
-// the barrier waits for.
+// products, frees its buffer for the stage after those in flight.  Three to
+// six buffers keep loads on their way behind the one that the barrier waits
+// for.
 #include "mx.h"
 
 #include <type_traits>
@@ -98,10 +98,16 @@ struct Shape {
   static constexpr int kRows = 32 * WM * FM, kBlocks = 2 * WN * FN;  // of the tile
   static constexpr int kRowBytes = FMT == kFp4 ? 64 : 128;           // of a stage
   static constexpr int kRowKiB = kRows * kRowBytes / 1024, kCodeKiB = kBlocks;
-  static constexpr int kBuffers = FMT == kFp4 ? 4 : 3;
   static constexpr int kStageBytes = (kRowKiB + kCodeKiB) * 1024;
   static constexpr int kScaleKiB = (kRows + 16 * kBlocks) / 64;
+  // As many buffers as half of a compute unit's LDS holds (of the wide tiles,
+  // which run alone, all of it), at most six: scales are kept of two supers,
+  // and the sixth stage on may begin the super after the next when the last
+  // scales of this one have just been read.
+  static constexpr int kRoom = (kBlocks > 8 ? 160 : 80) * 1024 - 2 * kScaleKiB * 1024;
+  static constexpr int kBuffers = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
   static constexpr int kLds = kBuffers * kStageBytes + 2 * kScaleKiB * 1024;
+  static_assert(kBuffers >= 3, "a stage in use, one to read next, one on its way");
 };
 
 template <int FMT, int WM, int WN, int FM, int FN, bool GATED, bool SPLIT>
