@@ -471,7 +471,7 @@ int w4a8_mx_grouped_linear(const void* x, int32_t x_dtype, int32_t act, int32_t 
     return fail(W4A8_ERR_UNSUPPORTED_SHAPE, "N=%lld gates and values are not a multiple of 32", (long long)N);
   if (!rows && M != P)
     return fail(W4A8_ERR_INVALID_ARG, "without rows M=%lld and P=%lld must agree", (long long)M, (long long)P);
-  if (rows && M * mx_row_bytes(K, act) > kMostOffset)
+  if (rows && M * mx_row_bytes(K, act) >= kOob)
     return fail(W4A8_ERR_UNSUPPORTED_SHAPE, "rows by index are addressed with 32-bit offsets (M=%lld K=%lld)",
                 (long long)M, (long long)K);
   const size_t wb = (size_t)mx_weight_bytes(E * N, K);

@@ -157,7 +157,8 @@ mx_tile_kernel(const MxArgs a) {
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
     const int r = (wave * kRowLoads + i) * (64 / kChunks) + lane / kChunks;
-    ox[i] = (uint32_t)source(r) * a.ldx + 16 * (lane % kChunks ^ place(r));
+    // rows past the tile's: zeros, which ask for no memory and the matrix cores for little power
+    ox[i] = r < sp.rows ? (uint32_t)source(r) * a.ldx + 16 * (lane % kChunks ^ place(r)) : (uint32_t)kOob;
   }
 #pragma unroll
   for (int i = 0; i < kCodeLoads; ++i)

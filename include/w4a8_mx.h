@@ -139,7 +139,8 @@ int w4a8_mx_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, co
  * A row's result does not depend on the other rows except through the kernel
  * that the sizes select.  The call never synchronises and can be captured.
  * Requirements: as w4a8_mx_linear, 1 <= M, P <= 2^24, 1 <= E <= 1024, gated:
- * N % 32 == 0; with rows the quantised rows of x below 2^32 bytes.
+ * N % 32 == 0; with rows the quantised rows of x (inputs rounded up
+ * to 256, and 128 bytes) below 2^31 bytes.
  */
 int w4a8_mx_grouped_linear_plan(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act,
                                 w4a8_mx_plan_t* plan);
