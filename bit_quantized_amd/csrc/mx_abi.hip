@@ -54,9 +54,8 @@ double plan_tiles(MxPlan& p, int64_t M, int64_t N, int64_t Q) {
   return best;
 }
 
-// Rows that the stream takes, all at once or of a group, and its 16-row
-// fragments a workgroup.
-constexpr int kStreamRows = 64;
+// Most rows that the stream takes: of the linear; of a group, evenly shared.
+constexpr int kStreamRows = 64, kStreamPerGroup = 8;
 
 // Microseconds of the stream for M rows: the weight from memory, or the rows
 // through the L1 caches of the compute units, KiB at 45 a microsecond (33 rows
@@ -111,7 +110,7 @@ MxPlan mx_plan(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
     // 261 (64 x 128).
     const double per = double(P) / E;
     p.path = kMxTile;
-    if (per <= 8) {
+    if (per <= kStreamPerGroup) {
       p.path = kMxStream;
       p.bn = 32;  // (of the plain product: 27.1 against 29.7 us at 4 rows a group)
     } else if (per <= 80) {
@@ -153,7 +152,7 @@ namespace {
 // Bytes that serve M (P) rows and every smaller number of them.
 int64_t workspace_bound(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
   // rows, or interleaved product rows of the stream
-  const int64_t Ps = std::min<int64_t>(P, E ? (int64_t)kStreamRows * E : kStreamRows);
+  const int64_t Ps = std::min<int64_t>(P, E ? (int64_t)kStreamPerGroup * E : kStreamRows);
   const int64_t n = std::max(round_up256(M * mx_row_bytes(K, fmt)) + round_up256(M * mx_row_scale_bytes(K)),
                              ceil_div(Ps, 16) * (mx_block_bytes(K, fmt) + mx_block_scale_bytes(K)));
   if (E) return n + 256 + round_up256(mx_tile_slots(P, E, 16) * (int64_t)sizeof(MxTile));

@@ -18,7 +18,7 @@ def magnitudes(fmt):
 
 def quantise(x, fmt, rule):
     """x [M][K] -> (codes uint8 [M][K], one a value; scale bytes uint8 [M][K / 32])."""
-    mags = magnitudes(fmt)
+    mags = magnitudes(fmt).to(x.device)
     x = x.double()
     M, K = x.shape
     b = x.reshape(-1, BLOCK)
@@ -47,9 +47,9 @@ def quantise(x, fmt, rule):
 def values(codes, scales, fmt):
     """The values of codes (one a byte) and scale bytes, 64 bits."""
     half = 8 if fmt == "fp4" else 128
-    mags = magnitudes(fmt)
+    mags = magnitudes(fmt).to(codes.device)
     if fmt == "fp8":
-        mags = torch.cat([mags, torch.tensor([float("nan")], dtype=torch.float64)])
+        mags = torch.cat([mags, mags.new_tensor([float("nan")])])
     c = codes.long()
     v = torch.where(c >= half, -1.0, 1.0) * mags[c % half]
     s = torch.where(scales == 255, float("nan"), torch.exp2(scales.double() - 127))

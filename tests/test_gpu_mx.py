@@ -164,18 +164,29 @@ def linear_case(w4, M, N, K, act, rule, dtype, near, seed=0, **kw):
     q, s = weight(g, N, K)
     w = w4.mx_pack_weights(ref.pack4(q).cuda(), s.cuda())
     y = w4.mx_linear(x.cuda(), w, act=act, rule=rule, **kw)
-    xv, wv = ref.rounded(x, act, rule).cuda(), ref.values(q, s, "fp4").cuda()
+    xv, wv = ref.rounded(x.cuda(), act, rule), ref.values(q.cuda(), s.cuda(), "fp4")
     e, cut = ref.slack(xv, wv, act)
     check(y, xv @ wv.t().contiguous(), e if near else e + cut, f"{M} {N} {K} {act}")
     return y
 
 
-@pytest.mark.parametrize("act", FMTS)
-@pytest.mark.parametrize("near", [True, False])
-@pytest.mark.parametrize("M,N,K", [
+SIZES = [
     (1, 16, 32), (1, 48, 160), (1, 3584, 3584), (2, 64, 2912), (4, 512, 18944), (5, 256, 384), (13, 4112, 1056),
     (16, 3584, 2048), (17, 128, 32), (33, 272, 18944), (33, 3584, 4096), (64, 400, 544), (65, 4112, 2912),
-    (100, 128, 128), (129, 144, 1184), (200, 2064, 640), (257, 1040, 288), (300, 16, 4096), (517, 4112, 2912)])
+    (100, 128, 128), (129, 144, 1184), (200, 2064, 640), (257, 1040, 288), (300, 16, 4096), (517, 4112, 2912)]
+TILES = [
+    (2048, 8192, 1056, (256, 256)), (1030, 12816, 288, (256, 256)), (300, 18960, 416, (128, 256)),
+    (517, 4112, 672, (128, 128)), (200, 8208, 288, (128, 128)), (150, 4112, 288, (64, 128)), (65, 4112, 672, (64, 128))]
+SLICES = [(33, 256, 18944), (100, 144, 4128), (513, 528, 16416), (70, 2064, 9248), (700, 3584, 18944),
+          (130, 6544, 17472)]
+STREAMED = [(16, 4112, 2912, 16), (17, 528, 1056, 16), (40, 4112, 544, 16), (64, 4096, 1024, 16), (20, 8208, 160, 32),
+            (48, 8208, 160, 32), (60, 8208, 160, 32)]
+LINEAR = SIZES + [c[:3] for c in TILES] + SLICES + [c[:3] for c in STREAMED]
+
+
+@pytest.mark.parametrize("act", FMTS)
+@pytest.mark.parametrize("near", [True, False])
+@pytest.mark.parametrize("M,N,K", SIZES)
 def test_linear(w4, act, near, M, N, K):
     linear_case(w4, M, N, K, act, "floor", "bf16", near)
 
@@ -188,9 +199,7 @@ def test_linear_of_float_rows_and_ceil(w4, act, M, N, K):
 
 
 @pytest.mark.parametrize("act", FMTS)
-@pytest.mark.parametrize("M,N,K,tile", [
-    (2048, 8192, 1056, (256, 256)), (1030, 12816, 288, (256, 256)), (300, 18960, 416, (128, 256)),
-    (517, 4112, 672, (128, 128)), (200, 8208, 288, (128, 128)), (150, 4112, 288, (64, 128)), (65, 4112, 672, (64, 128))])
+@pytest.mark.parametrize("M,N,K,tile", TILES)
 def test_linear_of_each_tile(w4, act, M, N, K, tile):
     p = w4.mx_linear_plan(M, N, K, act)
     assert (p.path, p.tile_rows, p.tile_cols, p.ksplit) == (w4.MX_TILE, *tile, 1)
@@ -198,15 +207,14 @@ def test_linear_of_each_tile(w4, act, M, N, K, tile):
 
 
 @pytest.mark.parametrize("act", FMTS)
-@pytest.mark.parametrize("M,N,K", [(33, 256, 18944), (100, 144, 4128), (513, 528, 16416), (70, 2064, 9248)])
+@pytest.mark.parametrize("M,N,K", SLICES)
 def test_linear_in_slices(w4, act, M, N, K):
     assert w4.mx_linear_plan(M, N, K, act).ksplit > 1
     linear_case(w4, M, N, K, act, "floor", "bf16", True)
 
 
 @pytest.mark.parametrize("act", FMTS)
-@pytest.mark.parametrize("M,N,K,cols", [(16, 4112, 2912, 16), (17, 528, 1056, 16), (40, 4112, 544, 16),
-                                        (64, 4096, 1024, 16), (48, 8208, 160, 32), (60, 8208, 160, 32)])
+@pytest.mark.parametrize("M,N,K,cols", STREAMED)
 def test_linear_streamed(w4, act, M, N, K, cols):
     p = w4.mx_linear_plan(M, N, K, act)
     assert (p.path, p.tile_rows, p.tile_cols) == (w4.MX_STREAM, -(-M // 16) * 16, cols)
@@ -231,7 +239,7 @@ def grouped_case(w4, counts, N, K, act, rule="floor", dtype="bf16", gather=True,
                              act=act, rule=rule, out=out)
     assert y is out
     assert bool((y[:lead] == 7.5).all()) and bool((y[P - tail:] == 7.5).all())
-    xv, wv = ref.rounded(x, act, rule).cuda(), ref.values(q, s, "fp4").cuda()
+    xv, wv = ref.rounded(x.cuda(), act, rule), ref.values(q.cuda(), s.cuda(), "fp4")
     for e in range(E):
         lo, hi = int(offsets[e]), int(offsets[e + 1])
         if lo == hi:
@@ -272,12 +280,24 @@ def test_grouped(w4, act, gated, counts):
     grouped_case(w4, counts, 96, 2912, act, gated=gated, tail=5, lead=2, gather=False)
 
 
+MANY = [((*[(i * 7) % 4 for i in range(200)],), 64, 288), ((1,) * 16, 64, 1056), ((4, 0, 9, 1, 6, 0, 0, 3), 1056, 544),
+        ((130, 60, 80), 288, 544), ((300, 250, 500), 352, 800), ((400, 500, 0, 700, 900), 544, 288),
+        ((1100, 900, 0, 1300), 4128, 544)]
+
+
+def grouped_sizes():
+    """(counts, N, K, gated) of the tests of grouped products."""
+    out = [(c, 160, 416, g) for c in RAGGED for g in (False, True) if sum(c)]
+    return out + [(c, N, K, g) for c, N, K in MANY for g in (False, True)]
+
+
 @pytest.mark.parametrize("act", FMTS)
-def test_grouped_of_many_groups_and_large_tiles(w4, act):
-    grouped_case(w4, [(i * 7) % 4 for i in range(200)], 64, 288, act, gated=True)
-    grouped_case(w4, [1] * 16, 64, 1056, act, dtype="f32", rule="ceil")
-    grouped_case(w4, [1100, 900, 0, 1300], 4096, 544, act, gated=True, M=500)
-    grouped_case(w4, [1100, 900, 0, 1300], 4112, 544, act, gather=False, tail=9)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{sum(c[0])}rows_{len(c[0])}groups")
+def test_grouped_of_many_groups_and_each_tile(w4, act, gated, case):
+    counts, N, K = case
+    grouped_case(w4, counts, N, K, act, gated=gated, tail=7)
+    grouped_case(w4, counts, N, K, act, gated=gated, gather=False, tail=7, dtype="f32", rule="ceil", near=False)
 
 
 @pytest.mark.parametrize("counts", [(3, 2), (20, 40), (140, 90)])
