@@ -1,0 +1,78 @@
+"""The microscaled tile kernels' assembly, as built, keeps what their LDS-direct
+loads rely on (test_rows_asm_cpu.py states the first two for the row tiles):
+- a load comes five wait states after anything before its block;
+- m0 has no other use;
+- each barrier of the main loop leaves exactly the loads of the stages behind
+  the one that is read next, and the loop has no other request to memory.
+"""
+import os
+import re
+import subprocess
+
+import pytest
+
+import test_rows_asm_cpu as rows
+
+BARRIER = re.compile(r"s_waitcnt vmcnt\((\d+)\) lgkmcnt\(0\)$")
+
+
+@pytest.fixture(scope="module")
+def kernels(tmp_path_factory):
+    from bit_quantized_amd import build as B
+    out = str(tmp_path_factory.mktemp("asm") / "mx_tile.s")
+    r = subprocess.run([B.HIPCC, *B.FLAGS, "--cuda-device-only", "-S", os.path.join(B.CSRC, "mx_tile.hip"), "-o", out],
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    with open(out) as f:
+        found = rows._kernels(f.read())
+    assert len(found) == 24  # two formats, four tiles; plain, gated, split
+    return found
+
+
+def test_loads_come_after_the_rest_their_operands_need(kernels):
+    rows.test_loads_come_after_the_rest_their_operands_need(kernels)
+
+
+def test_m0_has_no_other_use(kernels):
+    rows.test_m0_has_no_other_use(kernels)
+
+
+def _shape(name):
+    """(loads of a stage without its scales, buffers) of a kernel, from its template arguments."""
+    fmt, wm, wn, fm, fn = map(int, re.search(r"ILi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d)E", name).groups())
+    tall, blocks = 32 * wm * fm, 2 * wn * fn
+    row_kib = tall * (128 if fmt else 64) // 1024
+    scales = (tall + 16 * blocks) // 64
+    room = (160 if blocks > 8 else 80) - 2 * scales
+    return (row_kib + blocks) // (wm * wn), min(room // (row_kib + blocks), 6)
+
+
+def _loop(code):
+    """The instructions of the innermost loop that holds the products."""
+    label = {ins[:-1]: i for i, (ins, _) in enumerate(code) if ins.endswith(":")}
+    best = None
+    for i, (ins, _) in enumerate(code):
+        m = re.match(r"s_c?branch\w* (\.LBB\w+)", ins)
+        if m and label[m.group(1)] < i:
+            body = [c[0] for c in code[label[m.group(1)]:i]]
+            if any("mfma" in c for c in body) and (best is None or len(body) < len(best)):
+                best = body
+    return best
+
+
+def test_barriers_leave_the_stages_that_are_not_read_next(kernels):
+    for name, code in kernels.items():
+        loads, buffers = _shape(name)
+        body = _loop(code)
+        waits = [i for i, c in enumerate(body) if BARRIER.match(c) and body[i + 1].startswith("s_barrier")]
+        assert len(waits) == 2, name
+        assert not any(c.startswith(("scratch", "global", "flat")) for c in body), name
+        # requests after each barrier, around the loop: stage t + buffers of steps 0 and 1
+        span = body[waits[0]:waits[1]], body[waits[1]:] + body[:waits[0]]
+        sent = [sum("offen lds" in c for c in s) for s in span]
+        assert [sum(bool(rows.REQUEST.match(c)) for c in s) for s in span] == sent, name
+        assert sorted(sent) == [loads, loads + 1], name  # one of the two brings scales
+        for step in (0, 1):
+            # the last of them were sent at the step before this one
+            behind = sum(sent[(step - 1 - k) % 2] for k in range(buffers - 2))
+            assert int(BARRIER.match(body[waits[step]]).group(1)) == behind, f"{name}: step {step}"
