@@ -185,24 +185,34 @@ mx_tile_kernel(const MxArgs a) {
   // same bytes once more (a branch here would let the compiler move the
   // products of the whole iteration behind it).
   constexpr int kLoads = kRowLoads + kCodeLoads;
-  auto fill = [&](int at, int t, bool even) __attribute__((always_inline)) {
-    if (even) {
-      const int q = min(t, T1 - 1) >> 2;
-      load_at(rs, lds0 + scales_at((q - Q0) & 1) + scale_kib * 1024, os, q * scale_step);
+  auto fill_scales = [&](int t) __attribute__((always_inline)) {
+    const int q = min(t, T1 - 1) >> 2;
+    load_at(rs, lds0 + scales_at((q - Q0) & 1) + scale_kib * 1024, os, q * scale_step);
+  };
+  auto fill_one = [&](int i, int at, int t) __attribute__((always_inline)) {
+    if (i == 0) {
+      rx.words[2] = t < T1 ? (int)(uint32_t)(left * a.ldx) : 0;
+      rw.words[2] = t < T1 ? (int)(uint32_t)code_bytes : 0;
     }
-    rx.words[2] = t < T1 ? (int)(uint32_t)(left * a.ldx) : 0;
-    rw.words[2] = t < T1 ? (int)(uint32_t)code_bytes : 0;
-#pragma unroll
-    for (int i = 0; i < kRowLoads; ++i)
+    if (i < kRowLoads)
       load_at(rx, lds0 + at + (wave * kRowLoads + i) * 1024, ox[i], t * S::kRowBytes);
+    else
+      load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i - kRowLoads) * 1024, ow[i - kRowLoads],
+              t * kBlockBytes);
+  };
+  auto fill = [&](int at, int t, bool even) __attribute__((always_inline)) {
+    if (even) fill_scales(t);
 #pragma unroll
-    for (int i = 0; i < kCodeLoads; ++i)
-      load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i) * 1024, ow[i], t * kBlockBytes);
+    for (int i = 0; i < kLoads; ++i) fill_one(i, at, t);
   };
 
-  // ---- operands of a half step, in two sets; scales, by half of a step
-  v4i w[2][FN], x[2][FM][kUnits];
-  int sw[2][FN], sx[2][FM];
+  // ---- operands: of two half steps of 64 inputs, or (small wavefront tiles,
+  // whose few products would not cover the reads) of two whole steps; scales
+  // by half of a step
+  constexpr bool kDeep = FM * FN <= 4;
+  constexpr int kSets = kDeep ? 2 : 1;
+  v4i w[kSets][2][FN], x[kSets][2][FM][kUnits];
+  int sw[2][FN], sx[2][FM], sw1[2][FN], sx1[2][FM];
   int x_at[kChunks / 2];  // this lane's row of the first 32, chunks 2 i and 2 i + 1 of it
 #pragma unroll
   for (int i = 0; i < kChunks / 2; ++i)
@@ -210,24 +220,25 @@ mx_tile_kernel(const MxArgs a) {
   const int w_at = S::kRowKiB * 1024 + (wn * FN * 2 + (c >> 4)) * 1024 + j * 256 + (c & 15) * 16;
   const int sx_at = (wm * FM * 32 + c) * 16 + 4 * j;
   const int sw_at = S::kRows * 16 + (wn * FN * 2 + (c >> 4)) * 256 + j * 64 + (c & 15) * 4;
-  // half h of the stage in the buffer at byte `at`
-  auto read_row = [&](int m, int at, int h) __attribute__((always_inline)) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u)
-      x[h][m][u] = *reinterpret_cast<const v4i*>(lds + at + x_at[h * kUnits + u] + m * 32 * S::kRowBytes);
+  // read i of half h of the stage in the buffer at byte `at`
+  constexpr int kReads = FM * kUnits + FN;
+  auto read_one = [&](int i, int set, int h, int at) __attribute__((always_inline)) {
+    if (i < FM * kUnits)
+      x[set][h][i / kUnits][i % kUnits] = *reinterpret_cast<const v4i*>(
+          lds + at + x_at[h * kUnits + i % kUnits] + i / kUnits * 32 * S::kRowBytes);
+    else
+      w[set][h][i - FM * kUnits] =
+          *reinterpret_cast<const v4i*>(lds + at + w_at + (i - FM * kUnits) * 2048 + h * 512);
   };
-  auto read_blocks = [&](int n, int at, int h) __attribute__((always_inline)) {
-    w[h][n] = *reinterpret_cast<const v4i*>(lds + at + w_at + n * 2048 + h * 512);
-  };
-  // (an iteration's two steps have the upper or the lower two of four bytes)
-  auto read_scales = [&](int h, int it) __attribute__((always_inline)) {
+  // scale i of half h (an iteration's two steps have the upper or the lower
+  // two of four bytes)
+  constexpr int kScaleReads = FM + FN;
+  auto read_scale = [&](int i, int h, int it, int (&dw)[FN], int (&dx)[FM]) __attribute__((always_inline)) {
     const int at = scales_at(((it >> 1) - Q0) & 1) + 2 * (it & 1);
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-      sx[h][m] = *reinterpret_cast<const uint16_t*>(lds + at + sx_at + m * 512 + h * 8);
-#pragma unroll
-    for (int n = 0; n < FN; ++n)
-      sw[h][n] = *reinterpret_cast<const uint16_t*>(lds + at + sw_at + n * 512 + h * 128);
+    if (i < FM)
+      dx[i] = *reinterpret_cast<const uint16_t*>(lds + at + sx_at + i * 512 + h * 8);
+    else
+      dw[i - FM] = *reinterpret_cast<const uint16_t*>(lds + at + sw_at + (i - FM) * 512 + h * 128);
   };
 
   v16f_mx acc[FM][FN];
@@ -237,58 +248,89 @@ mx_tile_kernel(const MxArgs a) {
     for (int n = 0; n < FN; ++n)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+  // product i of half h (step s of its iteration)
+  constexpr int kProducts = FM * FN;
+  auto multiply = [&](auto sc, int set, int h, int i) __attribute__((always_inline)) {
+    const int m = i / FN, n = i % FN;
+    v8i_mx xv;
+    if constexpr (FMT == kFp4) xv = mx_wide(x[set][h][m][0]);
+    else xv = mx_wide(x[set][h][m][0], x[set][h][m][kUnits - 1]);
+    acc[m][n] = mx_mfma32<FMT, decltype(sc)::value>(mx_wide(w[set][h][n]), xv, acc[m][n], sw[h][n], sx[h][m]);
+  };
 
   if (T0 < T1) {
 #pragma unroll
     for (int b = 0; b < S::kBuffers; ++b) fill(b * S::kStageBytes, T0 + b, b % 2 == 0);
     stage_barrier<(S::kBuffers - 1) * kLoads + (S::kBuffers - 1) / 2>();
-    read_scales(0, I0);
 #pragma unroll
-    for (int m = 0; m < FM; ++m) read_row(m, 0, 0);
+    for (int h = 0; h < (kDeep ? 2 : 1); ++h) {
 #pragma unroll
-    for (int n = 0; n < FN; ++n) read_blocks(n, 0, 0);
+      for (int i = 0; i < kScaleReads; ++i) read_scale(i, h, I0, sw[h], sx[h]);
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) read_one(i, 0, h, 0);
+    }
   }
   int own = 0;  // the buffer of the stage that is multiplied
   for (int it = I0; it < I1; ++it) {
-    auto half_step = [&](auto sc, auto hc) __attribute__((always_inline)) {
-      constexpr int s = decltype(sc)::value, h = decltype(hc)::value;
-      constexpr bool last = h == 1;
+    // Products and, between them, what they leave the issue slots for: the
+    // reads of the next (half) step first, then scales, then the stage's
+    // loads.  Issued in blocks of their own they add up: 622 cycles a step
+    // of a 128 x 128 tile whose products take 256, TBD so.
+    auto step = [&](auto sc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value;
       const int next = own == (S::kBuffers - 1) * S::kStageBytes ? 0 : own + S::kStageBytes;
-      const int from = last ? next : own;
+      const int t = 2 * it + s + S::kBuffers;  // the stage that takes this one's buffer
+      constexpr bool even = (s + S::kBuffers) % 2 == 0;
+      // loads behind the stage that is read next: kBuffers - 2 stages, the
+      // first of step s; the even ones with a load of scales
+      constexpr int kBehind = S::kBuffers - 2;
+      constexpr int kLeft = kBehind * kLoads + (kBehind + (s == 0 ? 1 : 0)) / 2;
+      constexpr int kHalves = kDeep ? 1 : 2;  // parts of a step with reads of their own
 #pragma unroll
-      for (int m = 0; m < FM; ++m) {
-        v8i_mx xv;
-        if constexpr (FMT == kFp4) xv = mx_wide(x[h][m][0]);
-        else xv = mx_wide(x[h][m][0], x[h][m][kUnits - 1]);
+      for (int part = 0; part < kHalves; ++part) {
+        const bool last = part == kHalves - 1;
+        constexpr int kSlots = 2 * kProducts / kHalves;
+        // this part's items, in their order
+        constexpr int kOperands = kDeep ? 2 * kReads : kReads;
+        const int scales = kDeep ? (s == 1 ? 2 * kScaleReads : 0) : (s == part ? kScaleReads : 0);
+        const int loads = last ? kLoads + (even ? 1 : 0) : 0;
+        const int items = kOperands + scales + loads;
 #pragma unroll
-        for (int n = 0; n < FN; ++n) acc[m][n] = mx_mfma32<FMT, s>(mx_wide(w[h][n]), xv, acc[m][n], sw[h][n], sx[h][m]);
-        if (m == 0) {
-          // behind the stage that is read next: kBuffers - 2 of them, every
-          // second one with a load of scales (even stages go to even steps
-          // when the buffers are even in number, to odd ones when not)
-          constexpr int kBehind = S::kBuffers - 2;
-          constexpr bool even_first = s == 0;  // stage t + 2 for step s of t
-          if constexpr (last) stage_barrier<kBehind * kLoads + (kBehind + (even_first ? 1 : 0)) / 2>();
+        for (int slot = 0; slot < kSlots; ++slot) {
+          multiply(sc, kDeep ? s : 0, kDeep ? slot / kProducts : part, slot % kProducts);
+          if (slot == 0 && last) stage_barrier<kLeft>();
 #pragma unroll
-          for (int i = 0; i < FM; ++i) read_row(i, from, 1 - h);
-#pragma unroll
-          for (int i = 0; i < FN; ++i) read_blocks(i, from, 1 - h);
-          // scales of this iteration's odd halves, of the next one's even ones
-          if constexpr (s == 0 && h == 0) read_scales(1, it);
-          if constexpr (s == 1 && h == 1) read_scales(0, it + 1);
-          if constexpr (last) {
-            const int t = 2 * it + s + S::kBuffers;
-            fill(own, t, (s + S::kBuffers) % 2 == 0);
+          for (int i = slot * items / kSlots; i < (slot + 1) * items / kSlots; ++i) {
+            if (i < kOperands) {
+              if constexpr (kDeep) read_one(i % kReads, 1 - s, i / kReads, next);
+              else read_one(i, 0, 1 - part, last ? next : own);
+            } else if (i < kOperands + scales) {
+              const int k = i - kOperands;
+              if constexpr (kDeep) read_scale(k % kScaleReads, k / kScaleReads, it + 1, sw1[k / kScaleReads], sx1[k / kScaleReads]);
+              else if (part == 0) read_scale(k, 1, it, sw[1], sx[1]);  // of this iteration's odd halves
+              else read_scale(k, 0, it + 1, sw1[0], sx1[0]);           // of the next one's even ones
+            } else {
+              const int k = i - kOperands - scales;
+              if (even && k == 0) fill_scales(t);
+              else fill_one(k - (even ? 1 : 0), own, t);
+            }
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (last) own = next;
+      if constexpr (s == 1) {
+#pragma unroll
+        for (int h = 0; h < (kDeep ? 2 : 1); ++h) {
+#pragma unroll
+          for (int m = 0; m < FM; ++m) sx[h][m] = sx1[h][m];
+#pragma unroll
+          for (int n = 0; n < FN; ++n) sw[h][n] = sw1[h][n];
+        }
+      }
+      own = next;
     };
-    half_step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
-    half_step(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
-    half_step(std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
-    half_step(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
   }
   stage_barrier<0>();  // (the last loads, none of them a request)
 
@@ -343,13 +385,22 @@ mx_tile_kernel(const MxArgs a) {
   }
 }
 
-// y = bf16 of the slices' sums, in order; four channels a thread.
+// y = bf16 of the slices' sums, in order; four channels a thread, eight
+// slices' loads at a time.
 __global__ void __launch_bounds__(256)
 mx_reduce_kernel(const float* __restrict__ parts, int64_t quads, int ksplit, uint16_t* __restrict__ y) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= quads) return;
-  v4f_mx v = reinterpret_cast<const v4f_mx*>(parts)[t];
-  for (int k = 1; k < ksplit; ++k) v += reinterpret_cast<const v4f_mx*>(parts)[t + k * quads];
+  const v4f_mx* p = reinterpret_cast<const v4f_mx*>(parts) + t;
+  v4f_mx v = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < ksplit; k0 += 8) {
+    v4f_mx part[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[k] = p[min(k0 + k, ksplit - 1) * quads];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k0 + k < ksplit) v += part[k];
+  }
   reinterpret_cast<uint2*>(y)[t] = mx_bf16x4(v);
 }
 
@@ -373,7 +424,7 @@ template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
   if (p.bm == 256 && p.bn == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
   if (p.bm == 128 && p.bn == 256) return launch_shape<FMT, 2, 4, 2, 2>(a, p, gated, blocks, st);
-  if (p.bm == 128 && p.bn == 128) return launch_shape<FMT, 2, 2, 2, 2>(a, p, gated, blocks, st);
+  if (p.bm == 128 && p.bn == 128) return launch_shape<FMT, 4, 2, 1, 2>(a, p, gated, blocks, st);
   if (p.bm == 64 && p.bn == 128) return launch_shape<FMT, 2, 2, 1, 2>(a, p, gated, blocks, st);
   return hipErrorInvalidValue;
 }
