@@ -29,9 +29,10 @@ struct Spot {
 
 // Work is ordered by group, then strip, then tile: the tiles of one group that
 // read the same weights run side by side on one XCD.
+template <bool GROUPED>
 __device__ __forceinline__ bool locate(const MxArgs& a, Spot& s) {
   const int b = blockIdx.x;
-  if (!a.offsets) {
+  if constexpr (!GROUPED) {
     // bands of kBand row tiles, strip by strip: the 32 compute units of an XCD
     // work on 8 x 4 tiles, whose rows and channels they share in its L2
     const int tiles = (int)((a.P + a.bm - 1) / a.bm);
@@ -59,7 +60,7 @@ __device__ __forceinline__ bool locate(const MxArgs& a, Spot& s) {
   return true;
 }
 
-__device__ __forceinline__ int source_row(const MxArgs& a, int p) {
+__device__ __forceinline__ int source_row(const MxArgs& a, int p) {  // (of groups)
   if (!a.rows) return p;
   const int r = a.rows[p];
   return r >= 0 && r < a.M ? r : -1;
@@ -91,8 +92,12 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// What a launch computes: the linear whole or in slices of the inputs, groups,
+// groups with the gated activation.
+enum Kind { kWhole = 0, kSlices = 1, kGroups = 2, kGated = 3 };
+
 // WM x WN wavefronts of 32 FM rows and 32 FN channels each.
-template <int FMT, int WM, int WN, int FM, int FN>
+template <int FMT, int WM, int WN, int FM, int FN, int KIND>
 struct Shape {
   static constexpr int kWaves = WM * WN;
   static constexpr int kRows = 32 * WM * FM, kBlocks = 2 * WN * FN;  // of the tile
@@ -103,21 +108,27 @@ struct Shape {
   // As many buffers as half of a compute unit's LDS holds (of the wide tiles,
   // which run alone, all of it), at most six: scales are kept of two supers,
   // and the sixth stage on may begin the super after the next when the last
-  // scales of this one have just been read.
-  static constexpr int kRoom = (kBlocks > 8 ? 160 : 80) * 1024 - 2 * kScaleKiB * 1024;
+  // scales of this one have just been read.  Groups, whose many tiles are
+  // short, take a third where that holds three buffers: 4096 rows of 128
+  // groups, 2048 inputs: 53 us in three buffers, three workgroups to a compute
+  // unit, 57 in six and two; but 33 rows 18944 -> 3584 15 in four, 16.6 in three.
+  static constexpr int kFixed = 2 * kScaleKiB * 1024;
+  static constexpr bool kThird = KIND >= kGroups && kBlocks <= 8 && 160 * 1024 / 3 - kFixed >= 3 * kStageBytes;
+  static constexpr int kRoom = (kThird ? 160 * 1024 / 3 : (kBlocks > 8 ? 160 : 80) * 1024) - kFixed;
   static constexpr int kBuffers = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
   static constexpr int kLds = kBuffers * kStageBytes + 2 * kScaleKiB * 1024;
   static_assert(kBuffers >= 3, "a stage in use, one to read next, one on its way");
 };
 
-template <int FMT, int WM, int WN, int FM, int FN, bool GATED, bool SPLIT>
+template <int FMT, int WM, int WN, int FM, int FN, int KIND>
 __global__ void __launch_bounds__(64 * WM * WN)
 mx_tile_kernel(const MxArgs a) {
-  using S = Shape<FMT, WM, WN, FM, FN>;
+  using S = Shape<FMT, WM, WN, FM, FN, KIND>;
+  constexpr bool SPLIT = KIND == kSlices, GATED = KIND == kGated;
   constexpr int kUnits = FMT == kFp4 ? 1 : 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   Spot sp;
-  if (!locate(a, sp)) return;
+  if (!locate<(KIND >= kGroups)>(a, sp)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int c = lane & 31, j = lane >> 5;
@@ -275,7 +286,7 @@ mx_tile_kernel(const MxArgs a) {
     // Products and, between them, what they leave the issue slots for: the
     // reads of the next (half) step first, then scales, then the stage's
     // loads.  Issued in blocks of their own they add up: 622 cycles a step
-    // of a 128 x 128 tile whose products take 256, TBD so.
+    // of a 128 x 128 tile whose products take 256, 510 so.
     auto step = [&](auto sc) __attribute__((always_inline)) {
       constexpr int s = decltype(sc)::value;
       const int next = own == (S::kBuffers - 1) * S::kStageBytes ? 0 : own + S::kStageBytes;
@@ -404,27 +415,28 @@ mx_reduce_kernel(const float* __restrict__ parts, int64_t quads, int ksplit, uin
   reinterpret_cast<uint2*>(y)[t] = mx_bf16x4(v);
 }
 
-template <int FMT, int WM, int WN, int FM, int FN, bool GATED, bool SPLIT>
+template <int FMT, int WM, int WN, int FM, int FN, int KIND>
 hipError_t launch_one(const MxArgs& a, const MxPlan& p, unsigned blocks, hipStream_t st) {
-  using S = Shape<FMT, WM, WN, FM, FN>;
+  using S = Shape<FMT, WM, WN, FM, FN, KIND>;
   static_assert(S::kLds <= 160 * 1024, "LDS of a compute unit");
-  constexpr auto kernel = mx_tile_kernel<FMT, WM, WN, FM, FN, GATED, SPLIT>;
+  constexpr auto kernel = mx_tile_kernel<FMT, WM, WN, FM, FN, KIND>;
   hipLaunchKernelGGL(kernel, dim3(blocks, (unsigned)p.ksplit), dim3(64 * S::kWaves), S::kLds, st, a);
   return hipGetLastError();
 }
 
 template <int FMT, int WM, int WN, int FM, int FN>
 hipError_t launch_shape(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
-  if (gated) return launch_one<FMT, WM, WN, FM, FN, true, false>(a, p, blocks, st);
-  if (p.ksplit > 1) return launch_one<FMT, WM, WN, FM, FN, false, true>(a, p, blocks, st);
-  return launch_one<FMT, WM, WN, FM, FN, false, false>(a, p, blocks, st);
+  if (gated) return launch_one<FMT, WM, WN, FM, FN, kGated>(a, p, blocks, st);
+  if (a.offsets) return launch_one<FMT, WM, WN, FM, FN, kGroups>(a, p, blocks, st);
+  if (p.ksplit > 1) return launch_one<FMT, WM, WN, FM, FN, kSlices>(a, p, blocks, st);
+  return launch_one<FMT, WM, WN, FM, FN, kWhole>(a, p, blocks, st);
 }
 
 template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
   if (p.bm == 256 && p.bn == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
   if (p.bm == 128 && p.bn == 256) return launch_shape<FMT, 2, 4, 2, 2>(a, p, gated, blocks, st);
-  if (p.bm == 128 && p.bn == 128) return launch_shape<FMT, 4, 2, 1, 2>(a, p, gated, blocks, st);
+  if (p.bm == 128 && p.bn == 128) return launch_shape<FMT, 2, 2, 2, 2>(a, p, gated, blocks, st);
   if (p.bm == 64 && p.bn == 128) return launch_shape<FMT, 2, 2, 1, 2>(a, p, gated, blocks, st);
   return hipErrorInvalidValue;
 }

@@ -25,7 +25,7 @@ def kernels(tmp_path_factory):
     assert r.returncode == 0, r.stderr[-2000:]
     with open(out) as f:
         found = rows._kernels(f.read())
-    assert len(found) == 24  # two formats, four tiles; plain, gated, split
+    assert len(found) == 32  # two formats, four tiles; whole, in slices, groups, gated groups
     return found
 
 
@@ -39,12 +39,15 @@ def test_m0_has_no_other_use(kernels):
 
 def _shape(name):
     """(loads of a stage without its scales, buffers) of a kernel, from its template arguments."""
-    fmt, wm, wn, fm, fn = map(int, re.search(r"ILi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d)E", name).groups())
+    fmt, wm, wn, fm, fn, kind = map(int, re.search(r"ILi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d)E", name).groups())
     tall, blocks = 32 * wm * fm, 2 * wn * fn
     row_kib = tall * (128 if fmt else 64) // 1024
     scales = (tall + 16 * blocks) // 64
     room = (160 if blocks > 8 else 80) - 2 * scales
-    return (row_kib + blocks) // (wm * wn), min(room // (row_kib + blocks), 6)
+    third = 160 / 3 - 2 * scales
+    if kind >= 2 and blocks <= 8 and third >= 3 * (row_kib + blocks):
+        room = third
+    return (row_kib + blocks) // (wm * wn), min(int(room // (row_kib + blocks)), 6)
 
 
 def _loop(code):
