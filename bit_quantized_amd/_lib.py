@@ -807,13 +807,15 @@ class MxTensor:
         return M, per * MX_BLOCK
 
     def check(self):
-        _mx(MX_FORMATS, self.format, "element format")
-        if self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
+        """(format, M, K) as the library takes them."""
+        fmt = _mx(MX_FORMATS, self.format, "element format")
+        codes, scales = self.codes, self.scales
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales must be uint8")
         M, K = self.shape
-        if self.codes.shape != (M, K // 2 if self.format == "fp4" else K):
-            raise ValueError(f"codes {tuple(self.codes.shape)} and scales {tuple(self.scales.shape)} do "
-                             f"not fit together")
+        if codes.shape != (M, K if fmt else K // 2):
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not fit together")
+        return fmt, M, K
 
 
 def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
@@ -844,15 +846,14 @@ def mx_dequant(t: MxTensor, dtype: torch.dtype = torch.bfloat16,
                out: torch.Tensor | None = None) -> torch.Tensor:
     """The values that codes and scales stand for, bfloat16 or float32 [M][K]."""
     lib = load()
-    t.check()
+    fmt, M, K = t.check()
     codes, scales = t.codes, t.scales
     _need_on(codes.get_device(), codes, scales, out)
-    M, K = t.shape
     if out is None:
         out = codes.new_empty((M, K), dtype=dtype)
     elif out.dtype != dtype or out.shape != (M, K):
         raise TypeError(f"out must be {dtype} [{M}][{K}]")
-    _check(lib.w4a8_mx_dequant(codes.data_ptr(), scales.data_ptr(), MX_FORMATS[t.format], M, K, out.data_ptr(),
+    _check(lib.w4a8_mx_dequant(codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(),
                                _act_dtype(out), _stream(out.device)))
     return out
 
