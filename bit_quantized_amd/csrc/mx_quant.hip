@@ -1,5 +1,6 @@
 // Rows to microscaled codes and scales and back, and the weight layout of the
-// products.  All of it streams: bound by memory.
+// products.  All of it streams: bound by memory (16384 x 3584 bfloat16 rows to
+// 4 bits or back, 150 MB, in 22 us: 6.8 TB/s).
 #include "mx.h"
 
 #include <type_traits>

@@ -13,6 +13,12 @@
 // registers four steps ahead like the weight; or raw: each wavefront quantises
 // its own inputs of every row into LDS while its first code blocks are on
 // their way, which saves a launch and needs no barrier.
+//
+// Measured: one token 3584 -> 18944 8.0 us (36 MB; the read rate of a large
+// buffer, 6.9 TB/s, would take 5.2, an empty launch 1.5); 8 of 128 experts 2048
+// -> 1536 gated 5.8 us (13 MB: the chain of offsets, row and first weights);
+// 512 rows of 126 such experts 26 us (211 MB, some of it from the last-level
+// cache).
 #include "mx.h"
 
 #include <type_traits>

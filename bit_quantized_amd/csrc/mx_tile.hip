@@ -14,6 +14,12 @@
 // products, frees its buffer for the stage after those in flight.  Three to
 // six buffers keep loads on their way behind the one that the barrier waits
 // for.
+//
+// Measured: 4096 rows 3584 -> 18944 in 4 bits 157 to 165 us (3.4 PFLOP/s), 2048
+// rows 18944 -> 3584 in 8 bits 106 to 120 (2.4).  The matrix cores are busy for
+// 46 and 60 % of the cycles, LDS reads for 34 and 35 %, and the clock falls to
+// 1.9 and 2.0 GHz: the products of random operands alone, without a load or an
+// LDS read, reach 6.4 and 3.9 PFLOP/s here.
 #include "mx.h"
 
 #include <type_traits>
