@@ -198,7 +198,8 @@ mx_tile_kernel(const MxArgs a) {
   // lie past the inputs, where rows have code 0.
   const int I0 = Q0 * 2, I1 = min(Q1 * 2, (a.G + 1) / 2), T0 = I0 * 2, T1 = I1 * 2;
   // Loads of stage t to the buffer at byte `at`; past the last stage without a
-  // request.  Even stages bring the scales of their super, the second time the
+  // request (no records, and no scalar offset, which the bounds check may
+  // subtract from them).  Even stages bring the scales of their super, the second time the
   // same bytes once more (a branch here would let the compiler move the
   // products of the whole iteration behind it).
   constexpr int kLoads = kRowLoads + kCodeLoads;
@@ -211,11 +212,12 @@ mx_tile_kernel(const MxArgs a) {
       rx.words[2] = t < T1 ? (int)(uint32_t)(left * a.ldx) : 0;
       rw.words[2] = t < T1 ? (int)(uint32_t)code_bytes : 0;
     }
+    const int from = t < T1 ? t : 0;
     if (i < kRowLoads)
-      load_at(rx, lds0 + at + (wave * kRowLoads + i) * 1024, ox[i], t * S::kRowBytes);
+      load_at(rx, lds0 + at + (wave * kRowLoads + i) * 1024, ox[i], from * S::kRowBytes);
     else
       load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i - kRowLoads) * 1024, ow[i - kRowLoads],
-              t * kBlockBytes);
+              from * kBlockBytes);
   };
   auto fill = [&](int at, int t, bool even) __attribute__((always_inline)) {
     if (even) fill_scales(t);

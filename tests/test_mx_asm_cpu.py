@@ -79,3 +79,31 @@ def test_barriers_leave_the_stages_that_are_not_read_next(kernels):
             # the last of them were sent at the step before this one
             behind = sum(sent[(step - 1 - k) % 2] for k in range(buffers - 2))
             assert int(BARRIER.match(body[waits[step]]).group(1)) == behind, f"{name}: step {step}"
+
+
+def test_loads_without_records_have_no_scalar_offset(kernels):
+    """The bounds check may subtract the scalar offset from the records: past
+    the last stage, where there are none, it must be 0 too."""
+    for name, code in kernels.items():
+        body = _loop(code)
+
+        def origin(i, reg):
+            """The instruction that chose `reg` before instruction i, through shifts and products of it."""
+            while True:
+                i -= 1
+                assert i >= 0, (name, reg)
+                m = re.match(r"(s_\w+) (s\d+), (.*)$", body[i])
+                if not m or m.group(2) != reg or m.group(1).startswith("s_cmp"):
+                    continue
+                if not m.group(1).startswith(("s_lshl", "s_mul")):
+                    return body[i]
+                reg = m.group(3).split(",")[0].strip()
+
+        chosen = 0
+        for i, c in enumerate(body):
+            m = re.match(r"buffer_load_dwordx4 v\d+, s\[\d+:\d+\], (s\d+) offen lds", c)
+            if not m:
+                continue
+            chosen += bool(re.match(r"s_cselect_b32 s\d+, s\d+, 0$", origin(i, m.group(1))))
+        loads, _ = _shape(name)
+        assert chosen == 2 * loads, name  # (all but the load of scales, which never passes the last super)
