@@ -119,6 +119,11 @@ mx_stream_kernel(const MxArgs a) {
   const uint8_t* wc = a.codes + (int64_t)sp.group * a.nb * a.gstride * kBlockBytes + lane * 16;
   const uint8_t* ws = a.scales + (int64_t)sp.group * a.nb * a.qstride * kMxScaleBytes + lane * 4;
 
+  // Where this lane's row comes from (tiles of groups have at most 16), asked
+  // for here and looked at when the sums are there.
+  int from = 0;
+  if (a.rows) from = a.rows[sp.first + min(c, sp.rows - 1)];
+
   // This lane's row of each 16: past the last, the last one again.
   const uint8_t* xc[MT];
   const uint8_t* xs[MT];
@@ -307,7 +312,7 @@ mx_stream_kernel(const MxArgs a) {
     if (at >= sp.rows || block * 16 >= width) continue;
     const int p = sp.first + at;
     uint2 bits = mx_bf16x4(out);
-    if (RAW && a.rows && source_row(a, p) < 0) bits = uint2{0u, 0u};
+    if (a.rows && (from < 0 || from >= a.M)) bits = uint2{0u, 0u};  // whatever the weight holds
     *reinterpret_cast<uint2*>(a.y + (int64_t)p * width + block * 16 + 4 * j) = bits;
   }
 }

@@ -334,3 +334,26 @@ def test_a_nan_weight_scale_stays_in_its_channel(w4):
         bad = torch.zeros(64, dtype=torch.bool)
         bad[21] = True
         assert bool(torch.isnan(y[:, bad]).all()) and bool(torch.isfinite(y[:, ~bad]).all())
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts,path", [((3, 2), 1), ((9, 0, 4) + (7,) * 6, 2), ((70, 3, 90), 3)])
+def test_rows_out_of_range_give_zeros_whatever_the_weight(w4, counts, path, gated):
+    """Also where the weight's scales, or row 0 of x, are NaN."""
+    E, N, K, P, M = len(counts), 64, 544, sum(counts), 37
+    assert w4.mx_grouped_linear_plan(M, P, E, N, K).path == path
+    g = gen(P)
+    q, s = weight(g, E * N, K)
+    s[::5, K // 32 - 1] = 255
+    w = w4.mx_pack_weights(ref.pack4(q).cuda(), s.cuda(), n_experts=E)
+    x = torch.randn(M, K, generator=g)
+    x[0, 7] = float("nan")
+    rows = torch.randint(1, M, (P,), generator=g, dtype=torch.int32)
+    bad = [0, 1, P // 2, P - 1]
+    rows[bad] = torch.tensor([-1, M, -2 ** 31, 2 ** 31 - 1], dtype=torch.int32)
+    offsets = torch.cumsum(torch.tensor([0] + list(counts)), 0).to(torch.int32)
+    y = w4.mx_grouped_linear(x.cuda(), w, offsets.cuda(), rows=rows.cuda(), gated=gated).cpu()
+    assert bool((y[bad] == 0).all())
+    good = torch.ones(P, dtype=torch.bool)
+    good[bad] = False
+    assert bool(torch.isnan(y[good]).any(1).all()) and bool(torch.isfinite(y[good]).any(1).all())
