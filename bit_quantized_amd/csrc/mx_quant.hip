@@ -200,11 +200,12 @@ rows_kernel(const uint8_t* __restrict__ x, int K, int rule, uint8_t* __restrict_
 
 // ------------------------------------------------------------ weight layout
 
-// Thread: 16 bytes of a codes block (lane L of block (nb, g)); blocks that only
-// fill the stride are zero.
+// Thread: 16 bytes of a codes block (lane L of block (nb, g)), of a launch whose
+// first are unit `first`; blocks that only fill the stride are zero.
 __global__ void __launch_bounds__(kThreads)
-pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t units, int K, int stride, uint8_t* __restrict__ packed) {
-  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t first, int64_t units, int K, int stride,
+                  uint8_t* __restrict__ packed) {
+  const int64_t t = first + (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units) return;
   const int L = (int)(t & 63), j = L >> 4, c = L & 15;
   const int64_t blk = t >> 6, nb = blk / stride;
@@ -216,8 +217,9 @@ pack_codes_kernel(const uint8_t* __restrict__ codes, int64_t units, int K, int s
 // Thread: the four scale bytes of lane L of super (nb, q); the last 256
 // threads clear the 1024 bytes behind the planes.
 __global__ void __launch_bounds__(kThreads)
-pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t units, int K, int stride, uint8_t* __restrict__ plane) {
-  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t first, int64_t units, int K, int stride,
+                   uint8_t* __restrict__ plane) {
+  const int64_t t = first + (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units + 256) return;
   uint32_t v = 0;
   if (t < units) {
@@ -233,8 +235,9 @@ pack_scales_kernel(const uint8_t* __restrict__ scales, int64_t units, int K, int
   reinterpret_cast<uint32_t*>(plane)[t] = v;
 }
 __global__ void __launch_bounds__(kThreads)
-unpack_codes_kernel(const uint8_t* __restrict__ packed, int64_t units, int K, int stride, uint8_t* __restrict__ codes) {
-  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+unpack_codes_kernel(const uint8_t* __restrict__ packed, int64_t first, int64_t units, int K, int stride,
+                    uint8_t* __restrict__ codes) {
+  const int64_t t = first + (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units) return;
   const int L = (int)(t & 63), j = L >> 4, c = L & 15;
   const int64_t blk = t >> 6, nb = blk / stride;
@@ -243,8 +246,9 @@ unpack_codes_kernel(const uint8_t* __restrict__ packed, int64_t units, int K, in
     *reinterpret_cast<v4u_rows*>(codes + ((nb * 16 + c) * K + k) / 2) = reinterpret_cast<const v4u_rows*>(packed)[t];
 }
 __global__ void __launch_bounds__(kThreads)
-unpack_scales_kernel(const uint8_t* __restrict__ plane, int64_t units, int K, int stride, uint8_t* __restrict__ scales) {
-  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+unpack_scales_kernel(const uint8_t* __restrict__ plane, int64_t first, int64_t units, int K, int stride,
+                     uint8_t* __restrict__ scales) {
+  const int64_t t = first + (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= units) return;
   const int L = (int)(t & 63), j = L >> 4, c = L & 15;
   const int64_t sup = t >> 6, nb = sup / stride;
@@ -272,36 +276,40 @@ void typed(int fmt, int f32, F&& f) {
   }
 }
 
-// Chunks of one launch: the grid stays below 2^31 / 256 workgroups.
+// Chunks of one launch: a launch has fewer than 2^32 threads.
 constexpr int64_t kMostChunks = (int64_t)1 << 30;
+
+// f(first, grid) for launches of a thread an item.
+template <typename F>
+void passes(int64_t items, F&& f) {
+  for (int64_t t = 0; t < items; t += kMostChunks)
+    f(t, dim3(blocks_of(items - t < kMostChunks ? items - t : kMostChunks)));
+}
 
 }  // namespace
 
 hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t st) {
   const int64_t total = a.M * a.K / 8;
-  for (int64_t t = 0; t < total; t += kMostChunks) {
-    const int64_t n = total - t < kMostChunks ? total - t : kMostChunks;
+  passes(total, [&](int64_t t, dim3 grid) {
     typed(a.fmt, a.f32, [&](auto fmt, auto f32) {
-      hipLaunchKernelGGL((quant_kernel<decltype(fmt)::value, decltype(f32)::value>), dim3(blocks_of(n)),
-                         dim3(kThreads), 0, st,
-                         static_cast<const uint8_t*>(a.x) + t * 8 * (a.f32 ? 4 : 2), n, a.rule,
+      hipLaunchKernelGGL((quant_kernel<decltype(fmt)::value, decltype(f32)::value>), grid, dim3(kThreads), 0, st,
+                         static_cast<const uint8_t*>(a.x) + t * 8 * (a.f32 ? 4 : 2), total - t, a.rule,
                          a.codes + t * (a.fmt == kFp4 ? 4 : 8), a.scales + t / 4);
     });
-  }
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t M, int64_t K,
                              void* y, int f32, hipStream_t st) {
   const int64_t total = M * K / 8;
-  for (int64_t t = 0; t < total; t += kMostChunks) {
-    const int64_t n = total - t < kMostChunks ? total - t : kMostChunks;
+  passes(total, [&](int64_t t, dim3 grid) {
     typed(fmt, f32, [&](auto fm, auto fl) {
-      hipLaunchKernelGGL((dequant_kernel<decltype(fm)::value, decltype(fl)::value>), dim3(blocks_of(n)),
-                         dim3(kThreads), 0, st, codes + t * (fmt == kFp4 ? 4 : 8), scales + t / 4, n,
+      hipLaunchKernelGGL((dequant_kernel<decltype(fm)::value, decltype(fl)::value>), grid, dim3(kThreads), 0, st,
+                         codes + t * (fmt == kFp4 ? 4 : 8), scales + t / 4, total - t,
                          static_cast<uint8_t*>(y) + t * 8 * (f32 ? 4 : 2));
     });
-  }
+  });
   return hipGetLastError();
 }
 
@@ -345,9 +353,13 @@ hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int64_t N
                           hipStream_t st) {
   const int cs = (int)mx_code_stride(K), ss = (int)mx_scale_stride(K);
   const int64_t uc = N / 16 * cs * 64, us = N / 16 * ss * 64;
-  hipLaunchKernelGGL(pack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, codes, uc, (int)K, cs, packed);
-  hipLaunchKernelGGL(pack_scales_kernel, dim3(blocks_of(us + 256)), dim3(kThreads), 0, st, scales, us, (int)K, ss,
-                     packed + mx_scales_offset(N, K));
+  passes(uc, [&](int64_t t, dim3 grid) {
+    hipLaunchKernelGGL(pack_codes_kernel, grid, dim3(kThreads), 0, st, codes, t, uc, (int)K, cs, packed);
+  });
+  passes(us + 256, [&](int64_t t, dim3 grid) {
+    hipLaunchKernelGGL(pack_scales_kernel, grid, dim3(kThreads), 0, st, scales, t, us, (int)K, ss,
+                       packed + mx_scales_offset(N, K));
+  });
   return hipGetLastError();
 }
 
@@ -355,9 +367,13 @@ hipError_t launch_mx_unpack(const uint8_t* packed, int64_t N, int64_t K, uint8_t
                             hipStream_t st) {
   const int cs = (int)mx_code_stride(K), ss = (int)mx_scale_stride(K);
   const int64_t uc = N / 16 * cs * 64, us = N / 16 * ss * 64;
-  hipLaunchKernelGGL(unpack_codes_kernel, dim3(blocks_of(uc)), dim3(kThreads), 0, st, packed, uc, (int)K, cs, codes);
-  hipLaunchKernelGGL(unpack_scales_kernel, dim3(blocks_of(us)), dim3(kThreads), 0, st,
-                     packed + mx_scales_offset(N, K), us, (int)K, ss, scales);
+  passes(uc, [&](int64_t t, dim3 grid) {
+    hipLaunchKernelGGL(unpack_codes_kernel, grid, dim3(kThreads), 0, st, packed, t, uc, (int)K, cs, codes);
+  });
+  passes(us, [&](int64_t t, dim3 grid) {
+    hipLaunchKernelGGL(unpack_scales_kernel, grid, dim3(kThreads), 0, st, packed + mx_scales_offset(N, K), t, us,
+                       (int)K, ss, scales);
+  });
   return hipGetLastError();
 }
 

@@ -271,3 +271,32 @@ def test_experts_past_2_to_32_bytes(w4, act, counts):  # noqa: F811
             err, _ = ref.slack(xv[run], wv, act)
             cols = slice(rows.start - e * N, rows.stop - e * N)
             check(y[run, cols], xv[run] @ wv.t().contiguous(), err, f"expert {e}")
+
+
+def test_packing_past_2_to_32_pieces(w4):  # noqa: F811
+    """68.9e9 bytes of codes: more pieces of 16 bytes than one launch has threads."""
+    K, some = 8192, 4096
+    N = (1 << 36) // (K // 2) + some
+    g = gen(9)
+    part = torch.randint(0, 256, (some, K // 2), generator=g, dtype=torch.uint8).cuda()
+    part_s = torch.randint(0, 255, (some, K // 32), generator=g, dtype=torch.uint8).cuda()
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((N, K // 32), dtype=torch.uint8, device="cuda")
+    codes.view(-1, some, K // 2)[:] = part
+    scales.view(-1, some, K // 32)[:] = part_s
+    w, want = w4.mx_pack_weights(codes, scales), w4.mx_pack_weights(part, part_s).buf
+    stride, per = (K // 128 + 1) * 1024, (K // 512 + 1) * 256  # of 16 channels; both counts made odd
+    plane = N // 16 * stride
+    n, m = some // 16 * stride, some // 16 * per
+    for at in (0, N // some // 2, N // some - 1):
+        assert torch.equal(w.buf[at * n:(at + 1) * n], want[:n]), at
+        assert torch.equal(w.buf[plane + at * m:plane + (at + 1) * m], want[n:n + m]), at
+    codes.zero_()
+    scales.zero_()
+    del codes, scales
+    back = w4.mx_unpack_weights(w)
+    for at in (0, N // some // 2, N // some - 1):
+        assert torch.equal(back.codes[at * some:(at + 1) * some], part), at
+        assert torch.equal(back.scales[at * some:(at + 1) * some], part_s), at
+    del w, back
+    torch.cuda.empty_cache()
