@@ -6,13 +6,13 @@
 // code blocks, which are operands as they lie.  16-byte chunk i of a row is
 // kept at another place, i ^ (row / 4 % 4) or i ^ (row / 2 % 8), so that the
 // 16 rows of a quarter of an operand read take 256 bytes of different banks.
-// Scales come once per 256 inputs (a load has those of 512).
+// Scales come 512 inputs at a time, one register a lane of those of 32 rows.
 //
 // A wavefront multiplies half steps of 64 inputs, with the operands of one in
 // registers while it reads those of the next.  At the last half step of a
 // stage all of the stage is in registers: one barrier there, behind the first
-// products, frees its buffer for the stage after those in flight.  Three to
-// six buffers keep loads on their way behind the one that the barrier waits
+// products, frees its buffer for the stage after those in flight.  Three or
+// four buffers keep loads on their way behind the one that the barrier waits
 // for.
 //
 // Measured: 4096 rows 3584 -> 18944 in 4 bits 157 to 165 us (3.4 PFLOP/s), 2048
@@ -111,23 +111,22 @@ struct Shape {
   static constexpr int kRowKiB = kRows * kRowBytes / 1024, kCodeKiB = kBlocks;
   static constexpr int kStageBytes = (kRowKiB + kCodeKiB) * 1024;
   static constexpr int kScaleKiB = (kRows + 16 * kBlocks) / 64;
-  // As many buffers as half of a compute unit's LDS holds (of the wide tiles,
-  // which run alone, all of it), at most six: scales are kept of two supers,
-  // and the sixth stage on may begin the super after the next when the last
-  // scales of this one have just been read.  Groups, whose many tiles are
-  // short, take a third where that holds three buffers: 4096 rows of 128
-  // groups, 2048 inputs: 53 us in three buffers, three workgroups to a compute
-  // unit, 57 in six and two; but 33 rows 18944 -> 3584 15 in four, 16.6 in three.
-  static constexpr int kFixed = 2 * kScaleKiB * 1024;
+  // As many buffers as half of a compute unit's LDS holds (of workgroups of
+  // eight wavefronts, which run alone, all of it), at most four.  Groups, whose
+  // many tiles are short, take a third where that holds three buffers: 4096
+  // rows of 128 groups, 2048 inputs: 53 us in three buffers, three workgroups
+  // to a compute unit, 57 in six and two; but 33 rows 18944 -> 3584 15 in four,
+  // 16.6 in three.
+  static constexpr int kFixed = kScaleKiB * 1024;
   static constexpr bool kThird = KIND >= kGroups && kBlocks <= 8 && 160 * 1024 / 3 - kFixed >= 3 * kStageBytes;
-  static constexpr int kRoom = (kThird ? 160 * 1024 / 3 : (kBlocks > 8 ? 160 : 80) * 1024) - kFixed;
-  static constexpr int kBuffers = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
-  static constexpr int kLds = kBuffers * kStageBytes + 2 * kScaleKiB * 1024;
+  static constexpr int kRoom = (kThird ? 160 * 1024 / 3 : (kWaves > 4 ? 160 : 80) * 1024) - kFixed;
+  static constexpr int kBuffers = kRoom / kStageBytes < 4 ? kRoom / kStageBytes : 4;
+  static constexpr int kLds = kBuffers * kStageBytes + kFixed;
   static_assert(kBuffers >= 3, "a stage in use, one to read next, one on its way");
 };
 
 template <int FMT, int WM, int WN, int FM, int FN, int KIND>
-__global__ void __launch_bounds__(64 * WM * WN)
+__global__ void __launch_bounds__(64 * WM * WN, 2)
 mx_tile_kernel(const MxArgs a) {
   using S = Shape<FMT, WM, WN, FM, FN, KIND>;
   constexpr bool SPLIT = KIND == kSlices, GATED = KIND == kGated;
@@ -167,7 +166,6 @@ mx_tile_kernel(const MxArgs a) {
   constexpr int kRowLoads = S::kRowKiB / S::kWaves;
   constexpr int kCodeLoads = S::kCodeKiB / S::kWaves;
   static_assert(S::kRowKiB % S::kWaves == 0 && S::kCodeKiB % S::kWaves == 0, "whole loads");
-  static_assert(S::kScaleKiB <= S::kWaves, "one load of scales");
   uint32_t ox[kRowLoads], ow[kCodeLoads];
   constexpr int kChunks = S::kRowBytes / 16;
   auto place = [&](int r) __attribute__((always_inline)) { return FMT == kFp4 ? r >> 2 & 3 : r >> 1 & 7; };
@@ -180,33 +178,33 @@ mx_tile_kernel(const MxArgs a) {
 #pragma unroll
   for (int i = 0; i < kCodeLoads; ++i)
     ow[i] = (uint32_t)block_of(wave * kCodeLoads + i) * a.gstride * kBlockBytes + lane * 16;
-  // One KiB of scales each, of rows or of blocks (wavefronts past the last KiB
-  // load it as well).
-  const int scale_kib = min(wave, S::kScaleKiB - 1);
-  const bool row_scales = scale_kib < S::kRows / 64;
-  const LdsSource rs = lds_source(row_scales ? a.qs + base * a.lds : a.scales + (int64_t)sp.group * a.nb * a.qstride * kMxScaleBytes,
-                                  row_scales ? left * a.lds : (int64_t)a.nb * a.qstride * kMxScaleBytes);
-  const int scale_step = row_scales ? kMxRowScale : kMxScaleBytes;
-  const uint32_t os = row_scales ? (uint32_t)source(scale_kib * 64 + lane) * a.lds
-                                 : (uint32_t)block_of((scale_kib - S::kRows / 64) * 4 + (lane >> 4)) * a.qstride * kMxScaleBytes +
-                                       (lane & 15) * 16;
+  // Scales of 512 inputs, rows' before blocks', a KiB at a time (wavefronts
+  // past the last KiB load it as well).
+  constexpr int kScaleLoads = (S::kScaleKiB + S::kWaves - 1) / S::kWaves;
+  LdsSource rs[kScaleLoads];
+  uint32_t os[kScaleLoads];
+  int scale_at[kScaleLoads], scale_step[kScaleLoads];
   const int lds0 = uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
-  auto scales_at = [&](int buf) __attribute__((always_inline)) {
-    return S::kBuffers * S::kStageBytes + buf * S::kScaleKiB * 1024;
-  };
+  constexpr int kScales = S::kBuffers * S::kStageBytes;
+#pragma unroll
+  for (int i = 0; i < kScaleLoads; ++i) {
+    const int kib = min(i * S::kWaves + wave, S::kScaleKiB - 1);
+    const bool rows = kib < S::kRows / 64;
+    rs[i] = lds_source(rows ? a.qs + base * a.lds : a.scales + (int64_t)sp.group * a.nb * a.qstride * kMxScaleBytes,
+                       rows ? left * a.lds : (int64_t)a.nb * a.qstride * kMxScaleBytes);
+    os[i] = rows ? (uint32_t)source(kib * 64 + lane) * a.lds
+                 : (uint32_t)block_of((kib - S::kRows / 64) * 4 + (lane >> 4)) * a.qstride * kMxScaleBytes +
+                       (lane & 15) * 16;
+    scale_at[i] = lds0 + kScales + kib * 1024;
+    scale_step[i] = rows ? kMxRowScale : kMxScaleBytes;
+  }
   // Stages of 128 inputs T0 .. T1 - 1, two to an iteration; the last one may
   // lie past the inputs, where rows have code 0.
   const int I0 = Q0 * 2, I1 = min(Q1 * 2, (a.G + 1) / 2), T0 = I0 * 2, T1 = I1 * 2;
   // Loads of stage t to the buffer at byte `at`; past the last stage without a
   // request (no records, and no scalar offset, which the bounds check may
-  // subtract from them).  Even stages bring the scales of their super, the second time the
-  // same bytes once more (a branch here would let the compiler move the
-  // products of the whole iteration behind it).
+  // subtract from them).
   constexpr int kLoads = kRowLoads + kCodeLoads;
-  auto fill_scales = [&](int t) __attribute__((always_inline)) {
-    const int q = min(t, T1 - 1) >> 2;
-    load_at(rs, lds0 + scales_at((q - Q0) & 1) + scale_kib * 1024, os, q * scale_step);
-  };
   auto fill_one = [&](int i, int at, int t) __attribute__((always_inline)) {
     if (i == 0) {
       rx.words[2] = t < T1 ? (int)(uint32_t)(left * a.ldx) : 0;
@@ -219,19 +217,19 @@ mx_tile_kernel(const MxArgs a) {
       load_at(rw, lds0 + at + (S::kRowKiB + wave * kCodeLoads + i - kRowLoads) * 1024, ow[i - kRowLoads],
               from * kBlockBytes);
   };
-  auto fill = [&](int at, int t, bool even) __attribute__((always_inline)) {
-    if (even) fill_scales(t);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) fill_one(i, at, t);
+  // Scales of super q (or of the last), where those of the one before have
+  // been read.
+  auto fill_scale = [&](int i, int q) __attribute__((always_inline)) {
+    load_at(rs[i], scale_at[i], os[i], min(q, (T1 - 1) >> 2) * scale_step[i]);
   };
 
   // ---- operands: of two half steps of 64 inputs, or (small wavefront tiles,
   // whose few products would not cover the reads) of two whole steps; scales
-  // by half of a step
+  // of a super, by half of a step, those of this iteration in the lower bytes
   constexpr bool kDeep = FM * FN <= 4;
   constexpr int kSets = kDeep ? 2 : 1;
   v4i w[kSets][2][FN], x[kSets][2][FM][kUnits];
-  int sw[2][FN], sx[2][FM], sw1[2][FN], sx1[2][FM];
+  uint32_t sw[2][FN], sx[2][FM], sw1[2][FN], sx1[2][FM];
   int x_at[kChunks / 2];  // this lane's row of the first 32, chunks 2 i and 2 i + 1 of it
 #pragma unroll
   for (int i = 0; i < kChunks / 2; ++i)
@@ -249,15 +247,12 @@ mx_tile_kernel(const MxArgs a) {
       w[set][h][i - FM * kUnits] =
           *reinterpret_cast<const v4i*>(lds + at + w_at + (i - FM * kUnits) * 2048 + h * 512);
   };
-  // scale i of half h (an iteration's two steps have the upper or the lower
-  // two of four bytes)
   constexpr int kScaleReads = FM + FN;
-  auto read_scale = [&](int i, int h, int it, int (&dw)[FN], int (&dx)[FM]) __attribute__((always_inline)) {
-    const int at = scales_at(((it >> 1) - Q0) & 1) + 2 * (it & 1);
+  auto read_scale = [&](int i, int h, uint32_t (&dw)[2][FN], uint32_t (&dx)[2][FM]) __attribute__((always_inline)) {
     if (i < FM)
-      dx[i] = *reinterpret_cast<const uint16_t*>(lds + at + sx_at + i * 512 + h * 8);
+      dx[h][i] = *reinterpret_cast<const uint32_t*>(lds + kScales + sx_at + i * 512 + h * 8);
     else
-      dw[i - FM] = *reinterpret_cast<const uint16_t*>(lds + at + sw_at + (i - FM) * 512 + h * 128);
+      dw[h][i - FM] = *reinterpret_cast<const uint32_t*>(lds + kScales + sw_at + (i - FM) * 512 + h * 128);
   };
 
   v16f_mx acc[FM][FN];
@@ -274,17 +269,24 @@ mx_tile_kernel(const MxArgs a) {
     v8i_mx xv;
     if constexpr (FMT == kFp4) xv = mx_wide(x[set][h][m][0]);
     else xv = mx_wide(x[set][h][m][0], x[set][h][m][kUnits - 1]);
-    acc[m][n] = mx_mfma32<FMT, decltype(sc)::value>(mx_wide(w[set][h][n]), xv, acc[m][n], sw[h][n], sx[h][m]);
+    acc[m][n] = mx_mfma32<FMT, decltype(sc)::value>(mx_wide(w[set][h][n]), xv, acc[m][n], (int)sw[h][n], (int)sx[h][m]);
   };
 
   if (T0 < T1) {
 #pragma unroll
-    for (int b = 0; b < S::kBuffers; ++b) fill(b * S::kStageBytes, T0 + b, b % 2 == 0);
-    stage_barrier<(S::kBuffers - 1) * kLoads + (S::kBuffers - 1) / 2>();
+    for (int i = 0; i < kScaleLoads; ++i) fill_scale(i, Q0);
+#pragma unroll
+    for (int b = 0; b < S::kBuffers; ++b)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) fill_one(i, b * S::kStageBytes, T0 + b);
+    stage_barrier<(S::kBuffers - 1) * kLoads>();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < kScaleReads; ++i) read_scale(i, h, sw, sx);
+    }
 #pragma unroll
     for (int h = 0; h < (kDeep ? 2 : 1); ++h) {
-#pragma unroll
-      for (int i = 0; i < kScaleReads; ++i) read_scale(i, h, I0, sw[h], sx[h]);
 #pragma unroll
       for (int i = 0; i < kReads; ++i) read_one(i, 0, h, 0);
     }
@@ -299,11 +301,16 @@ mx_tile_kernel(const MxArgs a) {
       constexpr int s = decltype(sc)::value;
       const int next = own == (S::kBuffers - 1) * S::kStageBytes ? 0 : own + S::kStageBytes;
       const int t = 2 * it + s + S::kBuffers;  // the stage that takes this one's buffer
-      constexpr bool even = (s + S::kBuffers) % 2 == 0;
-      // loads behind the stage that is read next: kBuffers - 2 stages, the
-      // first of step s; the even ones with a load of scales
+      // Every iteration loads the scales of the next super, behind the first
+      // of its barriers: all wavefronts have read this one's.  (In a super's
+      // second iteration that brings the same bytes once more: a branch here
+      // would let the compiler move the products of the whole iteration behind
+      // it.)  Two barriers later, where an iteration's first one leaves only
+      // the rows and codes of the stages behind the one that is read next,
+      // they are there, and the second step reads them.
       constexpr int kBehind = S::kBuffers - 2;
-      constexpr int kLeft = kBehind * kLoads + (kBehind + (s == 0 ? 1 : 0)) / 2;
+      constexpr int kLeft = kBehind * kLoads + (s == 1 ? kScaleLoads : 0);
+      static_assert(kBehind <= 2, "the scales come before what is left");
       constexpr int kHalves = kDeep ? 1 : 2;  // parts of a step with reads of their own
 #pragma unroll
       for (int part = 0; part < kHalves; ++part) {
@@ -311,8 +318,8 @@ mx_tile_kernel(const MxArgs a) {
         constexpr int kSlots = 2 * kProducts / kHalves;
         // this part's items, in their order
         constexpr int kOperands = kDeep ? 2 * kReads : kReads;
-        const int scales = kDeep ? (s == 1 ? 2 * kScaleReads : 0) : (s == part ? kScaleReads : 0);
-        const int loads = last ? kLoads + (even ? 1 : 0) : 0;
+        const int scales = s == 1 ? 2 * kScaleReads / kHalves : 0;
+        const int loads = last ? kLoads + (s == 0 ? kScaleLoads : 0) : 0;
         const int items = kOperands + scales + loads;
 #pragma unroll
         for (int slot = 0; slot < kSlots; ++slot) {
@@ -325,25 +332,25 @@ mx_tile_kernel(const MxArgs a) {
               else read_one(i, 0, 1 - part, last ? next : own);
             } else if (i < kOperands + scales) {
               const int k = i - kOperands;
-              if constexpr (kDeep) read_scale(k % kScaleReads, k / kScaleReads, it + 1, sw1[k / kScaleReads], sx1[k / kScaleReads]);
-              else if (part == 0) read_scale(k, 1, it, sw[1], sx[1]);  // of this iteration's odd halves
-              else read_scale(k, 0, it + 1, sw1[0], sx1[0]);           // of the next one's even ones
+              read_scale(k % kScaleReads, kDeep ? k / kScaleReads : part, sw1, sx1);
             } else {
               const int k = i - kOperands - scales;
-              if (even && k == 0) fill_scales(t);
-              else fill_one(k - (even ? 1 : 0), own, t);
+              if (s == 0 && k < kScaleLoads) fill_scale(k, (it >> 1) + 1);
+              else fill_one(k - (s == 0 ? kScaleLoads : 0), own, t);
             }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       if constexpr (s == 1) {
+        // the upper two bytes, or the next super's
+        const uint32_t pick = it & 1 ? 0x07060504u : 0x0C0C0302u;
 #pragma unroll
-        for (int h = 0; h < (kDeep ? 2 : 1); ++h) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int m = 0; m < FM; ++m) sx[h][m] = sx1[h][m];
+          for (int m = 0; m < FM; ++m) sx[h][m] = __builtin_amdgcn_perm(sx1[h][m], sx[h][m], pick);
 #pragma unroll
-          for (int n = 0; n < FN; ++n) sw[h][n] = sw1[h][n];
+          for (int n = 0; n < FN; ++n) sw[h][n] = __builtin_amdgcn_perm(sw1[h][n], sw[h][n], pick);
         }
       }
       own = next;
@@ -443,7 +450,11 @@ hipError_t launch_shape(const MxArgs& a, const MxPlan& p, bool gated, unsigned b
 template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
   if (p.bm == 256 && p.bn == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
-  if (p.bm == 128 && p.bn == 256) return launch_shape<FMT, 2, 4, 2, 2>(a, p, gated, blocks, st);
+  // in 4 bits two workgroups of four wavefronts share a compute unit
+  if (p.bm == 128 && p.bn == 256) {
+    if constexpr (FMT == kFp4) return launch_shape<FMT, 2, 2, 2, 4>(a, p, gated, blocks, st);
+    else return launch_shape<FMT, 2, 4, 2, 2>(a, p, gated, blocks, st);
+  }
   if (p.bm == 128 && p.bn == 128) return launch_shape<FMT, 2, 2, 2, 2>(a, p, gated, blocks, st);
   if (p.bm == 64 && p.bn == 128) return launch_shape<FMT, 2, 2, 1, 2>(a, p, gated, blocks, st);
   return hipErrorInvalidValue;
