@@ -17,13 +17,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles of the tile kernel.  `one` and `two`: microseconds of a step of 128
 // inputs where a compute unit has one of them, and where it has as many as fit
-// (`fit`); 3584 and 18944 inputs, either format, 16 to 4096 rows, +- 20 %.
+// (`fit`), with rows of 4 and of 8 bits; 2048 to 18944 inputs, 33 to 4096 rows,
+// +- 20 %.
 struct TileShape {
   int bm, bn, fit;
   double one, two;
 };
-constexpr TileShape kShapes[] = {{64, 128, 2, 0.35, 0.55}, {128, 128, 2, 0.47, 0.82}, {128, 256, 1, 0.80, 0.80},
-                                 {256, 256, 1, 1.25, 1.25}};
+constexpr TileShape kShapes[2][4] = {
+    {{64, 128, 2, 0.24, 0.46}, {128, 128, 2, 0.42, 0.80}, {128, 256, 2, 0.66, 1.28}, {256, 256, 1, 1.22, 1.22}},
+    {{64, 128, 2, 0.28, 0.54}, {128, 128, 2, 0.48, 0.88}, {128, 256, 1, 0.80, 0.80}, {256, 256, 1, 1.35, 1.35}}};
 constexpr int kSplitMost = 16;
 
 // Microseconds of `tiles` tiles of `steps` steps each.
@@ -33,12 +35,14 @@ double tile_cost(const TileShape& s, int64_t tiles, double steps) {
   return steps * (double(tiles / round) * s.two + (rest == 0 ? 0.0 : rest <= cus ? s.one : s.two));
 }
 
-// The linear's tiles: the shape and split of least cost.  A split adds a
-// launch and its sums, written and read at 4 TB/s (33 rows 18944 -> 3584: 16.8
-// us of 8 slices, 17.6 of 9, 52 unsplit).
-double plan_tiles(MxPlan& p, int64_t M, int64_t N, int64_t Q) {
+// The linear's tiles: the shape and split of least cost (over 54 sizes 1 % from
+// the fastest of a sweep, at worst 15: 1024 rows 18944 -> 3584 in 8 bits, 88 us
+// of 128 x 128, 77 of 128 x 256 in halves).  A split adds a launch and its
+// sums, written and read at 4 TB/s (33 rows 18944 -> 3584: 16.8 us of 8 slices,
+// 17.6 of 9, 52 unsplit).
+double plan_tiles(MxPlan& p, int64_t M, int64_t N, int64_t Q, int fmt) {
   double best = 1e30;
-  for (const TileShape& s : kShapes) {
+  for (const TileShape& s : kShapes[fmt]) {
     const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
     for (int64_t k = 1; k == 1 || (k <= kSplitMost && k <= Q / 2 && tiles * k <= device_cus()); ++k) {
       if (ceil_div(Q, ceil_div(Q, k)) != k) continue;  // as long with fewer
@@ -94,7 +98,7 @@ MxPlan mx_plan(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
   if (token_fits(P, N, K, fmt)) {
     p.path = kMxToken;
   } else if (!E) {
-    const double tiles = M > 16 ? plan_tiles(p, M, N, Q) : 1e30;
+    const double tiles = M > 16 ? plan_tiles(p, M, N, Q, fmt) : 1e30;
     p.path = kMxTile;
     if (M <= 16 || (M <= kStreamRows && stream_cost(M, N, K, fmt) < tiles)) {
       p.path = kMxStream;
@@ -104,10 +108,11 @@ MxPlan mx_plan(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
     }
   } else {
     // By the rows of a group, evenly shared (the groups' own numbers are on
-    // the device): 64 tokens x 8 of 128 (4 rows a group) take 31 us streamed,
-    // 256 (16 rows) 47, and 37 in tiles of 64; 64 rows a group 51, and 57 in
-    // tiles of 128; 384 rows 220, against 224 (128 x 128), 228 (256 x 256) and
-    // 261 (64 x 128).
+    // the device).  64 tokens x 8 of 128 (4 rows a group) take 31 us streamed,
+    // 256 (16 rows) 47, and 37 in tiles of 64.  With 4-bit rows 64 rows a group
+    // take 46 in tiles of 64 x 128, 51 in the next; 96 rows 98, 98 (128 x 128),
+    // 90 (128 x 256) and 118 (256 x 256); 576 rows 351, 297, 254 and 292.  With
+    // 8-bit rows 192 rows take 167, 162, 163 and 175.
     const double per = double(P) / E;
     p.path = kMxTile;
     if (per <= kStreamPerGroup) {
@@ -115,7 +120,7 @@ MxPlan mx_plan(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
       p.bn = 32;  // (of the plain product: 27.1 against 29.7 us at 4 rows a group)
     } else if (per <= 80) {
       p.bm = 64, p.bn = 128;
-    } else if (per <= 256 || N <= 256) {
+    } else if ((fmt == kFp8 && per <= 256) || N <= 256) {
       p.bm = 128, p.bn = 128;
     } else if (per <= 768) {
       p.bm = 128, p.bn = 256;
@@ -159,7 +164,7 @@ int64_t workspace_bound(int64_t M, int64_t P, int E, int64_t N, int64_t K, int f
   // ksplit times the tiles is at most the compute units; no split of fewer than four supers
   int64_t parts = 0;
   const int64_t Q = mx_supers(K);
-  for (const TileShape& s : kShapes)
+  for (const TileShape& s : kShapes[fmt])
     if (Q >= 4 && ceil_div(N, s.bn) * 2 <= device_cus())  // (else never split)
       parts = std::max(parts, std::min((int64_t)device_cus() * s.bm * s.bn, std::min<int64_t>(kSplitMost, Q / 2) * M * N));
   return std::max<int64_t>(n + round_up256(parts * 4), 256);

@@ -178,7 +178,7 @@ TILES = [
     (2048, 8192, 1056, (256, 256)), (1030, 12816, 288, (256, 256)), (300, 18960, 416, (128, 256)),
     (517, 4112, 672, (128, 128)), (200, 8208, 288, (128, 128)), (150, 4112, 288, (64, 128)), (65, 4112, 672, (64, 128))]
 SLICES = [(33, 256, 18944), (100, 144, 4128), (513, 528, 16416), (70, 2064, 9248), (700, 3584, 18944),
-          (130, 6544, 17472)]
+          (130, 6544, 17472), (65, 6160, 9248), (600, 6544, 14368)]
 STREAMED = [(16, 4112, 2912, 16), (17, 528, 1056, 16), (40, 4112, 544, 16), (64, 4096, 1024, 16), (20, 8208, 160, 32),
             (48, 8208, 160, 32), (60, 8208, 160, 32)]
 LINEAR = SIZES + [c[:3] for c in TILES] + SLICES + [c[:3] for c in STREAMED]
