@@ -16,10 +16,10 @@
 // for.
 //
 // Measured: 4096 rows 3584 -> 18944 in 4 bits 157 to 165 us (3.4 PFLOP/s), 2048
-// rows 18944 -> 3584 in 8 bits 106 to 120 (2.4).  The matrix cores are busy for
-// 46 and 60 % of the cycles, LDS reads for 34 and 35 %, and the clock falls to
-// 1.9 and 2.0 GHz: the products of random operands alone, without a load or an
-// LDS read, reach 6.4 and 3.9 PFLOP/s here.
+// rows 18944 -> 3584 in 8 bits 106 to 127 (2.2 to 2.6).  The matrix cores are
+// busy for 45 and 60 % of the cycles, LDS reads for 34 and 35 %, and the clock
+// falls to 1.8 and 2.0 GHz: the products of random operands alone, without a
+// load or an LDS read, reach 6.4 and 3.9 PFLOP/s here.
 #include "mx.h"
 
 #include <type_traits>
@@ -450,7 +450,9 @@ hipError_t launch_shape(const MxArgs& a, const MxPlan& p, bool gated, unsigned b
 template <int FMT>
 hipError_t launch_fmt(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
   if (p.bm == 256 && p.bn == 256) return launch_shape<FMT, 4, 2, 2, 4>(a, p, gated, blocks, st);
-  // in 4 bits two workgroups of four wavefronts share a compute unit
+  // In 4 bits two workgroups of four wavefronts share a compute unit, one's
+  // products beside the other's first loads and outputs: 24576 gated rows of 64
+  // groups 195 us, 227 of one with eight.  In 8 bits LDS has no room for two.
   if (p.bm == 128 && p.bn == 256) {
     if constexpr (FMT == kFp4) return launch_shape<FMT, 2, 2, 2, 4>(a, p, gated, blocks, st);
     else return launch_shape<FMT, 2, 4, 2, 2>(a, p, gated, blocks, st);
