@@ -357,3 +357,14 @@ def test_rows_out_of_range_give_zeros_whatever_the_weight(w4, counts, path, gate
     good = torch.ones(P, dtype=torch.bool)
     good[bad] = False
     assert bool(torch.isnan(y[good]).any(1).all()) and bool(torch.isfinite(y[good]).any(1).all())
+
+
+@pytest.mark.parametrize("act", FMTS)
+@pytest.mark.parametrize("per,path", [({3: 1, 127: 2, 128: 1, 700: 4, 1023: 3}, 1), ({0: 9, 511: 40, 512: 17, 1022: 3}, 2),
+                                      ({0: 700, 255: 64, 256: 65, 800: 9000, 1023: 130}, 3)])
+def test_grouped_of_1024_groups(w4, act, per, path):
+    """The most groups: rows in the first, the last and those around the borders of the lists."""
+    counts = tuple(per.get(e, 0) for e in range(1024))
+    assert w4.mx_grouped_linear_plan(37, sum(counts) + 2, 1024, 64, 160, act).path == path
+    grouped_case(w4, counts, 64, 160, act, tail=2)
+    grouped_case(w4, counts, 64, 160, act, tail=2, gather=False, gated=True)
