@@ -368,3 +368,30 @@ def test_grouped_of_1024_groups(w4, act, per, path):
     assert w4.mx_grouped_linear_plan(37, sum(counts) + 2, 1024, 64, 160, act).path == path
     grouped_case(w4, counts, 64, 160, act, tail=2)
     grouped_case(w4, counts, 64, 160, act, tail=2, gather=False, gated=True)
+
+
+@pytest.mark.parametrize("act", FMTS)
+@pytest.mark.parametrize("M", [1, 17, 70])
+def test_most_inputs(w4, act, M):
+    """K = 2^22: rows of zeros but for a few blocks, the first and the last among them, whose sums
+    are as near as those of few inputs."""
+    K, N = 1 << 22, 32
+    g = gen(M)
+    blocks = torch.randint(0, K // 32, (M, 6), generator=g)
+    blocks[:, 0] = K // 32 - 1
+    blocks[0, 1] = 0
+    x = torch.zeros(M, K // 32, 32)
+    x[torch.arange(M)[:, None], blocks] = activations(g, M, 6 * 32, True).view(M, 6, 32)
+    x = x.view(M, K).to(torch.bfloat16).cuda()
+    q = torch.randint(0, 16, (N, K), generator=g, dtype=torch.uint8)
+    s = torch.randint(118, 123, (N, K // 32), generator=g, dtype=torch.uint8)
+    w = w4.mx_pack_weights(ref.pack4(q).cuda(), s.cuda())
+    y = w4.mx_linear(x, w, act=act)
+    rows = w4.mx_grouped_linear(x, w, torch.tensor([0, M], dtype=torch.int32).cuda(), act=act)
+    for m in range(M):
+        at = (torch.unique(blocks[m])[:, None] * 32 + torch.arange(32)).reshape(-1)
+        xv = ref.rounded(x[m:m + 1, at.cuda()].contiguous(), act, "floor")
+        wv = ref.values(q[:, at].contiguous().cuda(), s[:, torch.unique(blocks[m])].contiguous().cuda(), "fp4")
+        e, _ = ref.slack(xv, wv, act)
+        for got in (y, rows):
+            check(got[m:m + 1], xv @ wv.t().contiguous(), e, f"row {m}")

@@ -300,3 +300,31 @@ def test_packing_past_2_to_32_pieces(w4):  # noqa: F811
         assert torch.equal(back.scales[at * some:(at + 1) * some], part_s), at
     del w, back
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("act", FMTS)
+def test_outputs_past_2_to_32_bytes(w4, act):  # noqa: F811
+    """2^20 rows of 4112 outputs, linear and by expert with rows read by index."""
+    M, N, K, E = 1 << 20, 4112, 96, 2
+    x = activations(gen(12), 4096, K, True).to(torch.bfloat16).cuda()
+    q, s = weight(gen(13), E * N, K)
+    w = pack(w4, q, s, n_experts=E)
+    xv, wv = ref.rounded(x, act, "floor"), ref.values(q.cuda(), s.cuda(), "fp4")
+    cut = M // 2 + 1000
+    offsets = torch.tensor([0, cut, M], dtype=torch.int32).cuda()
+    rows = torch.arange(M, dtype=torch.int32).cuda() % 4096
+    one = w4.MxWeight(pack(w4, q[:N], s[:N]).buf, 1, N, K)
+    for whole in (True, False):
+        y = w4.mx_linear(x.repeat(M // 4096, 1), one, act=act) if whole else \
+            w4.mx_grouped_linear(x, w, offsets, rows=rows, act=act)
+        for at in (0, cut - 300, (1 << 32) // (2 * N) - 100, M - 300):
+            for lo, hi in ((at, min(at + 300, max(cut, at))), (max(at, cut), at + 300)):
+                if whole:
+                    lo, hi = at, at + 300
+                if lo >= hi:
+                    continue
+                we = wv[:N] if whole or lo < cut else wv[N:]
+                part = xv[rows[lo:hi].long()]
+                e, _ = ref.slack(part, we, act)
+                check(y[lo:hi], part @ we.t().contiguous(), e, f"rows from {lo}")
+        del y
