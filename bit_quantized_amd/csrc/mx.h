@@ -198,7 +198,6 @@ struct MxArgs {
   int nb;                 // 16-channel blocks of a group
   int strips;             // column strips of a tile
   int bm;                 // rows of a tile
-  int ksplit;
   uint16_t* y;            // [P][16 nb], gated: [P][8 nb]
   float* parts;           // [ksplit][P][16 nb]
 };

@@ -309,7 +309,6 @@ hipError_t run(const Call& c, const MxPlan& p, hipStream_t st) {
   a.lds = (int)mx_row_scale_bytes(c.K);
   a.nb = (int)(c.N / 16);
   a.bm = p.bm;
-  a.ksplit = p.ksplit;
   a.y = c.y;
   if (p.path == kMxToken) {
     a.x = c.x;

@@ -326,10 +326,17 @@ hipError_t launch_one(const MxArgs& a, const MxPlan& p, unsigned blocks, hipStre
   return hipGetLastError();
 }
 
+// What plans ask for: the gated activation of groups, whose tiles have 16 rows
+// at most; of raw rows one block a workgroup where nothing is gated.
 template <int FMT, int MT, int RAW>
 hipError_t launch_cols(const MxArgs& a, const MxPlan& p, bool gated, unsigned blocks, hipStream_t st) {
-  if (gated) return launch_one<FMT, MT, RAW, 2, true>(a, p, blocks, st);
-  if (p.bn == 32) return launch_one<FMT, MT, RAW, 2, false>(a, p, blocks, st);
+  if constexpr (MT == 1) {
+    if (gated) return launch_one<FMT, MT, RAW, 2, true>(a, p, blocks, st);
+  }
+  if constexpr (!RAW) {
+    if (p.bn == 32 && !gated) return launch_one<FMT, MT, RAW, 2, false>(a, p, blocks, st);
+  }
+  if (gated || p.bn != 16) return hipErrorInvalidValue;
   return launch_one<FMT, MT, RAW, 1, false>(a, p, blocks, st);
 }
 
