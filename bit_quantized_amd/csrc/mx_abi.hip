@@ -245,7 +245,8 @@ int check_product(int64_t M, int64_t N, int64_t K, int32_t act) {
   if (int rc = check_rows(M)) return rc;
   if (int rc = check_weight(N, K)) return rc;
   if (int rc = check_format(act)) return rc;
-  if (N * mx_code_stride(K) * kMxStep > kMostOffset)
+  // (with the odd stride at most 1.5 2^31 bytes of codes)
+  if (N * mx_steps(K) * kMxStep > kMostOffset)
     return fail(W4A8_ERR_UNSUPPORTED_SHAPE, "the codes are addressed with 32-bit offsets (N=%lld K=%lld)",
                 (long long)N, (long long)K);
   return W4A8_OK;

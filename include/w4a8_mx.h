@@ -113,7 +113,10 @@ typedef struct {
  *           bytes; contents on entry are ignored.  The size for M rows serves
  *           every smaller number of them
  * Requirements: 1 <= M <= 2^24, N % 16 == 0, K % 32 == 0, 32 <= K <= 2^22,
- * N times K rounded up to 128 below 2^32.
+ * N times K rounded up to 128 below 2^32, and fewer than 2^32 threads in the
+ * launch that the plan names: ceil(M / tile_rows) times ceil(N / tile_cols),
+ * of W4A8_MX_TILE 512 each, of the others 64 to 1024.  Sizes past either are
+ * W4A8_ERR_UNSUPPORTED_SHAPE, from the plan query as from the call.
  */
 int w4a8_mx_linear_plan(int64_t M, int64_t N, int64_t K, int32_t act, w4a8_mx_plan_t* plan);
 size_t w4a8_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t act);
@@ -141,9 +144,10 @@ int w4a8_mx_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, co
  *            N, K, act) bytes; contents on entry are ignored
  * A row's result does not depend on the other rows except through the kernel
  * that the sizes select.  The call never synchronises and can be captured.
- * Requirements: as w4a8_mx_linear, 1 <= M, P <= 2^24, 1 <= E <= 1024, gated:
- * N % 32 == 0; with rows the quantised rows of x (inputs rounded up
- * to 256, and 128 bytes) below 2^31 bytes.
+ * Requirements: as w4a8_mx_linear, 1 <= M, P <= 2^24, 1 <= E <= 1024, N E <=
+ * 2^31, gated: N % 32 == 0; with rows the quantised rows of x (inputs rounded
+ * up to 256, and 128 bytes) below 2^31 - 16 bytes.  The launch has
+ * ceil(P / tile_rows) + min(E, P) times ceil(N / tile_cols) tiles.
  */
 int w4a8_mx_grouped_linear_plan(int64_t M, int64_t P, int32_t E, int64_t N, int64_t K, int32_t act,
                                 w4a8_mx_plan_t* plan);
