@@ -792,6 +792,17 @@ def _mx(table, name: str, what: str) -> int:
     return table[name]
 
 
+def _mx_call(device: int, call, *args):
+    """call(*args, stream) on GPU `device` and its current stream.  The library
+    works on the current GPU, and the default stream has one handle on all of
+    them: tensors of another GPU would be launched on the current one."""
+    if torch._C._cuda_getDevice() == device:
+        _check(call(*args, ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device))))
+        return
+    with torch.cuda.device(device):
+        _check(call(*args, ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device))))
+
+
 @dataclass
 class MxTensor:
     """Rows in a microscaled format: codes uint8 [M][K / 2] ("fp4", the even
@@ -825,7 +836,8 @@ def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
     last binade and may be clipped; "ceil": nothing is clipped."""
     lib = load()
     fmt, ru = _mx(MX_FORMATS, format, "element format"), _mx(MX_RULES, rule, "scale rule")
-    _need_on(x.get_device(), x, codes, scales)
+    device = x.get_device()
+    _need_on(device, x, codes, scales)
     M, K = x.shape
     dt = _act_dtype(x)
     width = K // 2 if fmt == 0 else K
@@ -837,8 +849,7 @@ def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
         scales = x.new_empty((M, K // MX_BLOCK), dtype=torch.uint8)
     elif scales.dtype != torch.uint8 or scales.shape != (M, K // MX_BLOCK):
         raise TypeError(f"scales must be uint8 [{M}][{K // MX_BLOCK}]")
-    _check(lib.w4a8_mx_quant(x.data_ptr(), dt, M, K, fmt, ru, codes.data_ptr(), scales.data_ptr(),
-                             _stream(x.device)))
+    _mx_call(device, lib.w4a8_mx_quant, x.data_ptr(), dt, M, K, fmt, ru, codes.data_ptr(), scales.data_ptr())
     return MxTensor(codes, scales, format)
 
 
@@ -848,13 +859,14 @@ def mx_dequant(t: MxTensor, dtype: torch.dtype = torch.bfloat16,
     lib = load()
     fmt, M, K = t.check()
     codes, scales = t.codes, t.scales
-    _need_on(codes.get_device(), codes, scales, out)
+    device = codes.get_device()
+    _need_on(device, codes, scales, out)
     if out is None:
         out = codes.new_empty((M, K), dtype=dtype)
     elif out.dtype != dtype or out.shape != (M, K):
         raise TypeError(f"out must be {dtype} [{M}][{K}]")
-    _check(lib.w4a8_mx_dequant(codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(),
-                               _act_dtype(out), _stream(out.device)))
+    _mx_call(device, lib.w4a8_mx_dequant, codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(),
+             _act_dtype(out))
     return out
 
 
@@ -878,7 +890,8 @@ def mx_pack_weights(codes: torch.Tensor, scales: torch.Tensor, n_experts: int = 
     32], as mx_quant(w, "fp4") and checkpoints hold them -> packed weight."""
     lib = load()
     MxTensor(codes, scales, "fp4").check()
-    _need_on(codes.get_device(), codes, scales, out)
+    device = codes.get_device()
+    _need_on(device, codes, scales, out)
     rows, K = codes.shape[0], codes.shape[1] * 2
     if n_experts < 1 or rows % n_experts:
         raise ValueError(f"{rows} channels are not those of {n_experts} experts")
@@ -887,20 +900,21 @@ def mx_pack_weights(codes: torch.Tensor, scales: torch.Tensor, n_experts: int = 
         _check(lib.w4a8_mx_pack_weights(None, None, rows, K, None, 0, None))
     if out is None:
         out = codes.new_empty(nbytes)
-    _check(lib.w4a8_mx_pack_weights(_p(codes), _p(scales), rows, K, _p(out),
-                                    out.numel() * out.element_size(), _stream(codes.device)))
+    _mx_call(device, lib.w4a8_mx_pack_weights, _p(codes), _p(scales), rows, K, _p(out),
+             out.numel() * out.element_size())
     return MxWeight(out, n_experts, rows // n_experts, K)
 
 
 def mx_unpack_weights(w: MxWeight) -> MxTensor:
     """The inverse of mx_pack_weights."""
     lib = load()
-    _need_on(w.buf.get_device(), w.buf)
+    device = w.buf.get_device()
+    _need_on(device, w.buf)
     rows = w.n_experts * w.N
     codes = w.buf.new_empty((rows, w.K // 2), dtype=torch.uint8)
     scales = w.buf.new_empty((rows, w.K // MX_BLOCK), dtype=torch.uint8)
-    _check(lib.w4a8_mx_unpack_weights(_p(w.buf), w.buf.numel() * w.buf.element_size(), rows, w.K, _p(codes),
-                                      _p(scales), _stream(w.buf.device)))
+    _mx_call(device, lib.w4a8_mx_unpack_weights, _p(w.buf), w.buf.numel() * w.buf.element_size(), rows, w.K,
+             _p(codes), _p(scales))
     return MxTensor(codes, scales, "fp4")
 
 
@@ -921,7 +935,8 @@ def mx_linear(x: torch.Tensor, w: MxWeight, act: str = "fp4", rule: str = "floor
     4-bit microscaled weight."""
     lib = load()
     fmt, ru = _mx(MX_FORMATS, act, "element format"), _mx(MX_RULES, rule, "scale rule")
-    _need_on(x.get_device(), x, w.buf, out, workspace)
+    device = x.get_device()
+    _need_on(device, x, w.buf, out, workspace)
     M, K = x.shape
     dt = _act_dtype(x)
     N = w.n_experts * w.N
@@ -930,9 +945,8 @@ def mx_linear(x: torch.Tensor, w: MxWeight, act: str = "fp4", rule: str = "floor
     out = _out(out, x, M, N)
     if workspace is None:
         workspace = x.new_empty(max(mx_linear_workspace_bytes(M, N, K, act), 16), dtype=torch.uint8)
-    _check(lib.w4a8_mx_linear(_p(x), dt, fmt, ru, _p(w.buf), w.buf.numel() * w.buf.element_size(), M, N, K,
-                              _p(out), _p(workspace), workspace.numel() * workspace.element_size(),
-                              _stream(x.device)))
+    _mx_call(device, lib.w4a8_mx_linear, _p(x), dt, fmt, ru, _p(w.buf), w.buf.numel() * w.buf.element_size(),
+             M, N, K, _p(out), _p(workspace), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -963,7 +977,8 @@ def mx_grouped_linear(x: torch.Tensor, w: MxWeight, offsets: torch.Tensor,
     outside [offsets[0], offsets[-1]) stay as they were."""
     lib = load()
     fmt, ru = _mx(MX_FORMATS, act, "element format"), _mx(MX_RULES, rule, "scale rule")
-    _need_on(x.get_device(), x, w.buf, offsets, rows, out, workspace)
+    device = x.get_device()
+    _need_on(device, x, w.buf, offsets, rows, out, workspace)
     M, K = x.shape
     dt = _act_dtype(x)
     E, N = w.n_experts, w.N
@@ -982,10 +997,9 @@ def mx_grouped_linear(x: torch.Tensor, w: MxWeight, offsets: torch.Tensor,
     if workspace is None:
         workspace = x.new_empty(max(mx_grouped_linear_workspace_bytes(M, P, E, N, K, act), 16),
                                 dtype=torch.uint8)
-    _check(lib.w4a8_mx_grouped_linear(_p(x), dt, fmt, ru, _p(w.buf),
-                                      w.buf.numel() * w.buf.element_size(), _p(offsets), _p(rows), M, P, E,
-                                      N, K, int(gated), _p(out), _p(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(x.device)))
+    _mx_call(device, lib.w4a8_mx_grouped_linear, _p(x), dt, fmt, ru, _p(w.buf),
+             w.buf.numel() * w.buf.element_size(), _p(offsets), _p(rows), M, P, E, N, K, int(gated), _p(out),
+             _p(workspace), workspace.numel() * workspace.element_size())
     return out
 
 
