@@ -140,6 +140,8 @@ int w4a8_mx_linear(const void* x, int32_t x_dtype, int32_t act, int32_t rule, co
  *   gated    0: y[p] = bf16( sums ), [P][N].  Else the first N / 2 channels of
  *            a group are gates, the others values, and y[p] = bf16(
  *            silu(gate) * value ), [P][N / 2]
+ *            (a gate whose sum lies past float's largest value below zero is
+ *            minus infinity, and its output NaN)
  *   workspace  device scratch of w4a8_mx_grouped_linear_workspace_bytes(M, P, E,
  *            N, K, act) bytes; contents on entry are ignored
  * A row's result does not depend on the other rows except through the kernel

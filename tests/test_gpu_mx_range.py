@@ -92,3 +92,19 @@ def test_groups_near_the_ends(w4, act, gated, case):  # noqa: F811
                 v = ref.silu_mul(v)
                 err = err + v.abs() * 2.0 ** -20
             mx_strict.check(y[run], v, err, f"group {e} 2^{ex} 2^{ew}")
+
+
+@pytest.mark.parametrize("act", FMTS)
+@pytest.mark.parametrize("counts", [(2, 0, 1), (9, 4, 0, 3), (70, 3, 90)])
+def test_a_gate_past_the_smallest_value_is_nan(w4, act, counts):  # noqa: F811
+    """As the header states: the sum is minus infinity, and its sigmoid's product NaN; the gates
+    beside it are their own."""
+    E, N, K = len(counts), 64, 544
+    g = gen(sum(counts))
+    q, s = weight(g, E * N, K, 60, True)
+    q[::4] |= 8  # of every four gates (and values) one is negative
+    offsets = torch.cumsum(torch.tensor([0] + list(counts)), 0).to(torch.int32)
+    w = w4.mx_pack_weights(ref.pack4(q).cuda(), s.cuda(), n_experts=E)
+    y = w4.mx_grouped_linear(rows_of(g, sum(counts), K, 62, True), w, offsets.cuda(), gated=True, act=act).cpu()
+    low = torch.arange(N // 2) % 4 == 0
+    assert bool(torch.isnan(y[:, low]).all()) and bool((y[:, ~low] == float("inf")).all())
