@@ -42,7 +42,7 @@ inline int64_t mx_weight_bytes(int64_t N, int64_t K) {
   return mx_scales_offset(N, K) + N / 16 * mx_scale_stride(K) * kMxScaleBytes + 1024;
 }
 // Quantised rows in a workspace, in one of two layouts; in both, inputs past K
-// have code 0 and scale 0.
+// up to whole 512 have code 0 and scale 0.
 // Rows (tiles, whose loads to LDS take whole pieces of a row): codes
 // [rows][mx_row_bytes], inputs in whole 256, so that no iteration of two steps
 // leaves its row; scales [rows][mx_row_scale_bytes], byte 4 j + s of 16 for

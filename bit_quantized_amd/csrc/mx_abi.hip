@@ -82,7 +82,8 @@ int stream_waves(int64_t Q, int most) {
 // Raw rows: every workgroup quantises all of its tile's.  It saves a launch
 // (2.5 us) where there are one or two, or the rows that workgroups read again
 // are few bytes (8 rows 3584 -> 3584: 8.2 against 9.6 us; 4 rows 3584 ->
-// 18944, 34 MB: 12.3 against 11.5).
+// 18944, 34 MB: 12.3 against 11.5).  The bytes are counted at two an input: a
+// plan does not know whether the rows are float.
 constexpr int64_t kTokenLds = 48 * 1024, kTokenReads = 20 << 20;
 bool token_fits(int64_t rows, int64_t N, int64_t K, int fmt) {
   return rows <= 16 && rows * (mx_row_bytes(K, fmt) + mx_row_scale_bytes(K)) <= kTokenLds &&
@@ -104,15 +105,19 @@ MxPlan mx_plan(int64_t M, int64_t P, int E, int64_t N, int64_t K, int fmt) {
       p.path = kMxStream;
       p.ksplit = 1;
       p.bm = (int)ceil_div(M, 16) * 16;
-      p.bn = M > 16 && N / 32 >= device_cus() ? 32 : 16;  // (20 rows 3584 -> 18944: 14.4 against 16.1 us)
+      // (32 rows 4096 -> 8192 in 8 bits: 9.1 against 10.4 us; 20 rows 2048 -> 8192 in 4: 5.8, 6.0)
+      p.bn = M > 16 && N / 32 >= device_cus() ? 32 : 16;
     }
   } else {
     // By the rows of a group, evenly shared (the groups' own numbers are on
-    // the device).  64 tokens x 8 of 128 (4 rows a group) take 31 us streamed,
-    // 256 (16 rows) 47, and 37 in tiles of 64.  With 4-bit rows 64 rows a group
-    // take 46 in tiles of 64 x 128, 51 in the next; 96 rows 98, 98 (128 x 128),
-    // 90 (128 x 256) and 118 (256 x 256); 576 rows 351, 297, 254 and 292.  With
-    // 8-bit rows 192 rows take 167, 162, 163 and 175.
+    // the device), measured with 64 and 128 groups, which fill the compute
+    // units whatever the tile.  Few groups do not: 17 rows of one group 3584 ->
+    // 3584 take 10.2 us in 28 tiles, 6.4 by the linear's plan.
+    // 64 tokens x 8 of 128 (4 rows a group) take 31 us streamed, 256 (16 rows)
+    // 47, and 37 in tiles of 64.  With 4-bit rows 64 rows a group take 46 in
+    // tiles of 64 x 128, 51 in the next; 96 rows 98, 98 (128 x 128), 90 (128 x
+    // 256) and 118 (256 x 256); 576 rows 351, 297, 254 and 292.  With 8-bit
+    // rows 192 rows take 167, 162, 163 and 175.
     const double per = double(P) / E;
     p.path = kMxTile;
     if (per <= kStreamPerGroup) {

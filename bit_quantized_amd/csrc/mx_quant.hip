@@ -321,7 +321,10 @@ hipError_t launch_mx_rows(const MxQuantArgs& a, const MxRowsArgs& r, hipStream_t
   at.Q = (int)mx_supers(a.K);
   at.rows = r.rows;
   at.M = a.M;
-  // whole supers; of the other layout the stride of the scales, which the codes' lies in
+  // whole supers; of the other layout the stride of the scales.  (Where the
+  // supers are odd in number and the last one more than half full, the codes'
+  // stride ends 128 bytes behind it.  They stay unwritten, and no stage reads
+  // them.)
   at.chunks = r.interleaved ? at.Q * 64 : at.lds * 4;
   const int64_t rows = r.interleaved ? r.P : a.M;
   const int wide = (at.chunks + kThreads - 1) / kThreads;

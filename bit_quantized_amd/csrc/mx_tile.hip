@@ -114,9 +114,9 @@ struct Shape {
   // As many buffers as half of a compute unit's LDS holds (of workgroups of
   // eight wavefronts, which run alone, all of it), at most four.  Groups, whose
   // many tiles are short, take a third where that holds three buffers: 4096
-  // rows of 128 groups, 2048 inputs: 53 us in three buffers, three workgroups
-  // to a compute unit, 57 in six and two; but 33 rows 18944 -> 3584 15 in four,
-  // 16.6 in three.
+  // gated rows of 128 groups, 2048 -> 1536 in 8 bits: 57 us in three buffers,
+  // three workgroups to a compute unit, 59 in four and two; but 33 rows 18944
+  // -> 3584 15 in four, 16.6 in three.
   static constexpr int kFixed = kScaleKiB * 1024;
   static constexpr bool kThird = KIND >= kGroups && kBlocks <= 8 && 160 * 1024 / 3 - kFixed >= 3 * kStageBytes;
   static constexpr int kRoom = (kThird ? 160 * 1024 / 3 : (kWaves > 4 ? 160 : 80) * 1024) - kFixed;
@@ -358,7 +358,9 @@ mx_tile_kernel(const MxArgs a) {
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
   }
-  stage_barrier<0>();  // (the last loads, none of them a request)
+  // The last loads: the stages' ask for nothing, but the scales' are requests to
+  // the end, and the outputs take the LDS that they write to.
+  stage_barrier<0>();
 
   // ---- out: a lane has row c of each 32, and of each 32 channels the four
   // from 8 i + 4 j, i = 0..3.  Each wavefront turns 32 rows of 256 bytes (or
