@@ -792,15 +792,21 @@ def _mx(table, name: str, what: str) -> int:
     return table[name]
 
 
-def _mx_call(device: int, call, *args):
-    """call(*args, stream) on GPU `device` and its current stream.  The library
-    works on the current GPU, and the default stream has one handle on all of
-    them: tensors of another GPU would be launched on the current one."""
-    if torch._C._cuda_getDevice() == device:
-        _check(call(*args, ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device))))
-        return
-    with torch.cuda.device(device):
-        _check(call(*args, ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device))))
+_gpus = 0  # of the process, counted when the first tensor is there
+
+
+def _mx_elsewhere(device: int) -> bool:
+    """Another GPU than the tensors' is current.  The library works on the
+    current one, and the default stream has one handle on all of them, so the
+    operators make the tensors' GPU current before they call it."""
+    global _gpus
+    if not _gpus:
+        _gpus = torch.cuda.device_count()
+    return _gpus > 1 and torch._C._cuda_getDevice() != device  # (the second takes 0.2 us)
+
+
+def _mx_stream(device: int):
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device))
 
 
 @dataclass
@@ -838,6 +844,9 @@ def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
     fmt, ru = _mx(MX_FORMATS, format, "element format"), _mx(MX_RULES, rule, "scale rule")
     device = x.get_device()
     _need_on(device, x, codes, scales)
+    if _mx_elsewhere(device):
+        with torch.cuda.device(device):
+            return mx_quant(x, format, rule, codes, scales)
     M, K = x.shape
     dt = _act_dtype(x)
     width = K // 2 if fmt == 0 else K
@@ -849,7 +858,8 @@ def mx_quant(x: torch.Tensor, format: str = "fp4", rule: str = "floor",
         scales = x.new_empty((M, K // MX_BLOCK), dtype=torch.uint8)
     elif scales.dtype != torch.uint8 or scales.shape != (M, K // MX_BLOCK):
         raise TypeError(f"scales must be uint8 [{M}][{K // MX_BLOCK}]")
-    _mx_call(device, lib.w4a8_mx_quant, x.data_ptr(), dt, M, K, fmt, ru, codes.data_ptr(), scales.data_ptr())
+    _check(lib.w4a8_mx_quant(x.data_ptr(), dt, M, K, fmt, ru, codes.data_ptr(), scales.data_ptr(),
+                             _mx_stream(device)))
     return MxTensor(codes, scales, format)
 
 
@@ -861,12 +871,15 @@ def mx_dequant(t: MxTensor, dtype: torch.dtype = torch.bfloat16,
     codes, scales = t.codes, t.scales
     device = codes.get_device()
     _need_on(device, codes, scales, out)
+    if _mx_elsewhere(device):
+        with torch.cuda.device(device):
+            return mx_dequant(t, dtype, out)
     if out is None:
         out = codes.new_empty((M, K), dtype=dtype)
     elif out.dtype != dtype or out.shape != (M, K):
         raise TypeError(f"out must be {dtype} [{M}][{K}]")
-    _mx_call(device, lib.w4a8_mx_dequant, codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(),
-             _act_dtype(out))
+    _check(lib.w4a8_mx_dequant(codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(),
+                               _act_dtype(out), _mx_stream(device)))
     return out
 
 
@@ -892,6 +905,9 @@ def mx_pack_weights(codes: torch.Tensor, scales: torch.Tensor, n_experts: int = 
     MxTensor(codes, scales, "fp4").check()
     device = codes.get_device()
     _need_on(device, codes, scales, out)
+    if _mx_elsewhere(device):
+        with torch.cuda.device(device):
+            return mx_pack_weights(codes, scales, n_experts, out)
     rows, K = codes.shape[0], codes.shape[1] * 2
     if n_experts < 1 or rows % n_experts:
         raise ValueError(f"{rows} channels are not those of {n_experts} experts")
@@ -900,8 +916,8 @@ def mx_pack_weights(codes: torch.Tensor, scales: torch.Tensor, n_experts: int = 
         _check(lib.w4a8_mx_pack_weights(None, None, rows, K, None, 0, None))
     if out is None:
         out = codes.new_empty(nbytes)
-    _mx_call(device, lib.w4a8_mx_pack_weights, _p(codes), _p(scales), rows, K, _p(out),
-             out.numel() * out.element_size())
+    _check(lib.w4a8_mx_pack_weights(_p(codes), _p(scales), rows, K, _p(out),
+                                    out.numel() * out.element_size(), _mx_stream(device)))
     return MxWeight(out, n_experts, rows // n_experts, K)
 
 
@@ -910,11 +926,14 @@ def mx_unpack_weights(w: MxWeight) -> MxTensor:
     lib = load()
     device = w.buf.get_device()
     _need_on(device, w.buf)
+    if _mx_elsewhere(device):
+        with torch.cuda.device(device):
+            return mx_unpack_weights(w)
     rows = w.n_experts * w.N
     codes = w.buf.new_empty((rows, w.K // 2), dtype=torch.uint8)
     scales = w.buf.new_empty((rows, w.K // MX_BLOCK), dtype=torch.uint8)
-    _mx_call(device, lib.w4a8_mx_unpack_weights, _p(w.buf), w.buf.numel() * w.buf.element_size(), rows, w.K,
-             _p(codes), _p(scales))
+    _check(lib.w4a8_mx_unpack_weights(_p(w.buf), w.buf.numel() * w.buf.element_size(), rows, w.K, _p(codes),
+                                      _p(scales), _mx_stream(device)))
     return MxTensor(codes, scales, "fp4")
 
 
@@ -937,6 +956,9 @@ def mx_linear(x: torch.Tensor, w: MxWeight, act: str = "fp4", rule: str = "floor
     fmt, ru = _mx(MX_FORMATS, act, "element format"), _mx(MX_RULES, rule, "scale rule")
     device = x.get_device()
     _need_on(device, x, w.buf, out, workspace)
+    if _mx_elsewhere(device):
+        with torch.cuda.device(device):
+            return mx_linear(x, w, act, rule, out, workspace)
     M, K = x.shape
     dt = _act_dtype(x)
     N = w.n_experts * w.N
@@ -945,8 +967,9 @@ def mx_linear(x: torch.Tensor, w: MxWeight, act: str = "fp4", rule: str = "floor
     out = _out(out, x, M, N)
     if workspace is None:
         workspace = x.new_empty(max(mx_linear_workspace_bytes(M, N, K, act), 16), dtype=torch.uint8)
-    _mx_call(device, lib.w4a8_mx_linear, _p(x), dt, fmt, ru, _p(w.buf), w.buf.numel() * w.buf.element_size(),
-             M, N, K, _p(out), _p(workspace), workspace.numel() * workspace.element_size())
+    _check(lib.w4a8_mx_linear(_p(x), dt, fmt, ru, _p(w.buf), w.buf.numel() * w.buf.element_size(), M, N, K,
+                              _p(out), _p(workspace), workspace.numel() * workspace.element_size(),
+                              _mx_stream(device)))
     return out
 
 
@@ -979,6 +1002,9 @@ def mx_grouped_linear(x: torch.Tensor, w: MxWeight, offsets: torch.Tensor,
     fmt, ru = _mx(MX_FORMATS, act, "element format"), _mx(MX_RULES, rule, "scale rule")
     device = x.get_device()
     _need_on(device, x, w.buf, offsets, rows, out, workspace)
+    if _mx_elsewhere(device):
+        with torch.cuda.device(device):
+            return mx_grouped_linear(x, w, offsets, rows, gated, act, rule, out, workspace)
     M, K = x.shape
     dt = _act_dtype(x)
     E, N = w.n_experts, w.N
@@ -997,9 +1023,10 @@ def mx_grouped_linear(x: torch.Tensor, w: MxWeight, offsets: torch.Tensor,
     if workspace is None:
         workspace = x.new_empty(max(mx_grouped_linear_workspace_bytes(M, P, E, N, K, act), 16),
                                 dtype=torch.uint8)
-    _mx_call(device, lib.w4a8_mx_grouped_linear, _p(x), dt, fmt, ru, _p(w.buf),
-             w.buf.numel() * w.buf.element_size(), _p(offsets), _p(rows), M, P, E, N, K, int(gated), _p(out),
-             _p(workspace), workspace.numel() * workspace.element_size())
+    _check(lib.w4a8_mx_grouped_linear(_p(x), dt, fmt, ru, _p(w.buf),
+                                      w.buf.numel() * w.buf.element_size(), _p(offsets), _p(rows), M, P, E,
+                                      N, K, int(gated), _p(out), _p(workspace),
+                                      workspace.numel() * workspace.element_size(), _mx_stream(device)))
     return out
 
 

@@ -50,6 +50,8 @@ def calls(request, monkeypatch):
                                  **{f"w4a8_mx_{n}": getattr(real, f"w4a8_mx_{n}") for n in
                                     ("weight_bytes", "linear_workspace_bytes", "grouped_linear_workspace_bytes")})
     monkeypatch.setattr(_lib, "load", lambda: fake)
+    monkeypatch.setattr(_lib, "_gpus", 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
